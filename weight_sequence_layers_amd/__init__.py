@@ -65,6 +65,20 @@ class ttt_block_weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in BLOCK_WEIGHTS]
 
 
+class ttt_rope_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "q_heads", "k_heads", "head_dim", "rot_dim", "axes", "pairing", "norm", "act")
+    ] + [("eps", ctypes.c_float)]
+
+
+class ttt_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")
+    ] + [("page_stride", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "pages", "page_size", "kv_heads", "head_dim", "dtype", "reserved")]
+
+
+HEAD_NORM = {"none": 0, "rms": 1}
+PAIRING = {"halves": 0, "pairs": 1}
 WINDOW = {"sliding": 0, "block": 1}
 LINEAR_EPI = {"plain": 0, "residual": 1, "gelu": 2}
 ATTN_HEAD_DIM = 128
@@ -81,6 +95,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         cfgp, vp, i64 = ctypes.POINTER(ttt_config), ctypes.c_void_p, ctypes.c_int64
         i32 = ctypes.c_int32
+        ropep, cachep = ctypes.POINTER(ttt_rope_config), ctypes.POINTER(ttt_kv_cache)
         sig = {
             "ttt_validate_config": [cfgp],
             "ttt_state_numel": [cfgp, ctypes.POINTER(i64)],
@@ -103,6 +118,21 @@ def lib() -> ctypes.CDLL:
                                ctypes.POINTER(ttt_block_weights), vp, vp, ctypes.POINTER(vp)],
             "ttt_block_forward": [vp, vp, vp, i64, vp],
             "ttt_block_destroy": [vp],
+            "ttt_validate_rope_config": [ropep],
+            "ttt_qk_norm_rope": [ropep, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64,
+                                 vp],
+            "ttt_qk_norm_rope_backward_work": [ropep, i64, ctypes.POINTER(i64)],
+            "ttt_qk_norm_rope_backward": [ropep, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp,
+                                          i64, vp, i64, vp, i64, vp, vp, vp, i64, i64, vp],
+            "ttt_qk_norm_rope_append": [ropep, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, cachep,
+                                        vp, vp, i64, i64, vp],
+            "ttt_paged_attention_work": [cachep, i32, i32, i32, i32, ctypes.POINTER(i64)],
+            "ttt_paged_attention": [vp, i64, cachep, vp, vp, vp, i64, vp, i32, i32, i32, i32,
+                                    ctypes.c_float, vp, i64, vp],
+            "ttt_window_attention_lse": [vp, vp, vp, i64, vp, i64, vp, i32, i32, i64, i32, i32,
+                                         vp],
+            "ttt_window_attention_backward": [vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, vp,
+                                              i64, vp, i32, i32, i64, i32, i32, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -406,3 +436,195 @@ def ttt_block_ttt_state(blk: Block) -> State:
 
 def ttt_block_destroy(blk: Block) -> None:
     blk.destroy()
+
+
+# ------------------------------------------- attention around the block (ttt_attention.h)
+def _arg(t, name: str, dtype, n: int, dense: bool = True) -> Optional[int]:
+    """The pointer of a device tensor argument, after the checks that the library cannot make:
+    a tensor of the current device, of its dtype, with at least n elements (dense: contiguous).
+    None passes as NULL."""
+    if t is None:
+        return None
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise TTTError(4, f"{name} is on {t.device}, not on the current HIP device")
+    if t.dtype != dtype:
+        raise TTTError(3, f"{name} is {t.dtype}, not {dtype}")
+    if t.numel() < n:
+        raise TTTError(2, f"{name} has {t.numel()} elements, {n} needed")
+    if dense and not t.is_contiguous():
+        raise TTTError(2, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _work(t):
+    """Pointer and bytes of a workspace tensor of any dtype (None: none)."""
+    return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0), t.numel() * t.element_size())
+
+
+def _act_dtype(cfg):
+    import torch
+    return torch.bfloat16 if cfg.act == 1 else torch.float32
+
+
+def make_rope_config(*, q_heads: int, k_heads: int, head_dim: int, rot_dim: Optional[int] = None,
+                     axes: int = 1, pairing="halves", norm="rms", act="bf16",
+                     eps: float = 1e-6) -> ttt_rope_config:
+    """ttt_rope_config; rot_dim None rotates whole heads."""
+    c = ttt_rope_config()
+    c.q_heads, c.k_heads, c.head_dim = int(q_heads), int(k_heads), int(head_dim)
+    c.rot_dim = int(head_dim if rot_dim is None else rot_dim)
+    c.axes = int(axes)
+    c.pairing = PAIRING[pairing] if isinstance(pairing, str) else int(pairing)
+    c.norm = HEAD_NORM[norm] if isinstance(norm, str) else int(norm)
+    c.act = ACT[act] if isinstance(act, str) else int(act)
+    c.eps = float(eps)
+    return c
+
+
+def ttt_validate_rope_config(cfg: ttt_rope_config) -> None:
+    _check(lib().ttt_validate_rope_config(ctypes.byref(cfg)))
+
+
+def _rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens):
+    import torch
+    dt, half = _act_dtype(cfg), cfg.rot_dim // 2
+    return (_arg(q_weight, "q_weight", dt, cfg.head_dim), _arg(k_weight, "k_weight", dt, cfg.head_dim),
+            _arg(freq, "freq", torch.float32, cfg.axes * half),
+            _arg(pos, "pos", torch.int32, cfg.axes * tokens if half else 0))
+
+
+def ttt_qk_norm_rope(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight, k_weight, freq,
+                     pos, q_out, ld_qo: int, k_out, ld_ko: int, tokens: int,
+                     stream=None) -> None:
+    """Per-head norm and position rotation of queries and keys: element (t, h, e) of q at
+    t ld_q + h head_dim + e (k, q_out and k_out with theirs); freq fp32 [axes, rot_dim / 2],
+    pos int32 [axes, tokens] (see include/ttt_attention.h)."""
+    dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
+    _check(lib().ttt_qk_norm_rope(
+        ctypes.byref(cfg), _arg(q, "q", dt, nq, False), ld_q, _arg(k, "k", dt, nk, False), ld_k,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens),
+        _arg(q_out, "q_out", dt, nq, False), ld_qo, _arg(k_out, "k_out", dt, nk, False), ld_ko, tokens,
+        _stream(stream)))
+
+
+def ttt_qk_norm_rope_backward_work(cfg: ttt_rope_config, tokens: int) -> int:
+    """Bytes of the workspace that ttt_qk_norm_rope_backward takes."""
+    n = ctypes.c_int64()
+    _check(lib().ttt_qk_norm_rope_backward_work(ctypes.byref(cfg), tokens, ctypes.byref(n)))
+    return n.value
+
+
+def ttt_qk_norm_rope_backward(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight, k_weight,
+                              freq, pos, dq_out, ld_dqo: int, dk_out, ld_dko: int, dq, ld_dq: int,
+                              dk, ld_dk: int, dq_weight, dk_weight, work, tokens: int,
+                              stream=None) -> None:
+    """Backward of ttt_qk_norm_rope: dq, dk (activation dtype) and dq_weight, dk_weight (fp32
+    [head_dim], or None); work: device tensor of at least ttt_qk_norm_rope_backward_work bytes
+    (see include/ttt_attention.h)."""
+    import torch
+    dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
+    f32 = torch.float32
+    _check(lib().ttt_qk_norm_rope_backward(
+        ctypes.byref(cfg), _arg(q, "q", dt, nq, False), ld_q, _arg(k, "k", dt, nk, False), ld_k,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens),
+        _arg(dq_out, "dq_out", dt, nq, False), ld_dqo, _arg(dk_out, "dk_out", dt, nk, False), ld_dko,
+        _arg(dq, "dq", dt, nq, False), ld_dq, _arg(dk, "dk", dt, nk, False), ld_dk,
+        _arg(dq_weight, "dq_weight", f32, cfg.head_dim), _arg(dk_weight, "dk_weight", f32, cfg.head_dim),
+        *_work(work), tokens, _stream(stream)))
+
+
+def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
+    """ttt_kv_cache over k and v, device tensors [pages, kv_heads, page_size, head_dim] of bf16
+    or float8_e4m3fn whose pages are contiguous and equally far apart (two tensors, or the
+    halves of one [pages, 2, ...]); the scales are fp32 [kv_heads] or None. The tensors stay
+    alive with the struct."""
+    import torch
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        raise TTTError(2, "k and v: two tensors [pages, kv_heads, page_size, head_dim] of one "
+                          "dtype and layout")
+    pages, heads, size, dim = k.shape
+    if not k[0].is_contiguous():
+        raise TTTError(2, "a page must be contiguous")
+    dtypes = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
+    if k.dtype not in dtypes:
+        raise TTTError(3, f"cache of {k.dtype}: bfloat16 or float8_e4m3fn")
+    c = ttt_kv_cache()
+    c.k, c.v = _arg(k, "k", k.dtype, 0, False), _arg(v, "v", v.dtype, 0, False)
+    c.k_scale = _arg(k_scale, "k_scale", torch.float32, heads)
+    c.v_scale = _arg(v_scale, "v_scale", torch.float32, heads)
+    c.page_stride = k.stride(0) if pages > 1 else heads * size * dim
+    c.pages, c.page_size, c.kv_heads, c.head_dim = pages, size, heads, dim
+    c.dtype, c.reserved = dtypes[k.dtype], 0
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def ttt_qk_norm_rope_append(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, v, ld_v: int,
+                            q_weight, k_weight, freq, pos, cache: ttt_kv_cache, slot, q_out,
+                            ld_qo: int, tokens: int, stream=None) -> None:
+    """ttt_qk_norm_rope of new tokens, keys and values going to the cache: slot int64 [tokens],
+    page * page_size + place, or negative for a token that is not stored
+    (see include/ttt_attention.h)."""
+    import torch
+    dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
+    _check(lib().ttt_qk_norm_rope_append(
+        ctypes.byref(cfg), _arg(q, "q", dt, nq, False), ld_q, _arg(k, "k", dt, nk, False), ld_k,
+        _arg(v, "v", dt, nk, False), ld_v, *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens),
+        ctypes.byref(cache), _arg(slot, "slot", torch.int64, tokens), _arg(q_out, "q_out", dt, nq, False),
+        ld_qo, tokens, _stream(stream)))
+
+
+def ttt_paged_attention_work(cache: ttt_kv_cache, seqs: int, heads: int, max_pages: int,
+                             window: int) -> int:
+    """Bytes of the workspace that ttt_paged_attention takes."""
+    n = ctypes.c_int64()
+    _check(lib().ttt_paged_attention_work(ctypes.byref(cache), seqs, heads, max_pages, window,
+                                          ctypes.byref(n)))
+    return n.value
+
+
+def ttt_paged_attention(q, ld_q: int, cache: ttt_kv_cache, table, lens, out, ld_out: int, lse,
+                        seqs: int, heads: int, max_pages: int, window: int, scale: float, work,
+                        stream=None) -> None:
+    """Attention of one new token per sequence over its cached tokens: table int32
+    [seqs, max_pages], lens int32 [seqs]; window 0: all of them; scale 0: 1 / sqrt(head_dim);
+    lse fp32 [seqs, heads] or None (see include/ttt_attention.h)."""
+    import torch
+    bf, n = torch.bfloat16, seqs * heads * cache.head_dim
+    _check(lib().ttt_paged_attention(
+        _arg(q, "q", bf, n, False), ld_q, ctypes.byref(cache),
+        _arg(table, "table", torch.int32, seqs * max_pages), _arg(lens, "lens", torch.int32, seqs),
+        _arg(out, "out", bf, n, False), ld_out, _arg(lse, "lse", torch.float32, seqs * heads), seqs,
+        heads, max_pages, window, scale, *_work(work), _stream(stream)))
+
+
+def ttt_window_attention_lse(q, k, v, ld: int, out, ld_out: int, lse, batch: int, heads: int,
+                             seq_len: int, window: int, mode="sliding", stream=None) -> None:
+    """ttt_window_attention that also stores lse, fp32 [batch, heads, seq_len], for the backward
+    (see include/ttt_attention.h)."""
+    import torch
+    m = WINDOW[mode] if isinstance(mode, str) else int(mode)
+    bf, rows = torch.bfloat16, batch * heads * seq_len
+    n = rows * ATTN_HEAD_DIM
+    _check(lib().ttt_window_attention_lse(
+        _arg(q, "q", bf, n, False), _arg(k, "k", bf, n, False), _arg(v, "v", bf, n, False), ld,
+        _arg(out, "out", bf, n, False), ld_out, _arg(lse, "lse", torch.float32, rows), batch, heads,
+        seq_len, window, m, _stream(stream)))
+
+
+def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout, ld_dout: int, dq,
+                                  dk, dv, ld_d: int, work, batch: int, heads: int, seq_len: int,
+                                  window: int, mode="sliding", stream=None) -> None:
+    """Backward of ttt_window_attention: dq, dk, dv with row stride ld_d; work fp32
+    [batch, heads, seq_len] (see include/ttt_attention.h)."""
+    import torch
+    m = WINDOW[mode] if isinstance(mode, str) else int(mode)
+    bf, f32, rows = torch.bfloat16, torch.float32, batch * heads * seq_len
+    n = rows * ATTN_HEAD_DIM
+    _check(lib().ttt_window_attention_backward(
+        _arg(q, "q", bf, n, False), _arg(k, "k", bf, n, False), _arg(v, "v", bf, n, False), ld,
+        _arg(out, "out", bf, n, False), ld_out, _arg(lse, "lse", f32, rows),
+        _arg(dout, "dout", bf, n, False), ld_dout, _arg(dq, "dq", bf, n, False),
+        _arg(dk, "dk", bf, n, False), _arg(dv, "dv", bf, n, False), ld_d, _arg(work, "work", f32, rows),
+        batch, heads, seq_len, window, m, _stream(stream)))

@@ -7,47 +7,18 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <new>
 
 #include "ttt_block_internal.h"
+#include "ttt_host.h"
 
 using namespace ttt;
 
 namespace {
-
-ttt_status failf(ttt_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return report(st, buf);
-}
-
-#define BLK_HIP(expr)                                                                   \
-  do {                                                                                  \
-    hipError_t e_ = (expr);                                                             \
-    if (e_ != hipSuccess)                                                               \
-      return failf(TTT_E_HIP, "%s failed: %s (%s:%d)", #expr, hipGetErrorString(e_),    \
-                   __FILE__, __LINE__);                                                 \
-  } while (0)
-
-#define BLK_TRY(expr)                  \
-  do {                                 \
-    ttt_status s_ = (expr);            \
-    if (s_ != TTT_OK) return s_;       \
-  } while (0)
-
-ttt_status need(const void* p, const char* name) {
-  if (!p) return failf(TTT_E_NULL, "%s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) % 16)
-    return failf(TTT_E_ALIGN, "%s is not 16-byte aligned", name);
-  return TTT_OK;
-}
-
 constexpr int64_t INT31 = (int64_t)1 << 31;
+}
+
+namespace ttt {
 
 ttt_status check_attention(int64_t ld, int64_t ld_out, int32_t batch, int32_t heads,
                            int64_t T, int32_t window, int32_t mode) {
@@ -75,6 +46,7 @@ AttnArgs attention_args(const void* q, const void* k, const void* v, int64_t ld,
   a.k = static_cast<const u16*>(k);
   a.v = static_cast<const u16*>(v);
   a.out = static_cast<u16*>(out);
+  a.lse = nullptr;
   a.ld = ld;
   a.ldo = ld_out;
   a.T = (int32_t)T;
@@ -86,6 +58,10 @@ AttnArgs attention_args(const void* q, const void* k, const void* v, int64_t ld,
   a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)ATT_D));
   return a;
 }
+
+}  // namespace ttt
+
+namespace {
 
 ttt_status check_linear(int64_t rows, int32_t K, int32_t N, int32_t epi) {
   if (rows < 0) return failf(TTT_E_SHAPE, "rows %lld < 0", (long long)rows);
@@ -121,11 +97,6 @@ LinearArgs linear_args(const void* x, const void* w, const void* resid, void* y,
   // of the block at width 1024 (in 1024 or 4096 features, out 1024 to 4096)
   a.group_m = std::min<int32_t>(a.tiles_m, 8);
   return a;
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const char *pa = static_cast<const char*>(a), *pb = static_cast<const char*>(b);
-  return pa < pb + nb && pb < pa + na;
 }
 
 }  // namespace

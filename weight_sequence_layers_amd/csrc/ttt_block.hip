@@ -47,6 +47,10 @@ __device__ __forceinline__ bf16x8 read_vt_frag(const char* tile, int dim_base, i
   return __builtin_bit_cast(bf16x8, v);
 }
 
+//
+// LSE: also stores each row's log-sum-exp for the backward, from a second sum of the
+// probabilities before they are rounded (the rounded ones would put it 2^-9 off).
+template <bool LSE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void k_window_attention(AttnArgs a) {
   constexpr int NT = 256, QB = ATT_Q;
@@ -134,7 +138,7 @@ void k_window_attention(AttnArgs a) {
   f32x16 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = f32x16{};
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY, l = 0.f, lx = 0.f;
 
   if (nsteps > 0) issue(st0, lo);
   __builtin_amdgcn_s_waitcnt(0);
@@ -178,6 +182,7 @@ void k_window_attention(AttnArgs a) {
     if (__any(mnew != m)) {   // wave-uniform: some running maximum moved
       const float alpha = __builtin_amdgcn_exp2f(m - mref);
       l *= alpha;
+      if (LSE) lx *= alpha;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -191,10 +196,11 @@ void k_window_attention(AttnArgs a) {
         bf16x8 pf;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const __bf16 p = static_cast<__bf16>(
-              __builtin_amdgcn_exp2f(fmaf(sc[kt][8 * sp + e], a.scale2, -mref)));
+          const float x = __builtin_amdgcn_exp2f(fmaf(sc[kt][8 * sp + e], a.scale2, -mref));
+          const __bf16 p = static_cast<__bf16>(x);
           pf[e] = p;
           l += static_cast<float>(p);
+          if (LSE) lx += x;
         }
 #pragma unroll
         for (int d = 0; d < 4; ++d)
@@ -207,6 +213,10 @@ void k_window_attention(AttnArgs a) {
 
   // element v of o[d]: dim 32 d + 8 (v / 4) + 4 (lane / 32) + v % 4 of query t
   const float lt = l + __shfl_xor(l, 32);
+  if (LSE) {
+    const float lxt = lx + __shfl_xor(lx, 32);
+    if (t < T && hl == 0) a.lse[(int64_t)bh * T + t] = (m + log2f(lxt)) * 0.69314718055994531f;
+  }
   if (t < T) {
     const float inv = 1.f / lt;
     u16* orow = a.out + (row0 + t) * a.ldo + (int64_t)h * ATT_D + 4 * hl;
@@ -475,7 +485,8 @@ __global__ __launch_bounds__(256) void k_blk_merge(HeadMergeArgs a) {
 
 hipError_t launch_window_attention(const AttnArgs& a, hipStream_t st) {
   if (a.total == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_window_attention, dim3(a.total), dim3(256), 0, st, a);
+  if (a.lse) hipLaunchKernelGGL(k_window_attention<true>, dim3(a.total), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(k_window_attention<false>, dim3(a.total), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

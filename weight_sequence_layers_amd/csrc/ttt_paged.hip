@@ -1,0 +1,340 @@
+// Attention of one new token per sequence over a paged key-value cache
+// (include/ttt_attention.h).
+//
+// Mathematics.  o = sum_j p_j v_j / sum_j p_j with p_j = 2^(s_j c - m), s_j = q . k_j, c =
+// scale log2(e) and m the running maximum: parts of the tokens are summed apart, each with its
+// own m, and joined as sum_i 2^(m_i - m) o_i.
+//
+// Every cached byte is read once: the memory bounds it.  A workgroup takes one key head of one
+// sequence, the query heads that share it (up to 16, the columns of a 16 x 16 x 32 MFMA; with
+// fewer the spare columns cost nothing that counts) and one part of the tokens; its four waves
+// take 32 tokens in turn.  Per step a wave computes S^T = K Q^T with K's fragments straight
+// from memory (a lane's 16 bytes of a key row are its fragment; which dims a fragment's k index
+// means is free as long as Q's agree), so each lane holds 8 tokens of one query head and P^T is
+// already laid out as the second product's B operand; V goes through the wave's own LDS tile,
+// read transposed.  The next step's rows are loaded into registers while this one is computed.
+#include "ttt_attention_internal.h"
+
+namespace ttt {
+namespace {
+
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// what rows outside the sequence or the cache read: lanes of a step that has fewer tokens
+__device__ const uint4 k_zero_row[1] = {{0u, 0u, 0u, 0u}};
+
+// 8 e4m3 numbers as bf16 (exact: e4m3's 4 significant bits and its range lie within bf16's)
+__device__ __forceinline__ uint4 bf16_of_e4m3(uint32_t lo, uint32_t hi) {
+  return make_uint4(
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true)));
+}
+
+// place of 16-byte chunk c of row r of a V tile (rows of D bf16): the rows that one transposing
+// read touches land on distinct banks
+template <int D>
+__device__ __forceinline__ int vt_chunk(int r, int c) {
+  if (D == 64) return c ^ (((r >> 1) & 3) << 1);
+  return c ^ ((r & 7) << 1);
+}
+
+// The wave's LDS accesses before come before those after (a wave's own are in order in the
+// hardware: this holds the compiler to it).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int D, bool E4>
+struct PagedShape {
+  static constexpr int RB = D * (E4 ? 1 : 2);         // bytes of a cached row
+  static constexpr int KL = PG_STEP * RB / 16 / 64;   // 16-byte loads per lane of 32 rows
+  static constexpr int LR = RB / 16;                  // lanes of a V row
+  static constexpr int RPI = 64 / LR;                 // V rows per load
+  static constexpr int KS = D / 32;                   // MFMA steps along D
+  static constexpr int VT = PG_STEP * D * 2;          // bytes of a wave's V tile
+};
+
+template <int D, bool E4>
+__global__ __launch_bounds__(PG_NT) void k_paged(PagedArgs a) {
+  using S = PagedShape<D, E4>;
+  // the V tiles, and after the loop the waves' sums
+  constexpr int JOIN = PG_WAVES * PG_HEADS * D * 4;
+  constexpr int LDS = PG_WAVES * S::VT > JOIN ? PG_WAVES * S::VT : JOIN;
+  __shared__ __attribute__((aligned(1024))) char lds[LDS];
+  __shared__ float wm[PG_WAVES][PG_HEADS], wl[PG_WAVES][PG_HEADS];
+
+  int id = blockIdx.x;
+  const int sp = id % a.splits;
+  id /= a.splits;
+  const int ht = id % a.htiles;
+  id /= a.htiles;
+  const int kh = id % a.kv_heads, seq = id / a.kv_heads;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int h0 = ht * PG_HEADS;                       // first query head of the group
+  const int nh = min(PG_HEADS, a.group - h0);
+
+  int lo, hi;
+  paged_span(a.lens[seq], a.max_pages, a.page_size, a.window, lo, hi);
+  const int part = paged_part(hi - lo, a.splits);
+  const int b0 = lo + min(hi - lo, sp * part), b1 = min(hi, b0 + part);
+  if (b0 >= b1 && sp > 0) return;   // part 0 stays: it writes an empty sequence's row
+  const bool whole = part >= hi - lo;                 // this part is all of it
+
+  // Q fragments: column n, k index 8 g + i of step s
+  bf16x8 qf[S::KS];
+  {
+    const u16* qr = a.q + (int64_t)seq * a.ldq + ((int64_t)kh * a.group + h0 + n) * D;
+#pragma unroll
+    for (int s = 0; s < S::KS; ++s) {
+      const int d = E4 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+      if (n < nh) qf[s] = *reinterpret_cast<const bf16x8*>(qr + d);
+      else qf[s] = bf16x8{};
+    }
+  }
+  const float ksc = E4 && a.ks ? a.ks[kh] : 1.f, vsc = E4 && a.vs ? a.vs[kh] : 1.f;
+  const float c2 = a.scale * ksc * 1.44269504088896341f;
+
+  const int32_t* tab = a.table + (int64_t)seq * a.max_pages;
+  const char* zero = reinterpret_cast<const char*>(k_zero_row);
+  // lane l < 32 of a step at token k0: the byte offset of row k0 + l, or -1
+  auto row_of = [&](int k0) __attribute__((always_inline)) {
+    const int key = k0 + (lane & 31);
+    int64_t off = -1;
+    if (key < b1) {
+      const int pg = key / a.page_size;
+      off = paged_row(tab[pg], a.pages, a.page_bytes, kh, a.page_size, key - pg * a.page_size, S::RB);
+    }
+    return off;
+  };
+  auto at_lane = [](int64_t x, int l) __attribute__((always_inline)) {
+    const int lo32 = __shfl((int)(uint32_t)x, l, 64), hi32 = __shfl((int)(x >> 32), l, 64);
+    return (int64_t)(((uint64_t)(uint32_t)hi32 << 32) | (uint32_t)lo32);
+  };
+  uint4 kr[S::KL], vr[S::KL];
+  auto load_k = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t off = at_lane(row, 16 * t + n);
+#pragma unroll
+      for (int s = 0; s < S::KL / 2; ++s) {
+        const char* p = off >= 0 ? a.k + off + 64 * s + 16 * g : zero;
+        kr[t * (S::KL / 2) + s] = *reinterpret_cast<const uint4*>(p);
+      }
+    }
+  };
+  auto load_v = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < S::KL; ++i) {
+      const int64_t off = at_lane(row, S::RPI * i + lane / S::LR);
+      const char* p = off >= 0 ? a.v + off + 16 * (lane % S::LR) : zero;
+      vr[i] = *reinterpret_cast<const uint4*>(p);
+    }
+  };
+
+  f32x4 o[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  char* vt = lds + w * S::VT;
+
+  int k0 = b0 + w * PG_STEP;
+  int64_t row = row_of(k0), nrow = row_of(k0 + PG_BLOCK);
+  load_k(row);
+  load_v(row);
+  for (; k0 < b1; k0 += PG_BLOCK) {
+    // scores: element v of tile t is token k0 + 16 t + 4 g + v of query head n
+    f32x4 sc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int s = 0; s < S::KS; ++s) {
+        uint4 x;
+        if constexpr (E4) {
+          const uint4 r = kr[t * (S::KL / 2) + (s >> 1)];
+          x = (s & 1) ? bf16_of_e4m3(r.z, r.w) : bf16_of_e4m3(r.x, r.y);
+        } else {
+          x = kr[t * (S::KL / 2) + s];
+        }
+        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), qf[s], sc[t], 0, 0, 0);
+      }
+    // tokens without a row (past the end, a page outside the cache) are left out
+    const uint32_t have = (uint32_t)__ballot(row >= 0);
+    load_k(nrow);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        sc[t][v] = (have >> (16 * t + 4 * g + v)) & 1 ? sc[t][v] * c2 : -INFINITY;
+        mx = fmaxf(mx, sc[t][v]);
+      }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float mnew = fmaxf(m, mx), mref = mnew == -INFINITY ? 0.f : mnew;
+    if (__any(mnew != m)) {
+      const float al = __builtin_amdgcn_exp2f(m - mref);
+      l *= al;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[i][v] *= al;
+    }
+    m = mnew;
+    // two bf16 numbers per probability: what the first leaves, the second holds, 16 bits in all
+    bf16x8 ph, pl;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float p = __builtin_amdgcn_exp2f(sc[t][v] - mref);
+        const __bf16 hi16 = static_cast<__bf16>(p);
+        l += p;
+        ph[4 * t + v] = hi16;
+        pl[4 * t + v] = static_cast<__bf16>(p - static_cast<float>(hi16));
+      }
+    // V into the wave's tile
+#pragma unroll
+    for (int i = 0; i < S::KL; ++i) {
+      const int r = S::RPI * i + lane / S::LR, c = lane % S::LR;
+      char* dst = vt + r * D * 2;
+      if constexpr (E4) {
+        *reinterpret_cast<uint4*>(dst + (vt_chunk<D>(r, 2 * c) << 4)) = bf16_of_e4m3(vr[i].x, vr[i].y);
+        *reinterpret_cast<uint4*>(dst + (vt_chunk<D>(r, 2 * c + 1) << 4)) = bf16_of_e4m3(vr[i].z, vr[i].w);
+      } else {
+        *reinterpret_cast<uint4*>(dst + (vt_chunk<D>(r, c) << 4)) = vr[i];
+      }
+    }
+    load_v(nrow);
+    row = nrow;
+    nrow = row_of(k0 + 2 * PG_BLOCK);
+    wave_order();
+    // O^T += V^T P^T: k slot (g, i) is token 4 g + i (i < 4) or 16 + 4 g + i - 4
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      s16x4 part2[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int r = 16 * t + 4 * g + (n >> 2), d = 16 * mt + 4 * (n & 3);
+        const char* p = vt + r * D * 2 + (vt_chunk<D>(r, d >> 3) << 4) + (d & 7) * 2;
+        part2[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+      }
+      const s16x8 vv = __builtin_shufflevector(part2[0], part2[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      const bf16x8 vf = __builtin_bit_cast(bf16x8, vv);
+      o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph, o[mt], 0, 0, 0);
+      o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, o[mt], 0, 0, 0);
+    }
+    wave_order();
+  }
+
+  // join the waves: l over the lanes of a head, then the four waves' sums through LDS
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    wm[w][n] = m;
+    wl[w][n] = l;
+  }
+  __syncthreads();   // every wave is done with its V tile
+  float* os = reinterpret_cast<float*>(lds) + (w * PG_HEADS + n) * D;
+  if (n < nh)
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt)
+      *reinterpret_cast<f32x4*>(os + 16 * mt + 4 * g) = o[mt];
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(lds);
+  for (int i = threadIdx.x; i < nh * (D / 4); i += PG_NT) {
+    const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+    float mm = -INFINITY, ll = 0.f;
+    for (int x = 0; x < PG_WAVES; ++x) mm = fmaxf(mm, wm[x][h]);
+    const float mr = mm == -INFINITY ? 0.f : mm;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < PG_WAVES; ++x) {
+      const float f = __builtin_amdgcn_exp2f(wm[x][h] - mr);
+      ll += f * wl[x][h];
+      const f32x4 ox = *reinterpret_cast<const f32x4*>(all + (x * PG_HEADS + h) * D + d);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] += f * ox[v];
+    }
+    const int64_t head = (int64_t)kh * a.group + h0 + h;
+    if (whole) {
+      const float inv = ll > 0.f ? vsc / ll : 0.f;
+      uint2 r;
+      r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
+      r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
+      *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + head * D + d) = r;
+      if (d == 0 && a.lse)
+        a.lse[(int64_t)seq * a.heads + head] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+    } else {
+      const int64_t at = ((int64_t)seq * a.heads + head) * a.splits + sp;
+      *reinterpret_cast<f32x4*>(a.po + at * D + d) = acc;
+      if (d == 0) {
+        a.pm[2 * at] = mm;
+        a.pm[2 * at + 1] = ll;
+      }
+    }
+  }
+}
+
+// Joins the parts of every sequence that took more than one: D / 4 threads per query head.
+template <int D>
+__global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
+  constexpr int TPH = D / 4;
+  const int64_t id = (int64_t)blockIdx.x * (256 / TPH) + threadIdx.x / TPH;
+  if (id >= (int64_t)a.seqs * a.heads) return;
+  const int seq = (int)(id / a.heads), head = (int)(id % a.heads), d = (threadIdx.x % TPH) * 4;
+  int lo, hi;
+  paged_span(a.lens[seq], a.max_pages, a.page_size, a.window, lo, hi);
+  const int part = paged_part(hi - lo, a.splits);
+  if (part >= hi - lo) return;
+  const int np = (hi - lo + part - 1) / part;
+  const float* pm = a.pm + id * a.splits * 2;
+  const float* po = a.po + id * a.splits * D + d;
+  float mm = -INFINITY;
+  for (int i = 0; i < np; ++i) mm = fmaxf(mm, pm[2 * i]);
+  const float mr = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = 0; i < np; ++i) {
+    const float f = __builtin_amdgcn_exp2f(pm[2 * i] - mr);
+    const f32x4 ox = *reinterpret_cast<const f32x4*>(po + (int64_t)i * D);
+    ll += f * pm[2 * i + 1];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] += f * ox[v];
+  }
+  const float vsc = a.vs ? a.vs[head / a.group] : 1.f;
+  const float inv = ll > 0.f ? vsc / ll : 0.f;
+  uint2 r;
+  r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
+  r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
+  *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + (int64_t)head * D + d) = r;
+  if (d == 0 && a.lse)
+    a.lse[id] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D>
+hipError_t launch_paged_d(const PagedArgs& a, int e4m3, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.seqs * a.kv_heads * a.htiles * a.splits));
+  if (e4m3) hipLaunchKernelGGL((k_paged<D, true>), grid, dim3(PG_NT), 0, st, a);
+  else hipLaunchKernelGGL((k_paged<D, false>), grid, dim3(PG_NT), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t rows = (int64_t)a.seqs * a.heads;
+  constexpr int per = 256 / (D / 4);
+  hipLaunchKernelGGL(k_paged_join<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_paged(const PagedArgs& a, int D, int e4m3, hipStream_t st) {
+  if (D == 64) return launch_paged_d<64>(a, e4m3, st);
+  if (D == 128) return launch_paged_d<128>(a, e4m3, st);
+  if (D == 256) return launch_paged_d<256>(a, e4m3, st);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace ttt

@@ -1,0 +1,392 @@
+// Per-head norm of queries and keys with the position rotation in one pass, its backward, and
+// the same pass storing keys and values into a paged cache (include/ttt_attention.h).
+//
+// Mathematics.  r = 1 / sqrt(mean(x^2) + eps), n = x r w; pair j of n turned by
+// angle_j = sum_a pos_a freq_a,j.  Backward: g = dy turned back, dw = sum g x r, u = g w,
+// dx = r (u - x r mean(u x r)).
+//
+// Every value is read once and written once, a few operations each: the memory bounds it, once
+// the angles are out of the way.  An angle needs 64-bit products (fp32 positions past 2^24
+// would lose the angle) and a sine and a cosine, but every head of a token turns by the same
+// ones: a workgroup takes a block of tokens, computes their angles once into LDS, and its
+// lanes then run over the block's heads.  A lane holds 16 elements of a head, chosen so that
+// both members of a pair are its own (two 8-element runs rot/2 apart, or 16 consecutive
+// elements): the rotation needs no exchange, the norm a few shuffles among the head's lanes.
+#include "ttt_attention_internal.h"
+
+namespace ttt {
+namespace {
+
+__device__ __forceinline__ void load8(const u16* p, float* x) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf2f((u16)(u[i] & 0xffffu));
+    x[2 * i + 1] = bf2f((u16)(u[i] >> 16));
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 w = *reinterpret_cast<const float4*>(p + 4 * i);
+    x[4 * i] = w.x;
+    x[4 * i + 1] = w.y;
+    x[4 * i + 2] = w.z;
+    x[4 * i + 3] = w.w;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  uint4 w;
+  w.x = f2bf(x[0]) | ((uint32_t)f2bf(x[1]) << 16);
+  w.y = f2bf(x[2]) | ((uint32_t)f2bf(x[3]) << 16);
+  w.z = f2bf(x[4]) | ((uint32_t)f2bf(x[5]) << 16);
+  w.w = f2bf(x[6]) | ((uint32_t)f2bf(x[7]) << 16);
+  return w;
+}
+__device__ __forceinline__ void store8(u16* p, const float* x) {
+  *reinterpret_cast<uint4*>(p) = pack8(x);
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// 8 values / scale as e4m3, held to +-448 (the conversion alone would turn larger ones to
+// NaN), a NaN kept.
+__device__ __forceinline__ void store8_e4m3(char* p, const float* x, float scale) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = x[i] / scale;
+    y[i] = v > 448.f ? 448.f : v < -448.f ? -448.f : v;
+  }
+  uint2 w;
+  w.x = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  w.x = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w.x, true);
+  w.y = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+  w.y = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], w.y, true);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+
+// Sum over the lph lanes (a power of two) that share a head.
+__device__ __forceinline__ float head_sum(float v, int lph) {
+  for (int off = lph >> 1; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// cos and sin of the block's angles: entry t * (rot / 2) + j.  The angle in turns is reduced
+// in 64 bits before it is rounded.
+__device__ __forceinline__ void turns(const RopeArgs& a, int64_t t0, int nt, float* cs, float* sn) {
+  const int half = a.rot >> 1, n = nt * half;
+  for (int i = threadIdx.x; i < n; i += ROPE_NT) {
+    const int t = i / half, j = i - t * half;
+    double ang = 0.0;
+    for (int x = 0; x < a.axes; ++x)
+      ang += (double)a.pos[(int64_t)x * a.tokens + t0 + t] * (double)a.freq[x * half + j];
+    ang *= 0.15915494309189533577;   // 1 / (2 pi)
+    ang -= rint(ang);
+    float s, c;
+    sincospif(2.f * (float)ang, &s, &c);
+    cs[i] = c;
+    sn[i] = s;
+  }
+}
+
+// The lane's two 8-element runs and whether they turn.
+struct LanePlan {
+  int e0, e1;
+  bool has, rot;
+};
+template <bool PAIRS>
+__device__ __forceinline__ LanePlan plan(const RopeArgs& a, int i) {
+  LanePlan p;
+  const int rc = a.rot >> 4;
+  p.has = i < (a.D >> 4);
+  p.rot = i < rc;
+  if (PAIRS || !p.rot) {
+    p.e0 = 16 * i;
+    p.e1 = p.e0 + 8;
+  } else {
+    p.e0 = 8 * i;
+    p.e1 = p.e0 + (a.rot >> 1);
+  }
+  return p;
+}
+
+// The lane's 8 pairs turned by (c, s): pair e is (x[e], x[8 + e]) or (x[2 e], x[2 e + 1]).
+template <bool PAIRS>
+__device__ __forceinline__ void turn(float* x, const float* c, const float* s) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i0 = PAIRS ? 2 * e : e, i1 = PAIRS ? 2 * e + 1 : 8 + e;
+    const float a = x[i0], b = x[i1];
+    x[i0] = a * c[e] - b * s[e];
+    x[i1] = a * s[e] + b * c[e];
+  }
+}
+template <bool BACK>
+__device__ __forceinline__ void read_turns(const float* cs, const float* sn, int at, float* c, float* s) {
+  load8(cs + at, c);
+  load8(sn + at, s);
+  if (BACK)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = -s[e];
+}
+
+template <typename T, bool PAIRS, bool APPEND>
+__global__ __launch_bounds__(ROPE_NT) void k_rope(RopeArgs a) {
+  __shared__ __attribute__((aligned(16))) float cs[ROPE_TURNS];
+  __shared__ __attribute__((aligned(16))) float sn[ROPE_TURNS];
+  __shared__ int64_t row[ROPE_MAX_TB];   // append: the token's first cache element, or -1
+  const int64_t t0 = (int64_t)blockIdx.x * a.tb;
+  const int nt = (int)min<int64_t>(a.tb, a.tokens - t0);
+  turns(a, t0, nt, cs, sn);
+  if (APPEND && (int)threadIdx.x < nt) {
+    const int64_t s = a.slot[t0 + threadIdx.x];
+    int64_t at = -1;
+    if (s >= 0 && s < a.slots) {
+      const int64_t page = s / a.page_size;
+      at = page * a.page_stride + (s - page * a.page_size) * a.D;
+    }
+    row[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int groups = ROPE_NT / a.lph;
+  const int g = (int)threadIdx.x / a.lph, li = (int)threadIdx.x % a.lph;
+  const LanePlan p = plan<PAIRS>(a, li);
+  const int heads = a.q.heads + (APPEND ? 2 : 1) * a.k.heads;
+  const int items = nt * heads;
+  // every lane of a wave runs the same rounds: the shuffles need the head's lanes together
+  for (int it0 = 0; it0 < items; it0 += groups) {
+    const int it = it0 + g;
+    const bool on = it < items && p.has;
+    const int tt = it / heads;
+    int h = it - tt * heads;
+    const int64_t t = t0 + tt;
+    const int which = h < a.q.heads ? 0 : h < a.q.heads + a.k.heads ? 1 : 2;
+    if (which) h -= a.q.heads + (which - 1) * a.k.heads;
+    float x[16];
+    float ss = 0.f;
+    if (on) {
+      const T* src = which == 0   ? static_cast<const T*>(a.q.x) + t * a.q.ldx
+                     : which == 1 ? static_cast<const T*>(a.k.x) + t * a.k.ldx
+                                  : static_cast<const T*>(a.v) + t * a.ldv;
+      src += (int64_t)h * a.D;
+      load8(src + p.e0, x);
+      load8(src + p.e1, x + 8);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+    }
+    if (a.norm == TTT_HEAD_NORM_RMS) ss = head_sum(ss, a.lph);
+    if (!on) continue;
+    if (which < 2) {
+      if (a.norm == TTT_HEAD_NORM_RMS) {
+        const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= r;
+        const T* w = static_cast<const T*>(which ? a.k.w : a.q.w);
+        if (w) {
+          float wv[16];
+          load8(w + p.e0, wv);
+          load8(w + p.e1, wv + 8);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] *= wv[e];
+        }
+      }
+      if (p.rot) {
+        float c[8], s[8];
+        read_turns<false>(cs, sn, tt * (a.rot >> 1) + 8 * li, c, s);
+        turn<PAIRS>(x, c, s);
+      }
+    }
+    if (!APPEND || which == 0) {
+      T* dst = which ? static_cast<T*>(a.k.y) + t * a.k.ldy : static_cast<T*>(a.q.y) + t * a.q.ldy;
+      dst += (int64_t)h * a.D;
+      store8(dst + p.e0, x);
+      store8(dst + p.e1, x + 8);
+    } else if (row[tt] >= 0) {
+      const int64_t at = row[tt] + (int64_t)h * a.page_size * a.D;
+      if (a.e4m3) {
+        const float* sc = which == 1 ? a.ks : a.vs;
+        const float scale = sc ? sc[h] : 1.f;
+        char* dst = reinterpret_cast<char*>(which == 1 ? a.kc : a.vc) + at;
+        store8_e4m3(dst + p.e0, x, scale);
+        store8_e4m3(dst + p.e1, x + 8, scale);
+      } else {
+        u16* dst = (which == 1 ? a.kc : a.vc) + at;
+        store8(dst + p.e0, x);
+        store8(dst + p.e1, x + 8);
+      }
+    }
+  }
+}
+
+// One side (queries or keys) of a block's backward; dw: the lane's running sums of g x r.
+template <typename T, bool PAIRS>
+__device__ __forceinline__ void rope_bwd_side(const RopeArgs& a, const RopeSide& sd, const LanePlan& p,
+                                              int64_t t0, int nt, int groups, int g, int li,
+                                              const float* cs, const float* sn, float* dw) {
+  const int items = nt * sd.heads;
+  const bool rms = a.norm == TTT_HEAD_NORM_RMS;
+  float w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = 1.f;
+  if (sd.w && p.has) {
+    load8(static_cast<const T*>(sd.w) + p.e0, w);
+    load8(static_cast<const T*>(sd.w) + p.e1, w + 8);
+  }
+  for (int it0 = 0; it0 < items; it0 += groups) {
+    const int it = it0 + g;
+    const bool on = it < items && p.has;
+    const int tt = it / sd.heads, h = it - tt * sd.heads;
+    const int64_t t = t0 + tt;
+    float x[16], u[16];
+    float ss = 0.f, dot = 0.f;
+    if (on) {
+      const T* sy = static_cast<const T*>(sd.dy) + t * sd.lddy + (int64_t)h * a.D;
+      load8(sy + p.e0, u);
+      load8(sy + p.e1, u + 8);
+      if (rms) {
+        const T* sx = static_cast<const T*>(sd.x) + t * sd.ldx + (int64_t)h * a.D;
+        load8(sx + p.e0, x);
+        load8(sx + p.e1, x + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+      }
+      if (p.rot) {
+        float c[8], s[8];
+        read_turns<true>(cs, sn, tt * (a.rot >> 1) + 8 * li, c, s);
+        turn<PAIRS>(u, c, s);
+      }
+    }
+    if (rms) {
+      ss = head_sum(ss, a.lph);
+      const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] *= r;
+          dw[e] = fmaf(u[e], x[e], dw[e]);
+          u[e] *= w[e];
+          dot = fmaf(u[e], x[e], dot);
+        }
+      }
+      dot = head_sum(dot, a.lph) / (float)a.D;
+      if (on)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = r * fmaf(-x[e], dot, u[e]);
+    }
+    if (on) {
+      T* dst = static_cast<T*>(sd.y) + t * sd.ldy + (int64_t)h * a.D;
+      store8(dst + p.e0, u);
+      store8(dst + p.e1, u + 8);
+    }
+  }
+}
+
+// Backward: workgroups walk over the token blocks, so that the partial sums of the scales'
+// gradients are few; a second launch adds them up in order.
+template <typename T, bool PAIRS>
+__global__ __launch_bounds__(ROPE_NT) void k_rope_bwd(RopeArgs a) {
+  __shared__ __attribute__((aligned(16))) float cs[ROPE_TURNS];
+  __shared__ __attribute__((aligned(16))) float sn[ROPE_TURNS];
+  const int groups = ROPE_NT / a.lph;
+  const int g = (int)threadIdx.x / a.lph, li = (int)threadIdx.x % a.lph;
+  const LanePlan p = plan<PAIRS>(a, li);
+  float dwq[16], dwk[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) dwq[e] = dwk[e] = 0.f;
+  const int64_t nb = (a.tokens + a.tb - 1) / a.tb;
+  for (int64_t b = blockIdx.x; b < nb; b += gridDim.x) {
+    const int64_t t0 = b * a.tb;
+    const int nt = (int)min<int64_t>(a.tb, a.tokens - t0);
+    __syncthreads();   // the last block's turns have been read
+    turns(a, t0, nt, cs, sn);
+    __syncthreads();
+    rope_bwd_side<T, PAIRS>(a, a.q, p, t0, nt, groups, g, li, cs, sn, dwq);
+    rope_bwd_side<T, PAIRS>(a, a.k, p, t0, nt, groups, g, li, cs, sn, dwk);
+  }
+  if (!a.part) return;
+  // the groups' sums: 16 values per thread through LDS, then one thread per column adds the
+  // groups' values in order.  cs and sn hold 16 * 256 floats together.
+  for (int side = 0; side < 2; ++side) {
+    const float* dw = side ? dwk : dwq;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cs[e * ROPE_NT + threadIdx.x] = dw[e];
+      sn[e * ROPE_NT + threadIdx.x] = dw[8 + e];
+    }
+    __syncthreads();
+    // column slot c = 16 * lane + e of the head's lanes
+    for (int c = threadIdx.x; c < a.D; c += ROPE_NT) {
+      const int lane = c >> 4, e = c & 15;
+      const float* src = (e < 8 ? cs + e * ROPE_NT : sn + (e - 8) * ROPE_NT) + lane;
+      float s = 0.f;
+      for (int i = 0; i < groups; ++i) s += src[i * a.lph];
+      const LanePlan q = plan<PAIRS>(a, lane);
+      a.part[((int64_t)side * a.wgs + blockIdx.x) * a.D + (e < 8 ? q.e0 + e : q.e1 + e - 8)] = s;
+    }
+  }
+}
+
+// Columns of the partial sums added up over the workgroups: 16 columns per workgroup, 16 rows
+// at a time, in 64 bits.
+__global__ __launch_bounds__(256) void k_rope_dw(RopeDwArgs a) {
+  __shared__ double acc[256];
+  const int side = blockIdx.y;
+  float* out = side ? a.dk : a.dq;
+  if (!out) return;
+  const int c = blockIdx.x * 16 + (threadIdx.x & 15), r0 = threadIdx.x >> 4;
+  const float* p = a.part + (int64_t)side * a.n * a.D + c;
+  double s = 0.0;
+  for (int r = r0; r < a.n; r += 16) s += (double)p[(int64_t)r * a.D];
+  acc[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    double t = 0.0;
+    for (int i = 0; i < 16; ++i) t += acc[16 * i + threadIdx.x];
+    out[c] = (float)t;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs& a, int bf16, hipStream_t st) {
+  const dim3 grid((unsigned)((a.tokens + a.tb - 1) / a.tb)), block(ROPE_NT);
+  if (bf16) {
+    if (a.pairs) hipLaunchKernelGGL((k_rope<u16, true, false>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_rope<u16, false, false>), grid, block, 0, st, a);
+  } else {
+    if (a.pairs) hipLaunchKernelGGL((k_rope<float, true, false>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_rope<float, false, false>), grid, block, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)((a.tokens + a.tb - 1) / a.tb)), block(ROPE_NT);
+  if (a.pairs) hipLaunchKernelGGL((k_rope<u16, true, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_rope<u16, false, true>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_backward(const RopeArgs& a, int bf16, hipStream_t st) {
+  const dim3 grid((unsigned)a.wgs), block(ROPE_NT);
+  if (bf16) {
+    if (a.pairs) hipLaunchKernelGGL((k_rope_bwd<u16, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_rope_bwd<u16, false>), grid, block, 0, st, a);
+  } else {
+    if (a.pairs) hipLaunchKernelGGL((k_rope_bwd<float, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_rope_bwd<float, false>), grid, block, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_dw(const RopeDwArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL(k_rope_dw, dim3(a.D / 16, 2), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace ttt

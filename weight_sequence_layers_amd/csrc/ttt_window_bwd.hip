@@ -1,0 +1,371 @@
+// Backward of the window attention (include/ttt_attention.h; the forward is in ttt_block.hip).
+//
+// Mathematics, with c = 1 / sqrt(128), p = exp(c q k - lse), dp = dout . v, delta = dout . out:
+//   ds = p (dp - delta),  dq = c sum_j ds k_j,  dk = c sum_t ds q_t,  dv = sum_t p dout_t.
+//
+// Two launches, each recomputing p and dp, so that every sum is one workgroup's in one order
+// and nothing is added by atomics: seven products of 2 * 128 operations per (query, key) pair
+// for the five that the formulas need.  The first takes 128 queries per workgroup and runs over
+// their keys (dq, and delta for the second); the second takes 128 keys and runs over their
+// queries (dk, dv).  Four waves hold 32 queries (keys) each: the operand that stays (q and dout;
+// k and v) in registers as MFMA fragments, the one that passes by (k and v; q and dout) in LDS
+// tiles of 64 rows, loaded one step ahead.  As in the forward the scores are computed
+// transposed, so that a lane's elements are the B operand of the product that follows; k (or q
+// and dout) is read from the same tile both along its rows and, transposed, along its columns.
+#include "ttt_attention_internal.h"
+
+namespace ttt {
+namespace {
+
+constexpr int WB_ROWS = 64;                    // rows of a tile
+constexpr int WB_TILE = WB_ROWS * ATT_D * 2;   // bytes
+
+// A tile keeps chunk c (16 bytes) of row r at chunk c ^ wb_swz(r) of the row: any 16
+// consecutive rows at one chunk, and the two chunks of 32 dims over 4 consecutive rows, lie on
+// distinct banks, so that both ways of reading it are free of conflicts.
+__device__ __forceinline__ int wb_swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+
+struct WbLoad {
+  uint32_t off[4];
+  int slice;
+  __device__ __forceinline__ void init(int64_t ld) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int p = c * 256 + tid, r = p >> 4;
+      off[c] = (uint32_t)(r * (ld * 2)) + (uint32_t)(((p & 15) ^ wb_swz(r)) << 4);
+    }
+    slice = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+  }
+  // rows [r0, r0 + 64) of a matrix of T rows at base; rows past T read as 0
+  __device__ __forceinline__ void issue(char* tile, const u16* base, int64_t ld, int r0, int T) const {
+    const uint32_t nrec = (uint32_t)max(0, min(T - r0, WB_ROWS)) * (uint32_t)(ld * 2);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + (int64_t)r0 * ld), (short)0, (int)nrec, 0x00020000);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) dma16(rs, (lds_void_t*)(tile + c * 4096 + slice), off[c]);
+  }
+};
+
+// Fragment along the rows: row row_base + lane % 32, dims 16 s + 8 (lane / 32) .. + 7.
+__device__ __forceinline__ bf16x8 wb_row(const char* tile, int row_base, int s) {
+  const int lane = threadIdx.x & 63;
+  const int r = row_base + (lane & 31), ch = 2 * s + (lane >> 5);
+  return *reinterpret_cast<const bf16x8*>(tile + r * (ATT_D * 2) + ((ch ^ wb_swz(r)) << 4));
+}
+// Fragment along the columns: dim dim_base + lane % 32, rows row_base + 4 (lane / 32) + (0..3)
+// and + 8.
+__device__ __forceinline__ bf16x8 wb_col(const char* tile, int dim_base, int row_base) {
+  const int lane = threadIdx.x & 63;
+  const int g = lane >> 4, j = lane & 15;
+  const int m = dim_base + 16 * (g & 1) + 4 * (j & 3);
+  const int r0 = row_base + 4 * (g >> 1) + (j >> 2);
+  s16x4 x[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + 8 * i;
+    const char* p = tile + r * (ATT_D * 2) + (((m >> 3) ^ wb_swz(r)) << 4) + (m & 7) * 2;
+    x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
+  }
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+__device__ __forceinline__ f32x16 wb_mma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// a row's 64 values of this lane: dims 16 s + 8 hl .. + 7
+__device__ __forceinline__ void wb_frags(bf16x8 (&f)[8], const u16* row, int hl, bool in) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    if (in) f[s] = *reinterpret_cast<const bf16x8*>(row + 16 * s + 8 * hl);
+    else f[s] = bf16x8{};
+  }
+}
+
+// dims 32 d + 8 (v / 4) + 4 hl + v % 4 of a row, times f
+__device__ __forceinline__ void wb_store(u16* row, const f32x16 (&o)[4], float f, int hl) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint2 x;
+      x.x = f2bf(o[d][4 * g] * f) | ((uint32_t)f2bf(o[d][4 * g + 1] * f) << 16);
+      x.y = f2bf(o[d][4 * g + 2] * f) | ((uint32_t)f2bf(o[d][4 * g + 3] * f) << 16);
+      *reinterpret_cast<uint2*>(row + 32 * d + 8 * g + 4 * hl) = x;
+    }
+}
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void k_window_dq(AttnBwdArgs a) {
+  __shared__ __attribute__((aligned(1024))) char st0[2 * WB_TILE];
+  __shared__ __attribute__((aligned(1024))) char st1[2 * WB_TILE];
+  const int id = xcd_block(blockIdx.x, a.total);
+  const int qb = id % a.blocks, bh = id / a.blocks;
+  const int h = bh % a.heads, b = bh / a.heads;
+  const int lane = threadIdx.x & 63, hl = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int T = a.T, W = a.window;
+  const int q0 = qb * 128, w0 = q0 + 32 * w;
+  const int t = w0 + (lane & 31);
+
+  // keys the workgroup visits, the lane's own [lo_t, hi_t), and the range that needs no mask
+  const int qlast = min(q0 + 128, T) - 1, wl = min(w0 + 31, T - 1);
+  int lo, hi, lo_t, hi_t, in_lo, in_hi;
+  if (a.mode == TTT_WINDOW_SLIDING) {
+    lo = max(0, q0 - W + 1);
+    hi = qlast + 1;
+    lo_t = t - W + 1;
+    hi_t = t + 1;
+    in_lo = wl - W + 1;
+    in_hi = w0 + 1;
+  } else {
+    lo = (q0 / W) * W;
+    hi = (int)min<int64_t>(T, ((int64_t)(qlast / W) + 1) * W);
+    lo_t = (t / W) * W;
+    hi_t = (int)min<int64_t>(T, (int64_t)lo_t + W);
+    in_lo = (wl / W) * W;
+    in_hi = (int)min<int64_t>(T, ((int64_t)(w0 / W) + 1) * W);
+  }
+  if (t >= T) lo_t = hi_t = 0;
+  if (w0 >= T) {
+    in_lo = 1;
+    in_hi = 0;
+  }
+  const int len_t = hi_t - lo_t;
+  const int nsteps = (hi - lo + WB_ROWS - 1) / WB_ROWS;
+
+  const int64_t row0 = (int64_t)b * T;
+  const u16* kb = a.k + row0 * a.ld + (int64_t)h * ATT_D;
+  const u16* vb = a.v + row0 * a.ld + (int64_t)h * ATT_D;
+  WbLoad lk;
+  lk.init(a.ld);
+  lk.issue(st0, kb, a.ld, lo, T);
+  lk.issue(st0 + WB_TILE, vb, a.ld, lo, T);
+
+  bf16x8 qf[8], gf[8];
+  wb_frags(qf, a.q + (row0 + t) * a.ld + (int64_t)h * ATT_D, hl, t < T);
+  wb_frags(gf, a.dout + (row0 + t) * a.lddo + (int64_t)h * ATT_D, hl, t < T);
+  float delta = 0.f, lse2 = 0.f;
+  {
+    const u16* orow = a.out + (row0 + t) * a.ldo + (int64_t)h * ATT_D;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      bf16x8 x = bf16x8{};
+      if (t < T) x = *reinterpret_cast<const bf16x8*>(orow + 16 * s + 8 * hl);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        delta = fmaf(static_cast<float>(x[e]), static_cast<float>(gf[s][e]), delta);
+    }
+    delta += __shfl_xor(delta, 32);
+    if (t < T) {
+      const int64_t at = ((int64_t)b * a.heads + h) * T + t;
+      lse2 = a.lse[at] * 1.44269504088896341f;
+      if (hl == 0) a.delta[at] = delta;
+    }
+  }
+
+  f32x16 dq[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dq[i] = f32x16{};
+  auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
+    const int kv0 = lo + i * WB_ROWS;
+    if (i + 1 < nsteps) {
+      lk.issue(nxt, kb, a.ld, kv0 + WB_ROWS, T);
+      lk.issue(nxt + WB_TILE, vb, a.ld, kv0 + WB_ROWS, T);
+    }
+    const bool edge = kv0 < in_lo || kv0 + WB_ROWS > in_hi;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, 32 * kt, x), qf[x], s);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(cur + WB_TILE, 32 * kt, x), gf[x], dp);
+      if (edge) {
+        const int base = kv0 + 32 * kt + 4 * hl - lo_t;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if ((unsigned)(base + 8 * (v >> 2) + (v & 3)) >= (unsigned)len_t) s[v] = -INFINITY;
+      }
+#pragma unroll
+      for (int sp = 0; sp < 2; ++sp) {
+        bf16x8 ds;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[8 * sp + e], a.scale2, -lse2));
+          ds[e] = static_cast<__bf16>(p * (dp[8 * sp + e] - delta));
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          dq[d] = wb_mma(wb_col(cur, 32 * d, 32 * kt + 16 * sp), ds, dq[d]);
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+  };
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  int i = 0;
+  for (; i + 1 < nsteps; i += 2) {
+    step(st0, st1, i);
+    step(st1, st0, i + 1);
+  }
+  if (i < nsteps) step(st0, st1, i);
+  if (t < T) wb_store(a.dq + (row0 + t) * a.ldd + (int64_t)h * ATT_D, dq, a.scale, hl);
+}
+
+// LDS of a stage: the tiles of q and dout, then their 64 rows' lse and delta
+constexpr int WB_STAGE = 2 * WB_TILE + 2 * WB_ROWS * 4;
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void k_window_dkv(AttnBwdArgs a) {
+  __shared__ __attribute__((aligned(1024))) char st0[WB_STAGE];
+  __shared__ __attribute__((aligned(1024))) char st1[WB_STAGE];
+  const int id = xcd_block(blockIdx.x, a.total);
+  const int kb = id % a.blocks, bh = id / a.blocks;
+  const int h = bh % a.heads, b = bh / a.heads;
+  const int lane = threadIdx.x & 63, hl = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int T = a.T, W = a.window;
+  const int k0 = kb * 128, w0 = k0 + 32 * w;
+  const int j = w0 + (lane & 31);
+
+  // queries the workgroup visits, the lane's own [lo_j, hi_j), and for the wave the range that
+  // sees all of its keys (no mask) and the one that sees any
+  auto first = [&](int x) __attribute__((always_inline)) {
+    return a.mode == TTT_WINDOW_SLIDING ? x : (x / W) * W;
+  };
+  auto end = [&](int x) __attribute__((always_inline)) {
+    return (int)min<int64_t>(T, a.mode == TTT_WINDOW_SLIDING ? (int64_t)x + W
+                                                             : ((int64_t)(x / W) + 1) * W);
+  };
+  const int klast = min(k0 + 128, T) - 1, wl = min(w0 + 31, T - 1);
+  const int lo = first(k0), hi = end(klast);
+  int lo_j = 0, hi_j = 0, in_lo = 1, in_hi = 0, any_lo = 0, any_hi = 0;
+  if (j < T) {
+    lo_j = first(j);
+    hi_j = end(j);
+  }
+  if (w0 < T) {
+    in_lo = first(wl);
+    in_hi = end(w0);
+    any_lo = first(w0);
+    any_hi = end(wl);
+  }
+  const int len_j = hi_j - lo_j;
+  const int nsteps = (hi - lo + WB_ROWS - 1) / WB_ROWS;
+
+  const int64_t row0 = (int64_t)b * T;
+  const u16* qb = a.q + row0 * a.ld + (int64_t)h * ATT_D;
+  const u16* gb = a.dout + row0 * a.lddo + (int64_t)h * ATT_D;
+  const float* lb = a.lse + ((int64_t)b * a.heads + h) * T;
+  const float* db = a.delta + ((int64_t)b * a.heads + h) * T;
+  WbLoad lq, lg;
+  lq.init(a.ld);
+  lg.init(a.lddo);
+  auto issue = [&](char* st, int t0) __attribute__((always_inline)) {
+    lq.issue(st, qb, a.ld, t0, T);
+    lg.issue(st + WB_TILE, gb, a.lddo, t0, T);
+    if (w < 2) {
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)((w ? db : lb) + t0), (short)0, max(0, min(T - t0, WB_ROWS)) * 4, 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * WB_TILE + w * WB_ROWS * 4),
+                                               4, lane * 4, 0, 0, 0);
+    }
+  };
+  issue(st0, lo);
+
+  bf16x8 kf[8], vf[8];
+  wb_frags(kf, a.k + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
+  wb_frags(vf, a.v + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
+  f32x16 dk[4], dv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dk[i] = dv[i] = f32x16{};
+
+  auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
+    const int t0 = lo + i * WB_ROWS;
+    if (i + 1 < nsteps) issue(nxt, t0 + WB_ROWS);
+    const char* gt = cur + WB_TILE;
+    const float* ls = reinterpret_cast<const float*>(cur + 2 * WB_TILE);
+#pragma unroll
+    for (int qt = 0; qt < 2; ++qt) {
+      const int tq = t0 + 32 * qt;
+      if (tq + 32 <= any_lo || tq >= any_hi) continue;   // wave-uniform
+      const bool edge = tq < in_lo || tq + 32 > in_hi;
+      f32x16 s = f32x16{};
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, 32 * qt, x), kf[x], s);
+      if (edge) {
+        const int base = tq + 4 * hl - lo_j;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if ((unsigned)(base + 8 * (v >> 2) + (v & 3)) >= (unsigned)len_j) s[v] = -INFINITY;
+      }
+      // element v: query tq + 8 (v / 4) + 4 hl + v % 4
+      bf16x8 pf[2];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + 32 * qt + 8 * g + 4 * hl);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 4 * g + e;
+          s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], a.scale2, -l4[e] * 1.44269504088896341f));
+          pf[v >> 3][v & 7] = static_cast<__bf16>(s[v]);
+        }
+      }
+#pragma unroll
+      for (int sp = 0; sp < 2; ++sp)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          dv[d] = wb_mma(wb_col(gt, 32 * d, 32 * qt + 16 * sp), pf[sp], dv[d]);
+      f32x16 dp = f32x16{};
+#pragma unroll
+      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, 32 * qt, x), vf[x], dp);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 d4 = *reinterpret_cast<const f32x4*>(ls + WB_ROWS + 32 * qt + 8 * g + 4 * hl);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 4 * g + e;
+          pf[v >> 3][v & 7] = static_cast<__bf16>(s[v] * (dp[v] - d4[e]));
+        }
+      }
+#pragma unroll
+      for (int sp = 0; sp < 2; ++sp)
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          dk[d] = wb_mma(wb_col(cur, 32 * d, 32 * qt + 16 * sp), pf[sp], dk[d]);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+  };
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  int i = 0;
+  for (; i + 1 < nsteps; i += 2) {
+    step(st0, st1, i);
+    step(st1, st0, i + 1);
+  }
+  if (i < nsteps) step(st0, st1, i);
+  if (j < T) {
+    const int64_t at = (row0 + j) * a.ldd + (int64_t)h * ATT_D;
+    wb_store(a.dk + at, dk, a.scale, hl);
+    wb_store(a.dv + at, dv, 1.f, hl);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_window_bwd(const AttnBwdArgs& a, hipStream_t st) {
+  if (a.total == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_window_dq, dim3(a.total), dim3(256), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_window_dkv, dim3(a.total), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace ttt
