@@ -161,16 +161,24 @@ int64_t bwd_work_bytes(const ttt_rope_config* c, int64_t tokens) {
   return (int64_t)2 * bwd_wgs(a) * a.D * (int64_t)sizeof(float);
 }
 
-// Parts that each sequence's tokens are split into, at most: enough workgroups for
-// PG_WGS_TARGET, each part at least PG_MIN_PART tokens of the longest span a sequence may have.
-constexpr int64_t PG_WGS_TARGET = 1024;
-constexpr int64_t PG_MIN_PART = 256;
+// Parts that each sequence's tokens are split into, at most.  The lengths are on the device, so
+// the rule goes by the longest span a sequence may have.
+//   - enough workgroups to fill the CUs once, as many to a CU as the kernel's registers and LDS
+//     let in (paged_per_cu): more parts than that only make the join longer (one 131072-token
+//     sequence of 8 heads: 99 us at 512 workgroups, 106 at 2048);
+//   - no part above PG_MAX_PART tokens, so that one long sequence among short ones is not left
+//     to a few workgroups (64 sequences up to 8192 tokens: 213 us, against 219 unsplit), while
+//     the launch stays below PG_WGS_MOST workgroups, most of which a ragged batch leaves empty;
+//   - no part below PG_MIN_PART tokens: two steps of every wave.
+constexpr int64_t PG_MAX_PART = 2048, PG_MIN_PART = 256, PG_WGS_MOST = 16384, NUM_CU = 256;
 
-int32_t paged_splits(int32_t seqs, int32_t kv_heads, int32_t htiles, int64_t span) {
-  const int64_t wgs = (int64_t)seqs * kv_heads * htiles;
+int64_t paged_per_cu(int32_t D, bool e4m3) { return D == 64 ? 3 : D == 128 ? (e4m3 ? 3 : 2) : 1; }
+
+int32_t paged_splits(int64_t wgs, int64_t span, int64_t per_cu) {
   if (wgs == 0) return 1;
-  const int64_t want = (PG_WGS_TARGET + wgs - 1) / wgs, most = span / PG_MIN_PART;
-  return (int32_t)std::max<int64_t>(1, std::min(want, most));
+  const int64_t fill = (NUM_CU * per_cu + wgs - 1) / wgs;
+  const int64_t even = std::min((span + PG_MAX_PART - 1) / PG_MAX_PART, PG_WGS_MOST / wgs);
+  return (int32_t)std::max<int64_t>(1, std::min(std::max(fill, even), span / PG_MIN_PART));
 }
 
 struct PagedPlan {
@@ -193,8 +201,9 @@ ttt_status paged_plan(const ttt_kv_cache* c, int32_t seqs, int32_t heads, int32_
   p->htiles = (p->group + PG_HEADS - 1) / PG_HEADS;
   int64_t span = (int64_t)max_pages * c->page_size;
   if (window) span = std::min<int64_t>(span, window);
-  p->splits = paged_splits(seqs, c->kv_heads, p->htiles, span);
-  if ((int64_t)seqs * c->kv_heads * p->htiles * p->splits >= INT31)
+  p->splits = paged_splits((int64_t)seqs * c->kv_heads * p->htiles, span,
+                           paged_per_cu(c->head_dim, c->dtype == TTT_CACHE_E4M3));
+  if ((int64_t)seqs * heads * p->splits >= INT31)
     return failf(TTT_E_SHAPE, "seqs * heads too large");
   const int64_t parts = p->splits > 1 ? (int64_t)seqs * heads * p->splits : 0;
   p->sums = parts * c->head_dim * (int64_t)sizeof(float);

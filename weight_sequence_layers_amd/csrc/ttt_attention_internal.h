@@ -7,6 +7,14 @@
 
 namespace ttt {
 
+// A pointer as one to global memory.  The compiler takes a pointer chosen at run time among
+// several for a generic one, whose accesses also count as LDS accesses: every wait for an LDS
+// read would then wait for the global loads under way.
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(1))) T* as_global(T* p) {
+  return (__attribute__((address_space(1))) T*)p;
+}
+
 // ------------------------------------------------------------------------ norm and rotation
 constexpr int ROPE_NT = 256;           // threads of a workgroup
 constexpr int ROPE_TURNS = 2048;       // cos / sin pairs a workgroup keeps in LDS

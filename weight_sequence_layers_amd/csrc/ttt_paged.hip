@@ -21,15 +21,16 @@ namespace {
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 // what rows outside the sequence or the cache read: lanes of a step that has fewer tokens
-__device__ const uint4 k_zero_row[1] = {{0u, 0u, 0u, 0u}};
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ const u32x4 k_zero_row = {0u, 0u, 0u, 0u};
 
 // 8 e4m3 numbers as bf16 (exact: e4m3's 4 significant bits and its range lie within bf16's)
-__device__ __forceinline__ uint4 bf16_of_e4m3(uint32_t lo, uint32_t hi) {
-  return make_uint4(
+__device__ __forceinline__ u32x4 bf16_of_e4m3(uint32_t lo, uint32_t hi) {
+  return u32x4{
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
       __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true)));
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true))};
 }
 
 // place of 16-byte chunk c of row r of a V tile (rows of D bf16): the rows that one transposing
@@ -47,22 +48,36 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// place of 16-byte chunk c of row r of a K tile (rows as cached, RB bytes): 16 consecutive
+// rows at one chunk lie on distinct banks
+template <int RB>
+__device__ __forceinline__ int kt_chunk(int r, int c) {
+  if (RB == 64) return c ^ ((r >> 2) & 3);
+  if (RB == 128) return c ^ ((r >> 1) & 7);
+  return c ^ (r & 15);
+}
+
 template <int D, bool E4>
 struct PagedShape {
   static constexpr int RB = D * (E4 ? 1 : 2);         // bytes of a cached row
   static constexpr int KL = PG_STEP * RB / 16 / 64;   // 16-byte loads per lane of 32 rows
-  static constexpr int LR = RB / 16;                  // lanes of a V row
-  static constexpr int RPI = 64 / LR;                 // V rows per load
+  static constexpr int LR = RB / 16;                  // lanes of a row
+  static constexpr int RPI = 64 / LR;                 // rows per load
   static constexpr int KS = D / 32;                   // MFMA steps along D
-  static constexpr int VT = PG_STEP * D * 2;          // bytes of a wave's V tile
+  static constexpr int KT = PG_STEP * RB;             // bytes of a wave's K tile, as cached
+  static constexpr int VT = PG_STEP * D * 2;          // bytes of a wave's V tile, bf16
 };
 
+// Registers held to three waves per SIMD for e4m3 heads of 128 (the compiler takes two's worth
+// by itself): half the bytes per step leave too few in flight with two (96 windows of 2048:
+// 47.7 -> 42.2 us).
 template <int D, bool E4>
-__global__ __launch_bounds__(PG_NT) void k_paged(PagedArgs a) {
+__global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedArgs a) {
   using S = PagedShape<D, E4>;
-  // the V tiles, and after the loop the waves' sums
+  // the waves' K and V tiles, and after the loop their sums
   constexpr int JOIN = PG_WAVES * PG_HEADS * D * 4;
-  constexpr int LDS = PG_WAVES * S::VT > JOIN ? PG_WAVES * S::VT : JOIN;
+  constexpr int TILES = PG_WAVES * (S::KT + S::VT);
+  constexpr int LDS = TILES > JOIN ? TILES : JOIN;
   __shared__ __attribute__((aligned(1024))) char lds[LDS];
   __shared__ float wm[PG_WAVES][PG_HEADS], wl[PG_WAVES][PG_HEADS];
 
@@ -99,39 +114,28 @@ __global__ __launch_bounds__(PG_NT) void k_paged(PagedArgs a) {
   const float c2 = a.scale * ksc * 1.44269504088896341f;
 
   const int32_t* tab = a.table + (int64_t)seq * a.max_pages;
-  const char* zero = reinterpret_cast<const char*>(k_zero_row);
-  // lane l < 32 of a step at token k0: the byte offset of row k0 + l, or -1
-  auto row_of = [&](int k0) __attribute__((always_inline)) {
+  const char* zero = reinterpret_cast<const char*>(&k_zero_row);
+  // lane l < 32 of a step at token k0: the page of token k0 + l, and its row's byte offset (-1
+  // for none)
+  auto page_of = [&](int k0) __attribute__((always_inline)) {
     const int key = k0 + (lane & 31);
-    int64_t off = -1;
-    if (key < b1) {
-      const int pg = key / a.page_size;
-      off = paged_row(tab[pg], a.pages, a.page_bytes, kh, a.page_size, key - pg * a.page_size, S::RB);
-    }
-    return off;
+    return key < b1 ? tab[key / a.page_size] : -1;
+  };
+  auto row_of = [&](int page, int k0) __attribute__((always_inline)) {
+    return paged_row(page, a.pages, a.page_bytes, kh, a.page_size, (k0 + (lane & 31)) % a.page_size, S::RB);
   };
   auto at_lane = [](int64_t x, int l) __attribute__((always_inline)) {
     const int lo32 = __shfl((int)(uint32_t)x, l, 64), hi32 = __shfl((int)(x >> 32), l, 64);
     return (int64_t)(((uint64_t)(uint32_t)hi32 << 32) | (uint32_t)lo32);
   };
-  uint4 kr[S::KL], vr[S::KL];
-  auto load_k = [&](int64_t row) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int64_t off = at_lane(row, 16 * t + n);
-#pragma unroll
-      for (int s = 0; s < S::KL / 2; ++s) {
-        const char* p = off >= 0 ? a.k + off + 64 * s + 16 * g : zero;
-        kr[t * (S::KL / 2) + s] = *reinterpret_cast<const uint4*>(p);
-      }
-    }
-  };
-  auto load_v = [&](int64_t row) __attribute__((always_inline)) {
+  u32x4 kr[S::KL], vr[S::KL];
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < S::KL; ++i) {
       const int64_t off = at_lane(row, S::RPI * i + lane / S::LR);
-      const char* p = off >= 0 ? a.v + off + 16 * (lane % S::LR) : zero;
-      vr[i] = *reinterpret_cast<const uint4*>(p);
+      const int64_t at = off + 16 * (lane % S::LR);
+      kr[i] = *as_global(reinterpret_cast<const u32x4*>(off >= 0 ? a.k + at : zero));
+      vr[i] = *as_global(reinterpret_cast<const u32x4*>(off >= 0 ? a.v + at : zero));
     }
   };
 
@@ -139,31 +143,58 @@ __global__ __launch_bounds__(PG_NT) void k_paged(PagedArgs a) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
-  char* vt = lds + w * S::VT;
+  char* kt = lds + w * (S::KT + S::VT);
+  char* vt = kt + S::KT;
 
   int k0 = b0 + w * PG_STEP;
-  int64_t row = row_of(k0), nrow = row_of(k0 + PG_BLOCK);
-  load_k(row);
-  load_v(row);
+  // Page numbers are loaded before the rows of the step ahead of theirs: loads return in order,
+  // so waiting for them does not wait for rows still on their way.
+  const int page0 = page_of(k0);
+  int npage = page_of(k0 + PG_BLOCK);
+  int64_t row = row_of(page0, k0);
+  load(row);
   for (; k0 < b1; k0 += PG_BLOCK) {
+    // this step's rows into the wave's tiles, the next step's on their way
+#pragma unroll
+    for (int i = 0; i < S::KL; ++i) {
+      const int r = S::RPI * i + lane / S::LR, c = lane % S::LR;
+      *reinterpret_cast<u32x4*>(kt + r * S::RB + (kt_chunk<S::RB>(r, c) << 4)) = kr[i];
+    }
+#pragma unroll
+    for (int i = 0; i < S::KL; ++i) {
+      const int r = S::RPI * i + lane / S::LR, c = lane % S::LR;
+      char* dst = vt + r * D * 2;
+      if constexpr (E4) {
+        *reinterpret_cast<u32x4*>(dst + (vt_chunk<D>(r, 2 * c) << 4)) = bf16_of_e4m3(vr[i].x, vr[i].y);
+        *reinterpret_cast<u32x4*>(dst + (vt_chunk<D>(r, 2 * c + 1) << 4)) = bf16_of_e4m3(vr[i].z, vr[i].w);
+      } else {
+        *reinterpret_cast<u32x4*>(dst + (vt_chunk<D>(r, c) << 4)) = vr[i];
+      }
+    }
+    // tokens without a row (past the end, a page outside the cache) are left out
+    const uint32_t have = (uint32_t)__ballot(row >= 0);
+    row = row_of(npage, k0 + PG_BLOCK);
+    npage = page_of(k0 + 2 * PG_BLOCK);
+    load(row);
+    wave_order();
     // scores: element v of tile t is token k0 + 16 t + 4 g + v of query head n
     f32x4 sc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t) {
+      const int r = 16 * t + n;
 #pragma unroll
-      for (int s = 0; s < S::KS; ++s) {
-        uint4 x;
+      for (int s = 0; s < S::KL / 2; ++s) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(kt + r * S::RB + (kt_chunk<S::RB>(r, 4 * s + g) << 4));
         if constexpr (E4) {
-          const uint4 r = kr[t * (S::KL / 2) + (s >> 1)];
-          x = (s & 1) ? bf16_of_e4m3(r.z, r.w) : bf16_of_e4m3(r.x, r.y);
+          sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, bf16_of_e4m3(x.x, x.y)), qf[2 * s], sc[t], 0, 0, 0);
+          sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, bf16_of_e4m3(x.z, x.w)), qf[2 * s + 1], sc[t], 0, 0, 0);
         } else {
-          x = kr[t * (S::KL / 2) + s];
+          sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), qf[s], sc[t], 0, 0, 0);
         }
-        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), qf[s], sc[t], 0, 0, 0);
       }
-    // tokens without a row (past the end, a page outside the cache) are left out
-    const uint32_t have = (uint32_t)__ballot(row >= 0);
-    load_k(nrow);
+    }
     float mx = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -196,22 +227,6 @@ __global__ __launch_bounds__(PG_NT) void k_paged(PagedArgs a) {
         ph[4 * t + v] = hi16;
         pl[4 * t + v] = static_cast<__bf16>(p - static_cast<float>(hi16));
       }
-    // V into the wave's tile
-#pragma unroll
-    for (int i = 0; i < S::KL; ++i) {
-      const int r = S::RPI * i + lane / S::LR, c = lane % S::LR;
-      char* dst = vt + r * D * 2;
-      if constexpr (E4) {
-        *reinterpret_cast<uint4*>(dst + (vt_chunk<D>(r, 2 * c) << 4)) = bf16_of_e4m3(vr[i].x, vr[i].y);
-        *reinterpret_cast<uint4*>(dst + (vt_chunk<D>(r, 2 * c + 1) << 4)) = bf16_of_e4m3(vr[i].z, vr[i].w);
-      } else {
-        *reinterpret_cast<uint4*>(dst + (vt_chunk<D>(r, c) << 4)) = vr[i];
-      }
-    }
-    load_v(nrow);
-    row = nrow;
-    nrow = row_of(k0 + 2 * PG_BLOCK);
-    wave_order();
     // O^T += V^T P^T: k slot (g, i) is token 4 g + i (i < 4) or 16 + 4 g + i - 4
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) {
@@ -278,13 +293,16 @@ __global__ __launch_bounds__(PG_NT) void k_paged(PagedArgs a) {
   }
 }
 
-// Joins the parts of every sequence that took more than one: D / 4 threads per query head.
+// Joins the parts of every sequence that took more than one: a workgroup per query head, whose
+// groups of D / 4 threads each sum every G-th part before the groups are joined through LDS.
 template <int D>
 __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
-  constexpr int TPH = D / 4;
-  const int64_t id = (int64_t)blockIdx.x * (256 / TPH) + threadIdx.x / TPH;
-  if (id >= (int64_t)a.seqs * a.heads) return;
-  const int seq = (int)(id / a.heads), head = (int)(id % a.heads), d = (threadIdx.x % TPH) * 4;
+  constexpr int TPH = D / 4, G = 256 / TPH;
+  __shared__ __attribute__((aligned(16))) float acc_s[G][D];
+  __shared__ float m_s[G], l_s[G];
+  const int64_t id = blockIdx.x;
+  const int seq = (int)(id / a.heads), head = (int)(id % a.heads);
+  const int g = threadIdx.x / TPH, d = (threadIdx.x % TPH) * 4;
   int lo, hi;
   paged_span(a.lens[seq], a.max_pages, a.page_size, a.window, lo, hi);
   const int part = paged_part(hi - lo, a.splits);
@@ -293,26 +311,45 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
   const float* pm = a.pm + id * a.splits * 2;
   const float* po = a.po + id * a.splits * D + d;
   float mm = -INFINITY;
-  for (int i = 0; i < np; ++i) mm = fmaxf(mm, pm[2 * i]);
+#pragma unroll 4
+  for (int i = g; i < np; i += G) mm = fmaxf(mm, pm[2 * i]);
   const float mr = mm == -INFINITY ? 0.f : mm;
   float ll = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int i = 0; i < np; ++i) {
+  for (int i = g; i < np; i += G) {
     const float f = __builtin_amdgcn_exp2f(pm[2 * i] - mr);
     const f32x4 ox = *reinterpret_cast<const f32x4*>(po + (int64_t)i * D);
     ll += f * pm[2 * i + 1];
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] += f * ox[v];
   }
+  *reinterpret_cast<f32x4*>(&acc_s[g][d]) = acc;
+  if (d == 0) {
+    m_s[g] = mm;
+    l_s[g] = ll;
+  }
+  __syncthreads();
+  if (g) return;
+  float mt = -INFINITY, lt = 0.f;
+  for (int i = 0; i < G; ++i) mt = fmaxf(mt, m_s[i]);
+  const float mtr = mt == -INFINITY ? 0.f : mt;
+  acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < G; ++i) {
+    const float f = __builtin_amdgcn_exp2f(m_s[i] - mtr);
+    const f32x4 ox = *reinterpret_cast<const f32x4*>(&acc_s[i][d]);
+    lt += f * l_s[i];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] += f * ox[v];
+  }
   const float vsc = a.vs ? a.vs[head / a.group] : 1.f;
-  const float inv = ll > 0.f ? vsc / ll : 0.f;
+  const float inv = lt > 0.f ? vsc / lt : 0.f;
   uint2 r;
   r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
   r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
   *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + (int64_t)head * D + d) = r;
   if (d == 0 && a.lse)
-    a.lse[id] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+    a.lse[id] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int D>
@@ -322,9 +359,7 @@ hipError_t launch_paged_d(const PagedArgs& a, int e4m3, hipStream_t st) {
   else hipLaunchKernelGGL((k_paged<D, false>), grid, dim3(PG_NT), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t rows = (int64_t)a.seqs * a.heads;
-  constexpr int per = 256 / (D / 4);
-  hipLaunchKernelGGL(k_paged_join<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_paged_join<D>, dim3((unsigned)((int64_t)a.seqs * a.heads)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

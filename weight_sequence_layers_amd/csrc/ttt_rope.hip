@@ -17,9 +17,11 @@
 namespace ttt {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 __device__ __forceinline__ void load8(const u16* p, float* x) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const u32x4 u = *as_global(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = bf2f((u16)(u[i] & 0xffffu));
@@ -29,27 +31,22 @@ __device__ __forceinline__ void load8(const u16* p, float* x) {
 __device__ __forceinline__ void load8(const float* p, float* x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float4 w = *reinterpret_cast<const float4*>(p + 4 * i);
-    x[4 * i] = w.x;
-    x[4 * i + 1] = w.y;
-    x[4 * i + 2] = w.z;
-    x[4 * i + 3] = w.w;
+    const f32x4 w = *as_global(reinterpret_cast<const f32x4*>(p + 4 * i));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[4 * i + e] = w[e];
   }
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  uint4 w;
-  w.x = f2bf(x[0]) | ((uint32_t)f2bf(x[1]) << 16);
-  w.y = f2bf(x[2]) | ((uint32_t)f2bf(x[3]) << 16);
-  w.z = f2bf(x[4]) | ((uint32_t)f2bf(x[5]) << 16);
-  w.w = f2bf(x[6]) | ((uint32_t)f2bf(x[7]) << 16);
-  return w;
-}
 __device__ __forceinline__ void store8(u16* p, const float* x) {
-  *reinterpret_cast<uint4*>(p) = pack8(x);
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f2bf(x[2 * i]) | ((uint32_t)f2bf(x[2 * i + 1]) << 16);
+  *as_global(reinterpret_cast<u32x4*>(p)) = w;
 }
 __device__ __forceinline__ void store8(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *as_global(reinterpret_cast<f32x4*>(p + 4 * i)) =
+        f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
 }
 
 // 8 values / scale as e4m3, held to +-448 (the conversion alone would turn larger ones to
@@ -61,12 +58,11 @@ __device__ __forceinline__ void store8_e4m3(char* p, const float* x, float scale
     const float v = x[i] / scale;
     y[i] = v > 448.f ? 448.f : v < -448.f ? -448.f : v;
   }
-  uint2 w;
-  w.x = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-  w.x = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w.x, true);
-  w.y = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
-  w.y = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], w.y, true);
-  *reinterpret_cast<uint2*>(p) = w;
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+  *as_global(reinterpret_cast<u32x2*>(p)) = u32x2{(uint32_t)lo, (uint32_t)hi};
 }
 
 // Sum over the lph lanes (a power of two) that share a head.
@@ -127,8 +123,16 @@ __device__ __forceinline__ void turn(float* x, const float* c, const float* s) {
 }
 template <bool BACK>
 __device__ __forceinline__ void read_turns(const float* cs, const float* sn, int at, float* c, float* s) {
-  load8(cs + at, c);
-  load8(sn + at, s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(cs + at + 4 * i);
+    const f32x4 y = *reinterpret_cast<const f32x4*>(sn + at + 4 * i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[4 * i + e] = x[e];
+      s[4 * i + e] = y[e];
+    }
+  }
   if (BACK)
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] = -s[e];
