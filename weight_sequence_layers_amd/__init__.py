@@ -439,16 +439,24 @@ def ttt_block_destroy(blk: Block) -> None:
 
 
 # ------------------------------------------- attention around the block (ttt_attention.h)
-def _arg(t, name: str, dtype, n: int, dense: bool = True) -> Optional[int]:
+def _here(stream):
+    """The current device's number and the handle of `stream` (None: its current stream)."""
+    import torch
+    dev = torch.cuda.current_device()
+    if stream is None:   # the handle without a Stream object around it: 1 us less per call
+        return dev, torch._C._cuda_getCurrentRawStream(dev) or None
+    return dev, _stream(stream)
+
+
+def _arg(t, name: str, dtype, n: int, dev: int, dense: bool = True) -> Optional[int]:
     """The pointer of a device tensor argument, after the checks that the library cannot make:
-    a tensor of the current device, of its dtype, with at least n elements (dense: contiguous).
-    None passes as NULL."""
+    a tensor of the current device dev, of its dtype, with at least n elements (dense:
+    contiguous). None passes as NULL."""
     if t is None:
         return None
-    import torch
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise TTTError(4, f"{name} is on {t.device}, not on the current HIP device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TTTError(3, f"{name} is {t.dtype}, not {dtype}")
     if t.numel() < n:
         raise TTTError(2, f"{name} has {t.numel()} elements, {n} needed")
@@ -457,9 +465,9 @@ def _arg(t, name: str, dtype, n: int, dense: bool = True) -> Optional[int]:
     return t.data_ptr()
 
 
-def _work(t):
+def _work(t, dev: int):
     """Pointer and bytes of a workspace tensor of any dtype (None: none)."""
-    return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0), t.numel() * t.element_size())
+    return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0, dev), t.numel() * t.element_size())
 
 
 def _act_dtype(cfg):
@@ -486,12 +494,12 @@ def ttt_validate_rope_config(cfg: ttt_rope_config) -> None:
     _check(lib().ttt_validate_rope_config(ctypes.byref(cfg)))
 
 
-def _rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens):
+def _rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev):
     import torch
     dt, half = _act_dtype(cfg), cfg.rot_dim // 2
-    return (_arg(q_weight, "q_weight", dt, cfg.head_dim), _arg(k_weight, "k_weight", dt, cfg.head_dim),
-            _arg(freq, "freq", torch.float32, cfg.axes * half),
-            _arg(pos, "pos", torch.int32, cfg.axes * tokens if half else 0))
+    return (_arg(q_weight, "q_weight", dt, cfg.head_dim, dev), _arg(k_weight, "k_weight", dt, cfg.head_dim, dev),
+            _arg(freq, "freq", torch.float32, cfg.axes * half, dev),
+            _arg(pos, "pos", torch.int32, cfg.axes * tokens if half else 0, dev))
 
 
 def ttt_qk_norm_rope(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight, k_weight, freq,
@@ -500,12 +508,13 @@ def ttt_qk_norm_rope(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight,
     """Per-head norm and position rotation of queries and keys: element (t, h, e) of q at
     t ld_q + h head_dim + e (k, q_out and k_out with theirs); freq fp32 [axes, rot_dim / 2],
     pos int32 [axes, tokens] (see include/ttt_attention.h)."""
+    dev, st = _here(stream)
     dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
     _check(lib().ttt_qk_norm_rope(
-        ctypes.byref(cfg), _arg(q, "q", dt, nq, False), ld_q, _arg(k, "k", dt, nk, False), ld_k,
-        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens),
-        _arg(q_out, "q_out", dt, nq, False), ld_qo, _arg(k_out, "k_out", dt, nk, False), ld_ko, tokens,
-        _stream(stream)))
+        ctypes.byref(cfg), _arg(q, "q", dt, nq, dev, False), ld_q, _arg(k, "k", dt, nk, dev, False), ld_k,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev),
+        _arg(q_out, "q_out", dt, nq, dev, False), ld_qo, _arg(k_out, "k_out", dt, nk, dev, False), ld_ko, tokens,
+        st))
 
 
 def ttt_qk_norm_rope_backward_work(cfg: ttt_rope_config, tokens: int) -> int:
@@ -523,15 +532,16 @@ def ttt_qk_norm_rope_backward(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, 
     [head_dim], or None); work: device tensor of at least ttt_qk_norm_rope_backward_work bytes
     (see include/ttt_attention.h)."""
     import torch
+    dev, st = _here(stream)
     dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
     f32 = torch.float32
     _check(lib().ttt_qk_norm_rope_backward(
-        ctypes.byref(cfg), _arg(q, "q", dt, nq, False), ld_q, _arg(k, "k", dt, nk, False), ld_k,
-        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens),
-        _arg(dq_out, "dq_out", dt, nq, False), ld_dqo, _arg(dk_out, "dk_out", dt, nk, False), ld_dko,
-        _arg(dq, "dq", dt, nq, False), ld_dq, _arg(dk, "dk", dt, nk, False), ld_dk,
-        _arg(dq_weight, "dq_weight", f32, cfg.head_dim), _arg(dk_weight, "dk_weight", f32, cfg.head_dim),
-        *_work(work), tokens, _stream(stream)))
+        ctypes.byref(cfg), _arg(q, "q", dt, nq, dev, False), ld_q, _arg(k, "k", dt, nk, dev, False), ld_k,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev),
+        _arg(dq_out, "dq_out", dt, nq, dev, False), ld_dqo, _arg(dk_out, "dk_out", dt, nk, dev, False), ld_dko,
+        _arg(dq, "dq", dt, nq, dev, False), ld_dq, _arg(dk, "dk", dt, nk, dev, False), ld_dk,
+        _arg(dq_weight, "dq_weight", f32, cfg.head_dim, dev), _arg(dk_weight, "dk_weight", f32, cfg.head_dim, dev),
+        *_work(work, dev), tokens, st))
 
 
 def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
@@ -543,6 +553,7 @@ def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
     if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
         raise TTTError(2, "k and v: two tensors [pages, kv_heads, page_size, head_dim] of one "
                           "dtype and layout")
+    dev = torch.cuda.current_device()
     pages, heads, size, dim = k.shape
     if not k[0].is_contiguous():
         raise TTTError(2, "a page must be contiguous")
@@ -550,9 +561,9 @@ def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
     if k.dtype not in dtypes:
         raise TTTError(3, f"cache of {k.dtype}: bfloat16 or float8_e4m3fn")
     c = ttt_kv_cache()
-    c.k, c.v = _arg(k, "k", k.dtype, 0, False), _arg(v, "v", v.dtype, 0, False)
-    c.k_scale = _arg(k_scale, "k_scale", torch.float32, heads)
-    c.v_scale = _arg(v_scale, "v_scale", torch.float32, heads)
+    c.k, c.v = _arg(k, "k", k.dtype, 0, dev, False), _arg(v, "v", v.dtype, 0, dev, False)
+    c.k_scale = _arg(k_scale, "k_scale", torch.float32, heads, dev)
+    c.v_scale = _arg(v_scale, "v_scale", torch.float32, heads, dev)
     c.page_stride = k.stride(0) if pages > 1 else heads * size * dim
     c.pages, c.page_size, c.kv_heads, c.head_dim = pages, size, heads, dim
     c.dtype, c.reserved = dtypes[k.dtype], 0
@@ -567,12 +578,13 @@ def ttt_qk_norm_rope_append(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, v,
     page * page_size + place, or negative for a token that is not stored
     (see include/ttt_attention.h)."""
     import torch
+    dev, st = _here(stream)
     dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
     _check(lib().ttt_qk_norm_rope_append(
-        ctypes.byref(cfg), _arg(q, "q", dt, nq, False), ld_q, _arg(k, "k", dt, nk, False), ld_k,
-        _arg(v, "v", dt, nk, False), ld_v, *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens),
-        ctypes.byref(cache), _arg(slot, "slot", torch.int64, tokens), _arg(q_out, "q_out", dt, nq, False),
-        ld_qo, tokens, _stream(stream)))
+        ctypes.byref(cfg), _arg(q, "q", dt, nq, dev, False), ld_q, _arg(k, "k", dt, nk, dev, False), ld_k,
+        _arg(v, "v", dt, nk, dev, False), ld_v, *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev),
+        ctypes.byref(cache), _arg(slot, "slot", torch.int64, tokens, dev), _arg(q_out, "q_out", dt, nq, dev, False),
+        ld_qo, tokens, st))
 
 
 def ttt_paged_attention_work(cache: ttt_kv_cache, seqs: int, heads: int, max_pages: int,
@@ -591,12 +603,13 @@ def ttt_paged_attention(q, ld_q: int, cache: ttt_kv_cache, table, lens, out, ld_
     [seqs, max_pages], lens int32 [seqs]; window 0: all of them; scale 0: 1 / sqrt(head_dim);
     lse fp32 [seqs, heads] or None (see include/ttt_attention.h)."""
     import torch
+    dev, st = _here(stream)
     bf, n = torch.bfloat16, seqs * heads * cache.head_dim
     _check(lib().ttt_paged_attention(
-        _arg(q, "q", bf, n, False), ld_q, ctypes.byref(cache),
-        _arg(table, "table", torch.int32, seqs * max_pages), _arg(lens, "lens", torch.int32, seqs),
-        _arg(out, "out", bf, n, False), ld_out, _arg(lse, "lse", torch.float32, seqs * heads), seqs,
-        heads, max_pages, window, scale, *_work(work), _stream(stream)))
+        _arg(q, "q", bf, n, dev, False), ld_q, ctypes.byref(cache),
+        _arg(table, "table", torch.int32, seqs * max_pages, dev), _arg(lens, "lens", torch.int32, seqs, dev),
+        _arg(out, "out", bf, n, dev, False), ld_out, _arg(lse, "lse", torch.float32, seqs * heads, dev), seqs,
+        heads, max_pages, window, scale, *_work(work, dev), st))
 
 
 def ttt_window_attention_lse(q, k, v, ld: int, out, ld_out: int, lse, batch: int, heads: int,
@@ -605,12 +618,13 @@ def ttt_window_attention_lse(q, k, v, ld: int, out, ld_out: int, lse, batch: int
     (see include/ttt_attention.h)."""
     import torch
     m = WINDOW[mode] if isinstance(mode, str) else int(mode)
+    dev, st = _here(stream)
     bf, rows = torch.bfloat16, batch * heads * seq_len
     n = rows * ATTN_HEAD_DIM
     _check(lib().ttt_window_attention_lse(
-        _arg(q, "q", bf, n, False), _arg(k, "k", bf, n, False), _arg(v, "v", bf, n, False), ld,
-        _arg(out, "out", bf, n, False), ld_out, _arg(lse, "lse", torch.float32, rows), batch, heads,
-        seq_len, window, m, _stream(stream)))
+        _arg(q, "q", bf, n, dev, False), _arg(k, "k", bf, n, dev, False), _arg(v, "v", bf, n, dev, False), ld,
+        _arg(out, "out", bf, n, dev, False), ld_out, _arg(lse, "lse", torch.float32, rows, dev), batch, heads,
+        seq_len, window, m, st))
 
 
 def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout, ld_dout: int, dq,
@@ -620,11 +634,12 @@ def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout,
     [batch, heads, seq_len] (see include/ttt_attention.h)."""
     import torch
     m = WINDOW[mode] if isinstance(mode, str) else int(mode)
+    dev, st = _here(stream)
     bf, f32, rows = torch.bfloat16, torch.float32, batch * heads * seq_len
     n = rows * ATTN_HEAD_DIM
     _check(lib().ttt_window_attention_backward(
-        _arg(q, "q", bf, n, False), _arg(k, "k", bf, n, False), _arg(v, "v", bf, n, False), ld,
-        _arg(out, "out", bf, n, False), ld_out, _arg(lse, "lse", f32, rows),
-        _arg(dout, "dout", bf, n, False), ld_dout, _arg(dq, "dq", bf, n, False),
-        _arg(dk, "dk", bf, n, False), _arg(dv, "dv", bf, n, False), ld_d, _arg(work, "work", f32, rows),
-        batch, heads, seq_len, window, m, _stream(stream)))
+        _arg(q, "q", bf, n, dev, False), _arg(k, "k", bf, n, dev, False), _arg(v, "v", bf, n, dev, False), ld,
+        _arg(out, "out", bf, n, dev, False), ld_out, _arg(lse, "lse", f32, rows, dev),
+        _arg(dout, "dout", bf, n, dev, False), ld_dout, _arg(dq, "dq", bf, n, dev, False),
+        _arg(dk, "dk", bf, n, dev, False), _arg(dv, "dv", bf, n, dev, False), ld_d, _arg(work, "work", f32, rows, dev),
+        batch, heads, seq_len, window, m, st))

@@ -19,7 +19,7 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* as_global(T* p) 
 constexpr int ROPE_NT = 256;           // threads of a workgroup
 constexpr int ROPE_TURNS = 2048;       // cos / sin pairs a workgroup keeps in LDS
 constexpr int ROPE_MAX_TB = 16;        // tokens of a workgroup's block, at most
-constexpr int ROPE_BWD_WGS = 1024;     // workgroups of a backward launch, at most
+constexpr int ROPE_BWD_WGS = 512;      // workgroups of a side of a backward launch, at most
 
 // heads x head_dim values per token: rows of x, rows of y, the learned scale
 struct RopeSide {

@@ -10,8 +10,8 @@
 // would lose the angle) and a sine and a cosine, but every head of a token turns by the same
 // ones: a workgroup takes a block of tokens, computes their angles once into LDS, and its
 // lanes then run over the block's heads.  A lane holds 16 elements of a head, chosen so that
-// both members of a pair are its own (two 8-element runs rot/2 apart, or 16 consecutive
-// elements): the rotation needs no exchange, the norm a few shuffles among the head's lanes.
+// both members of a pair are its own: the rotation needs no exchange, the norm a few shuffles
+// among the head's lanes.
 #include "ttt_attention_internal.h"
 
 namespace ttt {
@@ -20,7 +20,10 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ void load8(const u16* p, float* x) {
+// 16 bytes of T and back: 8 bf16 or 4 fp32
+template <typename T>
+constexpr int VW = 16 / (int)sizeof(T);
+__device__ __forceinline__ void load16(const u16* p, float* x) {
   const u32x4 u = *as_global(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -28,25 +31,19 @@ __device__ __forceinline__ void load8(const u16* p, float* x) {
     x[2 * i + 1] = bf2f((u16)(u[i] >> 16));
   }
 }
-__device__ __forceinline__ void load8(const float* p, float* x) {
+__device__ __forceinline__ void load16(const float* p, float* x) {
+  const f32x4 w = *as_global(reinterpret_cast<const f32x4*>(p));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const f32x4 w = *as_global(reinterpret_cast<const f32x4*>(p + 4 * i));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[4 * i + e] = w[e];
-  }
+  for (int e = 0; e < 4; ++e) x[e] = w[e];
 }
-__device__ __forceinline__ void store8(u16* p, const float* x) {
+__device__ __forceinline__ void store16(u16* p, const float* x) {
   u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = f2bf(x[2 * i]) | ((uint32_t)f2bf(x[2 * i + 1]) << 16);
   *as_global(reinterpret_cast<u32x4*>(p)) = w;
 }
-__device__ __forceinline__ void store8(float* p, const float* x) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    *as_global(reinterpret_cast<f32x4*>(p + 4 * i)) =
-        f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+__device__ __forceinline__ void store16(float* p, const float* x) {
+  *as_global(reinterpret_cast<f32x4*>(p)) = f32x4{x[0], x[1], x[2], x[3]};
 }
 
 // 8 values / scale as e4m3, held to +-448 (the conversion alone would turn larger ones to
@@ -89,26 +86,47 @@ __device__ __forceinline__ void turns(const RopeArgs& a, int64_t t0, int nt, flo
   }
 }
 
-// The lane's two 8-element runs and whether they turn.
+// The lane's 16 elements of a head, as 16-byte runs: neighbouring lanes take neighbouring runs,
+// so that each load of a wave is contiguous.  Lanes i < rot / 16 hold what turns: with HALVES
+// half of their runs in each half of the rotated elements, at the same places.
+template <typename T, bool PAIRS>
 struct LanePlan {
-  int e0, e1;
+  static constexpr int N = 16 / VW<T>;          // runs
+  static constexpr int TN = PAIRS ? N : N / 2;  // runs of turns, 8 / TN each
+  int off[N], toff[TN];
   bool has, rot;
-};
-template <bool PAIRS>
-__device__ __forceinline__ LanePlan plan(const RopeArgs& a, int i) {
-  LanePlan p;
-  const int rc = a.rot >> 4;
-  p.has = i < (a.D >> 4);
-  p.rot = i < rc;
-  if (PAIRS || !p.rot) {
-    p.e0 = 16 * i;
-    p.e1 = p.e0 + 8;
-  } else {
-    p.e0 = 8 * i;
-    p.e1 = p.e0 + (a.rot >> 1);
+  __device__ __forceinline__ LanePlan(const RopeArgs& a, int i) {
+    const int rc = a.rot >> 4, all = a.D >> 4;
+    has = i < all;
+    rot = i < rc;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (!rot) off[n] = a.rot + VW<T> * (i - rc + n * (all - rc));
+      else if (PAIRS) off[n] = VW<T> * (i + n * rc);
+      else off[n] = VW<T> * (i + n % (N / 2) * rc) + (n / (N / 2)) * (a.rot >> 1);
+    }
+#pragma unroll
+    for (int n = 0; n < TN; ++n) toff[n] = 8 / TN * (i + n * rc);
   }
-  return p;
-}
+  __device__ __forceinline__ void load(const T* p, float* x) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) load16(p + off[n], x + VW<T> * n);
+  }
+  __device__ __forceinline__ void store(T* p, const float* x) const {
+#pragma unroll
+    for (int n = 0; n < N; ++n) store16(p + off[n], x + VW<T> * n);
+  }
+  // cos and sin of the lane's 8 pairs from a token's table
+  __device__ __forceinline__ void turns(const float* cs, const float* sn, float* c, float* s) const {
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int e = 0; e < 8 / TN; ++e) {
+        c[8 / TN * n + e] = cs[toff[n] + e];
+        s[8 / TN * n + e] = sn[toff[n] + e];
+      }
+  }
+};
 
 // The lane's 8 pairs turned by (c, s): pair e is (x[e], x[8 + e]) or (x[2 e], x[2 e + 1]).
 template <bool PAIRS>
@@ -121,23 +139,6 @@ __device__ __forceinline__ void turn(float* x, const float* c, const float* s) {
     x[i1] = a * s[e] + b * c[e];
   }
 }
-template <bool BACK>
-__device__ __forceinline__ void read_turns(const float* cs, const float* sn, int at, float* c, float* s) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const f32x4 x = *reinterpret_cast<const f32x4*>(cs + at + 4 * i);
-    const f32x4 y = *reinterpret_cast<const f32x4*>(sn + at + 4 * i);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[4 * i + e] = x[e];
-      s[4 * i + e] = y[e];
-    }
-  }
-  if (BACK)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = -s[e];
-}
-
 template <typename T, bool PAIRS, bool APPEND>
 __global__ __launch_bounds__(ROPE_NT) void k_rope(RopeArgs a) {
   __shared__ __attribute__((aligned(16))) float cs[ROPE_TURNS];
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(ROPE_NT) void k_rope(RopeArgs a) {
   __syncthreads();
   const int groups = ROPE_NT / a.lph;
   const int g = (int)threadIdx.x / a.lph, li = (int)threadIdx.x % a.lph;
-  const LanePlan p = plan<PAIRS>(a, li);
+  const LanePlan<T, PAIRS> p(a, li);
   const int heads = a.q.heads + (APPEND ? 2 : 1) * a.k.heads;
   const int items = nt * heads;
   // every lane of a wave runs the same rounds: the shuffles need the head's lanes together
@@ -177,8 +178,7 @@ __global__ __launch_bounds__(ROPE_NT) void k_rope(RopeArgs a) {
                      : which == 1 ? static_cast<const T*>(a.k.x) + t * a.k.ldx
                                   : static_cast<const T*>(a.v) + t * a.ldv;
       src += (int64_t)h * a.D;
-      load8(src + p.e0, x);
-      load8(src + p.e1, x + 8);
+      p.load(src, x);
 #pragma unroll
       for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
     }
@@ -192,115 +192,63 @@ __global__ __launch_bounds__(ROPE_NT) void k_rope(RopeArgs a) {
         const T* w = static_cast<const T*>(which ? a.k.w : a.q.w);
         if (w) {
           float wv[16];
-          load8(w + p.e0, wv);
-          load8(w + p.e1, wv + 8);
+          p.load(w, wv);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] *= wv[e];
         }
       }
       if (p.rot) {
         float c[8], s[8];
-        read_turns<false>(cs, sn, tt * (a.rot >> 1) + 8 * li, c, s);
+        p.turns(cs + tt * (a.rot >> 1), sn + tt * (a.rot >> 1), c, s);
         turn<PAIRS>(x, c, s);
       }
     }
-    if (!APPEND || which == 0) {
-      T* dst = which ? static_cast<T*>(a.k.y) + t * a.k.ldy : static_cast<T*>(a.q.y) + t * a.q.ldy;
-      dst += (int64_t)h * a.D;
-      store8(dst + p.e0, x);
-      store8(dst + p.e1, x + 8);
-    } else if (row[tt] >= 0) {
-      const int64_t at = row[tt] + (int64_t)h * a.page_size * a.D;
-      if (a.e4m3) {
-        const float* sc = which == 1 ? a.ks : a.vs;
-        const float scale = sc ? sc[h] : 1.f;
-        char* dst = reinterpret_cast<char*>(which == 1 ? a.kc : a.vc) + at;
-        store8_e4m3(dst + p.e0, x, scale);
-        store8_e4m3(dst + p.e1, x + 8, scale);
-      } else {
-        u16* dst = (which == 1 ? a.kc : a.vc) + at;
-        store8(dst + p.e0, x);
-        store8(dst + p.e1, x + 8);
-      }
-    }
-  }
-}
-
-// One side (queries or keys) of a block's backward; dw: the lane's running sums of g x r.
-template <typename T, bool PAIRS>
-__device__ __forceinline__ void rope_bwd_side(const RopeArgs& a, const RopeSide& sd, const LanePlan& p,
-                                              int64_t t0, int nt, int groups, int g, int li,
-                                              const float* cs, const float* sn, float* dw) {
-  const int items = nt * sd.heads;
-  const bool rms = a.norm == TTT_HEAD_NORM_RMS;
-  float w[16];
+    if constexpr (APPEND) {
+      if (which) {
+        if (row[tt] < 0) continue;
+        const int64_t at = row[tt] + (int64_t)h * a.page_size * a.D;
+        if (a.e4m3) {
+          const float* sc = which == 1 ? a.ks : a.vs;
+          const float scale = sc ? sc[h] : 1.f;
+          char* dst = reinterpret_cast<char*>(which == 1 ? a.kc : a.vc) + at;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = 1.f;
-  if (sd.w && p.has) {
-    load8(static_cast<const T*>(sd.w) + p.e0, w);
-    load8(static_cast<const T*>(sd.w) + p.e1, w + 8);
-  }
-  for (int it0 = 0; it0 < items; it0 += groups) {
-    const int it = it0 + g;
-    const bool on = it < items && p.has;
-    const int tt = it / sd.heads, h = it - tt * sd.heads;
-    const int64_t t = t0 + tt;
-    float x[16], u[16];
-    float ss = 0.f, dot = 0.f;
-    if (on) {
-      const T* sy = static_cast<const T*>(sd.dy) + t * sd.lddy + (int64_t)h * a.D;
-      load8(sy + p.e0, u);
-      load8(sy + p.e1, u + 8);
-      if (rms) {
-        const T* sx = static_cast<const T*>(sd.x) + t * sd.ldx + (int64_t)h * a.D;
-        load8(sx + p.e0, x);
-        load8(sx + p.e1, x + 8);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-      }
-      if (p.rot) {
-        float c[8], s[8];
-        read_turns<true>(cs, sn, tt * (a.rot >> 1) + 8 * li, c, s);
-        turn<PAIRS>(u, c, s);
-      }
-    }
-    if (rms) {
-      ss = head_sum(ss, a.lph);
-      const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
-      if (on) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] *= r;
-          dw[e] = fmaf(u[e], x[e], dw[e]);
-          u[e] *= w[e];
-          dot = fmaf(u[e], x[e], dot);
+          for (int n = 0; n < 2; ++n) store8_e4m3(dst + p.off[n], x + 8 * n, scale);
+        } else {
+          p.store((which == 1 ? a.kc : a.vc) + at, x);
         }
+        continue;
       }
-      dot = head_sum(dot, a.lph) / (float)a.D;
-      if (on)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) u[e] = r * fmaf(-x[e], dot, u[e]);
     }
-    if (on) {
-      T* dst = static_cast<T*>(sd.y) + t * sd.ldy + (int64_t)h * a.D;
-      store8(dst + p.e0, u);
-      store8(dst + p.e1, u + 8);
-    }
+    T* dst = which ? static_cast<T*>(a.k.y) + t * a.k.ldy : static_cast<T*>(a.q.y) + t * a.q.ldy;
+    p.store(dst + (int64_t)h * a.D, x);
   }
 }
 
-// Backward: workgroups walk over the token blocks, so that the partial sums of the scales'
-// gradients are few; a second launch adds them up in order.
+// Backward: blockIdx.y is the side (queries, keys); a side's workgroups walk over the token
+// blocks, so that the partial sums of the scales' gradients are few, and a second launch adds
+// them up in order.  (Both sides in one workgroup hold two sets of running sums: 140 registers,
+// three waves per SIMD instead of four.)
 template <typename T, bool PAIRS>
 __global__ __launch_bounds__(ROPE_NT) void k_rope_bwd(RopeArgs a) {
   __shared__ __attribute__((aligned(16))) float cs[ROPE_TURNS];
   __shared__ __attribute__((aligned(16))) float sn[ROPE_TURNS];
+  const RopeSide& sd = blockIdx.y ? a.k : a.q;
   const int groups = ROPE_NT / a.lph;
   const int g = (int)threadIdx.x / a.lph, li = (int)threadIdx.x % a.lph;
-  const LanePlan p = plan<PAIRS>(a, li);
-  float dwq[16], dwk[16];
+  const LanePlan<T, PAIRS> p(a, li);
+  const bool rms = a.norm == TTT_HEAD_NORM_RMS;
+  const T* sdx = static_cast<const T*>(sd.x);
+  const T* sdy = static_cast<const T*>(sd.dy);
+  T* sy = static_cast<T*>(sd.y);
+  const int64_t ldx = sd.ldx, lddy = sd.lddy, ldy = sd.ldy;
+  const int heads = sd.heads;
+  float w[16], dw[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dwq[e] = dwk[e] = 0.f;
+  for (int e = 0; e < 16; ++e) {
+    w[e] = 1.f;
+    dw[e] = 0.f;
+  }
+  if (sd.w && p.has) p.load(static_cast<const T*>(sd.w), w);
   const int64_t nb = (a.tokens + a.tb - 1) / a.tb;
   for (int64_t b = blockIdx.x; b < nb; b += gridDim.x) {
     const int64_t t0 = b * a.tb;
@@ -308,51 +256,91 @@ __global__ __launch_bounds__(ROPE_NT) void k_rope_bwd(RopeArgs a) {
     __syncthreads();   // the last block's turns have been read
     turns(a, t0, nt, cs, sn);
     __syncthreads();
-    rope_bwd_side<T, PAIRS>(a, a.q, p, t0, nt, groups, g, li, cs, sn, dwq);
-    rope_bwd_side<T, PAIRS>(a, a.k, p, t0, nt, groups, g, li, cs, sn, dwk);
+    const int items = nt * heads;
+    for (int it0 = 0; it0 < items; it0 += groups) {
+      const int it = it0 + g;
+      const bool on = it < items && p.has;
+      const int tt = it / heads, h = it - tt * heads;
+      const int64_t t = t0 + tt, col = (int64_t)h * a.D;
+      float x[16], u[16];
+      float ss = 0.f, dot = 0.f;
+      if (on) {
+        p.load(sdy + t * lddy + col, u);
+        if (rms) {
+          p.load(sdx + t * ldx + col, x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+        }
+        if (p.rot) {
+          float c[8], s[8];
+          p.turns(cs + tt * (a.rot >> 1), sn + tt * (a.rot >> 1), c, s);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = -s[e];
+          turn<PAIRS>(u, c, s);
+        }
+      }
+      if (rms) {
+        ss = head_sum(ss, a.lph);
+        const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
+        if (on) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[e] *= r;
+            dw[e] = fmaf(u[e], x[e], dw[e]);
+            u[e] *= w[e];
+            dot = fmaf(u[e], x[e], dot);
+          }
+        }
+        dot = head_sum(dot, a.lph) / (float)a.D;
+        if (on)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = r * fmaf(-x[e], dot, u[e]);
+      }
+      if (on) p.store(sy + t * ldy + col, u);
+    }
   }
   if (!a.part) return;
-  // the groups' sums: 16 values per thread through LDS, then one thread per column adds the
-  // groups' values in order.  cs and sn hold 16 * 256 floats together.
-  for (int side = 0; side < 2; ++side) {
-    const float* dw = side ? dwk : dwq;
-    __syncthreads();
+  // the groups' sums: 16 values per thread through LDS (cs and sn hold 16 * 256 floats
+  // together), then one thread per column adds the groups' values in order
+  __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e * ROPE_NT + threadIdx.x] = dw[e];
-      sn[e * ROPE_NT + threadIdx.x] = dw[8 + e];
-    }
-    __syncthreads();
-    // column slot c = 16 * lane + e of the head's lanes
-    for (int c = threadIdx.x; c < a.D; c += ROPE_NT) {
-      const int lane = c >> 4, e = c & 15;
-      const float* src = (e < 8 ? cs + e * ROPE_NT : sn + (e - 8) * ROPE_NT) + lane;
-      float s = 0.f;
-      for (int i = 0; i < groups; ++i) s += src[i * a.lph];
-      const LanePlan q = plan<PAIRS>(a, lane);
-      a.part[((int64_t)side * a.wgs + blockIdx.x) * a.D + (e < 8 ? q.e0 + e : q.e1 + e - 8)] = s;
-    }
+  for (int e = 0; e < 8; ++e) {
+    cs[e * ROPE_NT + threadIdx.x] = dw[e];
+    sn[e * ROPE_NT + threadIdx.x] = dw[8 + e];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.D; c += ROPE_NT) {
+    const int lane = c >> 4, e = c & 15;
+    const float* src = (e < 8 ? cs + e * ROPE_NT : sn + (e - 8) * ROPE_NT) + lane;
+    float s = 0.f;
+    for (int i = 0; i < groups; ++i) s += src[i * a.lph];
+    const LanePlan<T, PAIRS> q(a, lane);
+    int at = 0;   // a register array takes no run-time index
+#pragma unroll
+    for (int n = 0; n < LanePlan<T, PAIRS>::N; ++n)
+      if (e / VW<T> == n) at = q.off[n] + e % VW<T>;
+    a.part[((int64_t)blockIdx.y * a.wgs + blockIdx.x) * a.D + at] = s;
   }
 }
 
-// Columns of the partial sums added up over the workgroups: 16 columns per workgroup, 16 rows
-// at a time, in 64 bits.
-__global__ __launch_bounds__(256) void k_rope_dw(RopeDwArgs a) {
-  __shared__ double acc[256];
+// Columns of the partial sums added up over the workgroups: 16 columns per workgroup, 64 rows
+// at a time, in 64 bits and one order.
+__global__ __launch_bounds__(1024) void k_rope_dw(RopeDwArgs a) {
+  __shared__ double acc[1024];
   const int side = blockIdx.y;
   float* out = side ? a.dk : a.dq;
   if (!out) return;
   const int c = blockIdx.x * 16 + (threadIdx.x & 15), r0 = threadIdx.x >> 4;
   const float* p = a.part + (int64_t)side * a.n * a.D + c;
   double s = 0.0;
-  for (int r = r0; r < a.n; r += 16) s += (double)p[(int64_t)r * a.D];
+#pragma unroll 8
+  for (int r = r0; r < a.n; r += 64) s += (double)p[(int64_t)r * a.D];
   acc[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x < 16) {
-    double t = 0.0;
-    for (int i = 0; i < 16; ++i) t += acc[16 * i + threadIdx.x];
-    out[c] = (float)t;
+  for (int half = 512; half >= 16; half >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < half) acc[threadIdx.x] += acc[threadIdx.x + half];
   }
+  if (threadIdx.x < 16) out[c] = (float)acc[threadIdx.x];
 }
 
 }  // namespace
@@ -377,7 +365,7 @@ hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_rope_backward(const RopeArgs& a, int bf16, hipStream_t st) {
-  const dim3 grid((unsigned)a.wgs), block(ROPE_NT);
+  const dim3 grid((unsigned)a.wgs, 2), block(ROPE_NT);
   if (bf16) {
     if (a.pairs) hipLaunchKernelGGL((k_rope_bwd<u16, true>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_rope_bwd<u16, false>), grid, block, 0, st, a);
@@ -389,7 +377,7 @@ hipError_t launch_rope_backward(const RopeArgs& a, int bf16, hipStream_t st) {
 }
 
 hipError_t launch_rope_dw(const RopeDwArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(k_rope_dw, dim3(a.D / 16, 2), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_rope_dw, dim3(a.D / 16, 2), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
