@@ -57,8 +57,12 @@ void k_window_attention(AttnArgs a) {
   __shared__ __attribute__((aligned(1024))) char st0[ATT_STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[ATT_STAGE];
   const int id = xcd_block(blockIdx.x, a.total);
-  const int qb = id % a.qblocks, bh = id / a.qblocks;
-  const int h = bh % a.heads, b = bh / a.heads;
+  // uniform values that come out of vector arithmetic (the divisions) go back to scalar
+  // registers: a buffer resource made of vector registers takes a loop over the lanes for
+  // every load
+  const int qb = __builtin_amdgcn_readfirstlane(id % a.qblocks);
+  const int bh = __builtin_amdgcn_readfirstlane(id / a.qblocks);
+  const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
   const int lane = threadIdx.x & 63, hl = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int T = a.T, W = a.window;
@@ -79,6 +83,8 @@ void k_window_attention(AttnArgs a) {
     lo_t = (t / W) * W;
     hi_t = (int)min<int64_t>(T, (int64_t)lo_t + W);
   }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
   if (t >= T) lo_t = hi_t = 0;   // padding rows: every key masked, nothing stored
   const int len_t = hi_t - lo_t;
   const int nsteps = (hi - lo + ATT_KV - 1) / ATT_KV;
@@ -97,6 +103,8 @@ void k_window_attention(AttnArgs a) {
       in_lo = (wl / W) * W;
       in_hi = (int)min<int64_t>(T, ((int64_t)(w0 / W) + 1) * W);
     }
+    in_lo = __builtin_amdgcn_readfirstlane(in_lo);
+    in_hi = __builtin_amdgcn_readfirstlane(in_hi);
   }
 
   const int64_t row0 = (int64_t)b * T;

@@ -25,46 +25,60 @@ constexpr int WB_TILE = WB_ROWS * ATT_D * 2;   // bytes
 // distinct banks, so that both ways of reading it are free of conflicts.
 __device__ __forceinline__ int wb_swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 
+// Loads of a tile, straight into LDS: 16 rows at a time, the lanes' places in them the same for
+// each 16 (the swizzle depends on the row's number within them).
 struct WbLoad {
-  uint32_t off[4];
+  uint32_t off;
   int slice;
   __device__ __forceinline__ void init(int64_t ld) {
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int p = c * 256 + tid, r = p >> 4;
-      off[c] = (uint32_t)(r * (ld * 2)) + (uint32_t)(((p & 15) ^ wb_swz(r)) << 4);
-    }
+    const int tid = threadIdx.x, r = tid >> 4;
+    off = (uint32_t)(r * (ld * 2)) + (uint32_t)(((tid & 15) ^ wb_swz(r)) << 4);
     slice = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
   }
   // rows [r0, r0 + 64) of a matrix of T rows at base; rows past T read as 0
   __device__ __forceinline__ void issue(char* tile, const u16* base, int64_t ld, int r0, int T) const {
-    const uint32_t nrec = (uint32_t)max(0, min(T - r0, WB_ROWS)) * (uint32_t)(ld * 2);
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(base + (int64_t)r0 * ld), (short)0, (int)nrec, 0x00020000);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) dma16(rs, (lds_void_t*)(tile + c * 4096 + slice), off[c]);
+    for (int c = 0; c < 4; ++c) {
+      const int r = r0 + 16 * c;
+      const int rows = __builtin_amdgcn_readfirstlane(max(0, min(T - r, 16)));   // one clamp: vector
+      const uint32_t nrec = (uint32_t)rows * (uint32_t)(ld * 2);
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(base + (int64_t)r * ld), (short)0, (int)nrec, 0x00020000);
+      dma16(rs, (lds_void_t*)(tile + c * 4096 + slice), off);
+    }
   }
 };
 
+// Offsets of a lane's fragments in a tile.  Every fragment's offset is one of two bases with a
+// constant added (rows) and one xored in (chunks).
+struct WbAt {
+  int row;   // along the rows: row lane % 32, dims 8 (lane / 32) .. + 7
+  int col;   // along the columns: dims 16 (g & 1) + 4 (j & 3) .. + 3 of row 4 (g / 2) + j / 4
+  __device__ __forceinline__ void init() {
+    const int lane = threadIdx.x & 63, r = lane & 31;
+    const int g = lane >> 4, j = lane & 15;
+    row = r * (ATT_D * 2) + (((lane >> 5) ^ wb_swz(r)) << 4);
+    const int m = 16 * (g & 1) + 4 * (j & 3), rc = 4 * (g >> 1) + (j >> 2);
+    col = rc * (ATT_D * 2) + (((m >> 3) ^ wb_swz(rc)) << 4) + (m & 7) * 2;
+  }
+  // Keeps the compiler from holding every fragment's offset in a register of its own across
+  // the loop (an xor per read instead): with them the second kernel spills.
+  __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(row), "+v"(col)); }
+};
+
 // Fragment along the rows: row row_base + lane % 32, dims 16 s + 8 (lane / 32) .. + 7.
-__device__ __forceinline__ bf16x8 wb_row(const char* tile, int row_base, int s) {
-  const int lane = threadIdx.x & 63;
-  const int r = row_base + (lane & 31), ch = 2 * s + (lane >> 5);
-  return *reinterpret_cast<const bf16x8*>(tile + r * (ATT_D * 2) + ((ch ^ wb_swz(r)) << 4));
+// row_base a multiple of 32.
+__device__ __forceinline__ bf16x8 wb_row(const char* tile, const WbAt& at, int row_base, int s) {
+  return *reinterpret_cast<const bf16x8*>(tile + row_base * (ATT_D * 2) + (at.row ^ (s << 5)));
 }
 // Fragment along the columns: dim dim_base + lane % 32, rows row_base + 4 (lane / 32) + (0..3)
-// and + 8.
-__device__ __forceinline__ bf16x8 wb_col(const char* tile, int dim_base, int row_base) {
-  const int lane = threadIdx.x & 63;
-  const int g = lane >> 4, j = lane & 15;
-  const int m = dim_base + 16 * (g & 1) + 4 * (j & 3);
-  const int r0 = row_base + 4 * (g >> 1) + (j >> 2);
+// and + 8.  dim_base a multiple of 32, row_base of 16; 8 rows further the swizzle has bit 1 of
+// the chunk turned.
+__device__ __forceinline__ bf16x8 wb_col(const char* tile, const WbAt& at, int dim_base, int row_base) {
   s16x4 x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = r0 + 8 * i;
-    const char* p = tile + r * (ATT_D * 2) + (((m >> 3) ^ wb_swz(r)) << 4) + (m & 7) * 2;
+    const char* p = tile + (row_base + 8 * i) * (ATT_D * 2) + (at.col ^ (dim_base << 1) ^ (i << 5));
     x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
   }
   typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -103,8 +117,9 @@ void k_window_dq(AttnBwdArgs a) {
   __shared__ __attribute__((aligned(1024))) char st0[2 * WB_TILE];
   __shared__ __attribute__((aligned(1024))) char st1[2 * WB_TILE];
   const int id = xcd_block(blockIdx.x, a.total);
-  const int qb = id % a.blocks, bh = id / a.blocks;
-  const int h = bh % a.heads, b = bh / a.heads;
+  const int qb = __builtin_amdgcn_readfirstlane(id % a.blocks);
+  const int bh = __builtin_amdgcn_readfirstlane(id / a.blocks);
+  const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
   const int lane = threadIdx.x & 63, hl = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int T = a.T, W = a.window;
@@ -129,6 +144,12 @@ void k_window_dq(AttnBwdArgs a) {
     in_lo = (wl / W) * W;
     in_hi = (int)min<int64_t>(T, ((int64_t)(w0 / W) + 1) * W);
   }
+  // uniform values that come out of vector arithmetic (the divisions), back in scalar registers:
+  // a buffer resource made of vector registers takes a loop over the lanes for every load
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  in_lo = __builtin_amdgcn_readfirstlane(in_lo);
+  in_hi = __builtin_amdgcn_readfirstlane(in_hi);
   if (t >= T) lo_t = hi_t = 0;
   if (w0 >= T) {
     in_lo = 1;
@@ -161,12 +182,14 @@ void k_window_dq(AttnBwdArgs a) {
     }
     delta += __shfl_xor(delta, 32);
     if (t < T) {
-      const int64_t at = ((int64_t)b * a.heads + h) * T + t;
-      lse2 = a.lse[at] * 1.44269504088896341f;
-      if (hl == 0) a.delta[at] = delta;
+      const int64_t i = ((int64_t)b * a.heads + h) * T + t;
+      lse2 = a.lse[i] * 1.44269504088896341f;
+      if (hl == 0) a.delta[i] = delta;
     }
   }
 
+  WbAt at;
+  at.init();
   f32x16 dq[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dq[i] = f32x16{};
@@ -181,9 +204,9 @@ void k_window_dq(AttnBwdArgs a) {
     for (int kt = 0; kt < 2; ++kt) {
       f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, 32 * kt, x), qf[x], s);
+      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 32 * kt, x), qf[x], s);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(cur + WB_TILE, 32 * kt, x), gf[x], dp);
+      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(cur + WB_TILE, at, 32 * kt, x), gf[x], dp);
       if (edge) {
         const int base = kv0 + 32 * kt + 4 * hl - lo_t;
 #pragma unroll
@@ -200,7 +223,7 @@ void k_window_dq(AttnBwdArgs a) {
         }
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          dq[d] = wb_mma(wb_col(cur, 32 * d, 32 * kt + 16 * sp), ds, dq[d]);
+          dq[d] = wb_mma(wb_col(cur, at, 32 * d, 32 * kt + 16 * sp), ds, dq[d]);
       }
     }
     __builtin_amdgcn_s_waitcnt(0);
@@ -225,8 +248,9 @@ void k_window_dkv(AttnBwdArgs a) {
   __shared__ __attribute__((aligned(1024))) char st0[WB_STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[WB_STAGE];
   const int id = xcd_block(blockIdx.x, a.total);
-  const int kb = id % a.blocks, bh = id / a.blocks;
-  const int h = bh % a.heads, b = bh / a.heads;
+  const int kb = __builtin_amdgcn_readfirstlane(id % a.blocks);
+  const int bh = __builtin_amdgcn_readfirstlane(id / a.blocks);
+  const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
   const int lane = threadIdx.x & 63, hl = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int T = a.T, W = a.window;
@@ -235,6 +259,7 @@ void k_window_dkv(AttnBwdArgs a) {
 
   // queries the workgroup visits, the lane's own [lo_j, hi_j), and for the wave the range that
   // sees all of its keys (no mask) and the one that sees any
+  auto uniform = [](int x) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(x); };
   auto first = [&](int x) __attribute__((always_inline)) {
     return a.mode == TTT_WINDOW_SLIDING ? x : (x / W) * W;
   };
@@ -243,17 +268,17 @@ void k_window_dkv(AttnBwdArgs a) {
                                                              : ((int64_t)(x / W) + 1) * W);
   };
   const int klast = min(k0 + 128, T) - 1, wl = min(w0 + 31, T - 1);
-  const int lo = first(k0), hi = end(klast);
+  const int lo = uniform(first(k0)), hi = uniform(end(klast));
   int lo_j = 0, hi_j = 0, in_lo = 1, in_hi = 0, any_lo = 0, any_hi = 0;
   if (j < T) {
     lo_j = first(j);
     hi_j = end(j);
   }
   if (w0 < T) {
-    in_lo = first(wl);
-    in_hi = end(w0);
-    any_lo = first(w0);
-    any_hi = end(wl);
+    in_lo = uniform(first(wl));
+    in_hi = uniform(end(w0));
+    any_lo = uniform(first(w0));
+    any_hi = uniform(end(wl));
   }
   const int len_j = hi_j - lo_j;
   const int nsteps = (hi - lo + WB_ROWS - 1) / WB_ROWS;
@@ -271,7 +296,7 @@ void k_window_dkv(AttnBwdArgs a) {
     lg.issue(st + WB_TILE, gb, a.lddo, t0, T);
     if (w < 2) {
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)((w ? db : lb) + t0), (short)0, max(0, min(T - t0, WB_ROWS)) * 4, 0x00020000);
+          (void*)((w ? db : lb) + t0), (short)0, min(T - t0, WB_ROWS) * 4, 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * WB_TILE + w * WB_ROWS * 4),
                                                4, lane * 4, 0, 0, 0);
     }
@@ -281,6 +306,8 @@ void k_window_dkv(AttnBwdArgs a) {
   bf16x8 kf[8], vf[8];
   wb_frags(kf, a.k + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
   wb_frags(vf, a.v + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
+  WbAt at;
+  at.init();
   f32x16 dk[4], dv[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dk[i] = dv[i] = f32x16{};
@@ -294,10 +321,11 @@ void k_window_dkv(AttnBwdArgs a) {
     for (int qt = 0; qt < 2; ++qt) {
       const int tq = t0 + 32 * qt;
       if (tq + 32 <= any_lo || tq >= any_hi) continue;   // wave-uniform
+      at.fresh();
       const bool edge = tq < in_lo || tq + 32 > in_hi;
       f32x16 s = f32x16{};
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, 32 * qt, x), kf[x], s);
+      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 32 * qt, x), kf[x], s);
       if (edge) {
         const int base = tq + 4 * hl - lo_j;
 #pragma unroll
@@ -320,10 +348,10 @@ void k_window_dkv(AttnBwdArgs a) {
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          dv[d] = wb_mma(wb_col(gt, 32 * d, 32 * qt + 16 * sp), pf[sp], dv[d]);
+          dv[d] = wb_mma(wb_col(gt, at, 32 * d, 32 * qt + 16 * sp), pf[sp], dv[d]);
       f32x16 dp = f32x16{};
 #pragma unroll
-      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, 32 * qt, x), vf[x], dp);
+      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, at, 32 * qt, x), vf[x], dp);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4 d4 = *reinterpret_cast<const f32x4*>(ls + WB_ROWS + 32 * qt + 8 * g + 4 * hl);
@@ -337,7 +365,7 @@ void k_window_dkv(AttnBwdArgs a) {
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          dk[d] = wb_mma(wb_col(cur, 32 * d, 32 * qt + 16 * sp), pf[sp], dk[d]);
+          dk[d] = wb_mma(wb_col(cur, at, 32 * d, 32 * qt + 16 * sp), pf[sp], dk[d]);
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
@@ -351,9 +379,9 @@ void k_window_dkv(AttnBwdArgs a) {
   }
   if (i < nsteps) step(st0, st1, i);
   if (j < T) {
-    const int64_t at = (row0 + j) * a.ldd + (int64_t)h * ATT_D;
-    wb_store(a.dk + at, dk, a.scale, hl);
-    wb_store(a.dv + at, dv, 1.f, hl);
+    const int64_t i0 = (row0 + j) * a.ldd + (int64_t)h * ATT_D;
+    wb_store(a.dk + i0, dk, a.scale, hl);
+    wb_store(a.dv + i0, dv, 1.f, hl);
   }
 }
 
