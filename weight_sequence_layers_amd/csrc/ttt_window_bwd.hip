@@ -35,10 +35,11 @@ struct WbLoad {
     off = (uint32_t)(r * (ld * 2)) + (uint32_t)(((tid & 15) ^ wb_swz(r)) << 4);
     slice = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
   }
-  // rows [r0, r0 + 64) of a matrix of T rows at base; rows past T read as 0
+  // rows [r0, r0 + ROWS) of a matrix of T rows at base; rows past T read as 0
+  template <int ROWS>
   __device__ __forceinline__ void issue(char* tile, const u16* base, int64_t ld, int r0, int T) const {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < ROWS / 16; ++c) {
       const int r = r0 + 16 * c;
       const int rows = __builtin_amdgcn_readfirstlane(max(0, min(T - r, 16)));   // one clamp: vector
       const uint32_t nrec = (uint32_t)rows * (uint32_t)(ld * 2);
@@ -89,6 +90,11 @@ __device__ __forceinline__ bf16x8 wb_col(const char* tile, const WbAt& at, int d
 __device__ __forceinline__ f32x16 wb_mma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+
+// Orders the instructions of a stretch of straight-line code: n of a kind next.  Left alone the
+// compiler loads each fragment right before its product and waits for LDS every time.
+#define WB_ORDER(kind, n) __builtin_amdgcn_sched_group_barrier(kind, n, 0)
+constexpr int WB_VALU = 0x2, WB_MFMA = 0x8, WB_DS = 0x100;
 
 // a row's 64 values of this lane: dims 16 s + 8 hl .. + 7
 __device__ __forceinline__ void wb_frags(bf16x8 (&f)[8], const u16* row, int hl, bool in) {
@@ -163,8 +169,8 @@ void k_window_dq(AttnBwdArgs a) {
   const u16* vb = a.v + row0 * a.ld + (int64_t)h * ATT_D;
   WbLoad lk;
   lk.init(a.ld);
-  lk.issue(st0, kb, a.ld, lo, T);
-  lk.issue(st0 + WB_TILE, vb, a.ld, lo, T);
+  lk.issue<WB_ROWS>(st0, kb, a.ld, lo, T);
+  lk.issue<WB_ROWS>(st0 + WB_TILE, vb, a.ld, lo, T);
 
   bf16x8 qf[8], gf[8];
   wb_frags(qf, a.q + (row0 + t) * a.ld + (int64_t)h * ATT_D, hl, t < T);
@@ -196,36 +202,85 @@ void k_window_dq(AttnBwdArgs a) {
   auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
     const int kv0 = lo + i * WB_ROWS;
     if (i + 1 < nsteps) {
-      lk.issue(nxt, kb, a.ld, kv0 + WB_ROWS, T);
-      lk.issue(nxt + WB_TILE, vb, a.ld, kv0 + WB_ROWS, T);
+      lk.issue<WB_ROWS>(nxt, kb, a.ld, kv0 + WB_ROWS, T);
+      lk.issue<WB_ROWS>(nxt + WB_TILE, vb, a.ld, kv0 + WB_ROWS, T);
     }
+    // The step's two halves run one behind the other, a half's exponentials beside the other's
+    // products, in one stretch of straight-line code: the mask enters as the scores' first
+    // summand.
     const bool edge = kv0 < in_lo || kv0 + WB_ROWS > in_hi;
+    f32x16 s[2], dp[2];
+    bf16x8 ds[2][2];
+    if (edge) {
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      f32x16 s = f32x16{}, dp = f32x16{};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 32 * kt, x), qf[x], s);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(cur + WB_TILE, at, 32 * kt, x), gf[x], dp);
-      if (edge) {
+      for (int kt = 0; kt < 2; ++kt) {
         const int base = kv0 + 32 * kt + 4 * hl - lo_t;
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          if ((unsigned)(base + 8 * (v >> 2) + (v & 3)) >= (unsigned)len_t) s[v] = -INFINITY;
+          s[kt][v] = (unsigned)(base + 8 * (v >> 2) + (v & 3)) < (unsigned)len_t ? 0.f : -INFINITY;
       }
+    } else {
+      s[0] = s[1] = f32x16{};
+    }
+    auto scores = [&](int kt) __attribute__((always_inline)) {
+      dp[kt] = f32x16{};
 #pragma unroll
-      for (int sp = 0; sp < 2; ++sp) {
-        bf16x8 ds;
+      for (int x = 0; x < 8; ++x) s[kt] = wb_mma(wb_row(cur, at, 32 * kt, x), qf[x], s[kt]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p = __builtin_amdgcn_exp2f(fmaf(s[8 * sp + e], a.scale2, -lse2));
-          ds[e] = static_cast<__bf16>(p * (dp[8 * sp + e] - delta));
-        }
+      for (int x = 0; x < 8; ++x) dp[kt] = wb_mma(wb_row(cur + WB_TILE, at, 32 * kt, x), gf[x], dp[kt]);
+    };
+    auto probs = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[kt][v], a.scale2, -lse2));
+        ds[kt][v >> 3][v & 7] = static_cast<__bf16>(p * (dp[kt][v] - delta));
+      }
+    };
+    auto add = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+      for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          dq[d] = wb_mma(wb_col(cur, at, 32 * d, 32 * kt + 16 * sp), ds, dq[d]);
-      }
+          dq[d] = wb_mma(wb_col(cur, at, 32 * d, 32 * kt + 16 * sp), ds[kt][sp], dq[d]);
+    };
+    scores(0);
+    WB_ORDER(WB_DS, 4);
+#pragma unroll
+    for (int x = 0; x < 12; ++x) {
+      WB_ORDER(WB_MFMA, 1);
+      WB_ORDER(WB_DS, 1);
     }
+    WB_ORDER(WB_MFMA, 4);
+    scores(1);
+    probs(0);
+    WB_ORDER(WB_DS, 4);
+#pragma unroll
+    for (int x = 0; x < 12; ++x) {
+      WB_ORDER(WB_MFMA, 1);
+      WB_ORDER(WB_VALU, 7);
+      WB_ORDER(WB_DS, 1);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      WB_ORDER(WB_MFMA, 1);
+      WB_ORDER(WB_VALU, 7);
+    }
+    add(0);
+    probs(1);
+    add(1);
+    WB_ORDER(WB_DS, 6);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      WB_ORDER(WB_MFMA, 1);
+      WB_ORDER(WB_VALU, 13);
+      WB_ORDER(WB_DS, 2);
+    }
+#pragma unroll
+    for (int x = 0; x < 5; ++x) {
+      WB_ORDER(WB_MFMA, 1);
+      WB_ORDER(WB_DS, 2);
+    }
+    WB_ORDER(WB_MFMA, 3);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
   };
@@ -240,13 +295,18 @@ void k_window_dq(AttnBwdArgs a) {
   if (t < T) wb_store(a.dq + (row0 + t) * a.ldd + (int64_t)h * ATT_D, dq, a.scale, hl);
 }
 
-// LDS of a stage: the tiles of q and dout, then their 64 rows' lse and delta
-constexpr int WB_STAGE = 2 * WB_TILE + 2 * WB_ROWS * 4;
+// The second kernel's queries come 32 at a time: a stage is the tiles of q and dout, then the
+// rows' lse and delta (64 places each: a load of a wave).  Its 128 rows of v stay in LDS: with k
+// and v both in registers beside the two sums it spills.
+constexpr int WB_QROWS = 32, WB_QTILE = WB_QROWS * ATT_D * 2;
+constexpr int WB_STAGE = 2 * WB_QTILE + 2 * 64 * 4;
+constexpr int WB_VTILE = 128 * ATT_D * 2;
 
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void k_window_dkv(AttnBwdArgs a) {
   __shared__ __attribute__((aligned(1024))) char st0[WB_STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[WB_STAGE];
+  __shared__ __attribute__((aligned(1024))) char vt[WB_VTILE];
   const int id = xcd_block(blockIdx.x, a.total);
   const int kb = __builtin_amdgcn_readfirstlane(id % a.blocks);
   const int bh = __builtin_amdgcn_readfirstlane(id / a.blocks);
@@ -281,7 +341,7 @@ void k_window_dkv(AttnBwdArgs a) {
     any_hi = uniform(end(wl));
   }
   const int len_j = hi_j - lo_j;
-  const int nsteps = (hi - lo + WB_ROWS - 1) / WB_ROWS;
+  const int nsteps = (hi - lo + WB_QROWS - 1) / WB_QROWS;
 
   const int64_t row0 = (int64_t)b * T;
   const u16* qb = a.q + row0 * a.ld + (int64_t)h * ATT_D;
@@ -292,51 +352,53 @@ void k_window_dkv(AttnBwdArgs a) {
   lq.init(a.ld);
   lg.init(a.lddo);
   auto issue = [&](char* st, int t0) __attribute__((always_inline)) {
-    lq.issue(st, qb, a.ld, t0, T);
-    lg.issue(st + WB_TILE, gb, a.lddo, t0, T);
+    lq.issue<WB_QROWS>(st, qb, a.ld, t0, T);
+    lg.issue<WB_QROWS>(st + WB_QTILE, gb, a.lddo, t0, T);
     if (w < 2) {
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)((w ? db : lb) + t0), (short)0, min(T - t0, WB_ROWS) * 4, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * WB_TILE + w * WB_ROWS * 4),
-                                               4, lane * 4, 0, 0, 0);
+          (void*)((w ? db : lb) + t0), (short)0, min(T - t0, WB_QROWS) * 4, 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * WB_QTILE + w * 64 * 4), 4,
+                                               lane * 4, 0, 0, 0);
     }
   };
+  lq.issue<128>(vt, a.v + row0 * a.ld + (int64_t)h * ATT_D, a.ld, k0, T);
   issue(st0, lo);
 
-  bf16x8 kf[8], vf[8];
+  bf16x8 kf[8];
   wb_frags(kf, a.k + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
-  wb_frags(vf, a.v + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
   WbAt at;
   at.init();
+  const char* vw = vt + 32 * w * (ATT_D * 2);   // the wave's rows of v
   f32x16 dk[4], dv[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dk[i] = dv[i] = f32x16{};
 
   auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
-    const int t0 = lo + i * WB_ROWS;
-    if (i + 1 < nsteps) issue(nxt, t0 + WB_ROWS);
-    const char* gt = cur + WB_TILE;
-    const float* ls = reinterpret_cast<const float*>(cur + 2 * WB_TILE);
-#pragma unroll
-    for (int qt = 0; qt < 2; ++qt) {
-      const int tq = t0 + 32 * qt;
-      if (tq + 32 <= any_lo || tq >= any_hi) continue;   // wave-uniform
+    const int tq = lo + i * WB_QROWS;
+    if (i + 1 < nsteps) issue(nxt, tq + WB_QROWS);
+    const char* gt = cur + WB_QTILE;
+    const float* ls = reinterpret_cast<const float*>(cur + 2 * WB_QTILE);
+    if (tq + 32 > any_lo && tq < any_hi) {   // wave-uniform: some query here sees some key
       at.fresh();
-      const bool edge = tq < in_lo || tq + 32 > in_hi;
-      f32x16 s = f32x16{};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 32 * qt, x), kf[x], s);
-      if (edge) {
+      f32x16 s, dp = f32x16{};
+      if (tq < in_lo || tq + 32 > in_hi) {   // the mask as the scores' first summand
         const int base = tq + 4 * hl - lo_j;
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          if ((unsigned)(base + 8 * (v >> 2) + (v & 3)) >= (unsigned)len_j) s[v] = -INFINITY;
+          s[v] = (unsigned)(base + 8 * (v >> 2) + (v & 3)) < (unsigned)len_j ? 0.f : -INFINITY;
+      } else {
+        s = f32x16{};
       }
+      // the exponentials run beside the second product, the differences beside the third
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 0, x), kf[x], s);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, at, 0, x), wb_row(vw, at, 0, x), dp);
       // element v: query tq + 8 (v / 4) + 4 hl + v % 4
-      bf16x8 pf[2];
+      bf16x8 pf[2], df[2];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + 32 * qt + 8 * g + 4 * hl);
+        const f32x4 l4 = *reinterpret_cast<const f32x4*>(ls + 8 * g + 4 * hl);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int v = 4 * g + e;
@@ -347,25 +409,31 @@ void k_window_dkv(AttnBwdArgs a) {
 #pragma unroll
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          dv[d] = wb_mma(wb_col(gt, at, 32 * d, 32 * qt + 16 * sp), pf[sp], dv[d]);
-      f32x16 dp = f32x16{};
-#pragma unroll
-      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, at, 32 * qt, x), vf[x], dp);
+        for (int d = 0; d < 4; ++d) dv[d] = wb_mma(wb_col(gt, at, 32 * d, 16 * sp), pf[sp], dv[d]);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const f32x4 d4 = *reinterpret_cast<const f32x4*>(ls + WB_ROWS + 32 * qt + 8 * g + 4 * hl);
+        const f32x4 d4 = *reinterpret_cast<const f32x4*>(ls + 64 + 8 * g + 4 * hl);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int v = 4 * g + e;
-          pf[v >> 3][v & 7] = static_cast<__bf16>(s[v] * (dp[v] - d4[e]));
+          df[v >> 3][v & 7] = static_cast<__bf16>(s[v] * (dp[v] - d4[e]));
         }
       }
 #pragma unroll
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          dk[d] = wb_mma(wb_col(cur, at, 32 * d, 32 * qt + 16 * sp), pf[sp], dk[d]);
+        for (int d = 0; d < 4; ++d) dk[d] = wb_mma(wb_col(cur, at, 32 * d, 16 * sp), df[sp], dk[d]);
+      WB_ORDER(WB_DS, 3);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_DS, 1);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_DS, 2);
+      }
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
