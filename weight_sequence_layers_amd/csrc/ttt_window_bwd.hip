@@ -25,28 +25,25 @@ constexpr int WB_TILE = WB_ROWS * ATT_D * 2;   // bytes
 // distinct banks, so that both ways of reading it are free of conflicts.
 __device__ __forceinline__ int wb_swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 
-// Loads of a tile, straight into LDS: 16 rows at a time, the lanes' places in them the same for
-// each 16 (the swizzle depends on the row's number within them).
+// Loads of a tile, straight into LDS, 16 rows at a time: the lanes' places in them are the same
+// each time (the swizzle depends on a row's number modulo 16).
 struct WbLoad {
-  uint32_t off;
+  uint32_t off, ld2;   // byte offset of the lane's place, bytes of a row
   int slice;
   __device__ __forceinline__ void init(int64_t ld) {
     const int tid = threadIdx.x, r = tid >> 4;
-    off = (uint32_t)(r * (ld * 2)) + (uint32_t)(((tid & 15) ^ wb_swz(r)) << 4);
+    ld2 = (uint32_t)(ld * 2);
+    off = (uint32_t)r * ld2 + (uint32_t)(((tid & 15) ^ wb_swz(r)) << 4);
     slice = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
   }
-  // rows [r0, r0 + ROWS) of a matrix of T rows at base; rows past T read as 0
+  // ROWS rows at p, of which the first `rows` (> 0) are there: the others read as 0
   template <int ROWS>
-  __device__ __forceinline__ void issue(char* tile, const u16* base, int64_t ld, int r0, int T) const {
+  __device__ __forceinline__ void issue(char* tile, const u16* p, int rows) const {
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)p, (short)0, (int)((uint32_t)min(rows, ROWS) * ld2), 0x00020000);
 #pragma unroll
-    for (int c = 0; c < ROWS / 16; ++c) {
-      const int r = r0 + 16 * c;
-      const int rows = __builtin_amdgcn_readfirstlane(max(0, min(T - r, 16)));   // one clamp: vector
-      const uint32_t nrec = (uint32_t)rows * (uint32_t)(ld * 2);
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(base + (int64_t)r * ld), (short)0, (int)nrec, 0x00020000);
-      dma16(rs, (lds_void_t*)(tile + c * 4096 + slice), off);
-    }
+    for (int c = 0; c < ROWS / 16; ++c)
+      dma16(rs, (lds_void_t*)(tile + c * 4096 + slice), off + c * 16 * ld2);
   }
 };
 
@@ -62,9 +59,6 @@ struct WbAt {
     const int m = 16 * (g & 1) + 4 * (j & 3), rc = 4 * (g >> 1) + (j >> 2);
     col = rc * (ATT_D * 2) + (((m >> 3) ^ wb_swz(rc)) << 4) + (m & 7) * 2;
   }
-  // Keeps the compiler from holding every fragment's offset in a register of its own across
-  // the loop (an xor per read instead): with them the second kernel spills.
-  __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(row), "+v"(col)); }
 };
 
 // Fragment along the rows: row row_base + lane % 32, dims 16 s + 8 (lane / 32) .. + 7.
@@ -169,8 +163,15 @@ void k_window_dq(AttnBwdArgs a) {
   const u16* vb = a.v + row0 * a.ld + (int64_t)h * ATT_D;
   WbLoad lk;
   lk.init(a.ld);
-  lk.issue<WB_ROWS>(st0, kb, a.ld, lo, T);
-  lk.issue<WB_ROWS>(st0 + WB_TILE, vb, a.ld, lo, T);
+  const u16 *kp = kb + (int64_t)lo * a.ld, *vp = vb + (int64_t)lo * a.ld;   // the next step's rows
+  const int64_t adv = WB_ROWS * a.ld;
+  auto issue = [&](char* st, int rows) __attribute__((always_inline)) {
+    lk.issue<WB_ROWS>(st, kp, rows);
+    lk.issue<WB_ROWS>(st + WB_TILE, vp, rows);
+    kp += adv;
+    vp += adv;
+  };
+  issue(st0, T - lo);
 
   bf16x8 qf[8], gf[8];
   wb_frags(qf, a.q + (row0 + t) * a.ld + (int64_t)h * ATT_D, hl, t < T);
@@ -201,10 +202,7 @@ void k_window_dq(AttnBwdArgs a) {
   for (int i = 0; i < 4; ++i) dq[i] = f32x16{};
   auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
     const int kv0 = lo + i * WB_ROWS;
-    if (i + 1 < nsteps) {
-      lk.issue<WB_ROWS>(nxt, kb, a.ld, kv0 + WB_ROWS, T);
-      lk.issue<WB_ROWS>(nxt + WB_TILE, vb, a.ld, kv0 + WB_ROWS, T);
-    }
+    if (i + 1 < nsteps) issue(nxt, T - kv0 - WB_ROWS);
     // The step's two halves run one behind the other, a half's exponentials beside the other's
     // products, in one stretch of straight-line code: the mask enters as the scores' first
     // summand.
@@ -351,18 +349,24 @@ void k_window_dkv(AttnBwdArgs a) {
   WbLoad lq, lg;
   lq.init(a.ld);
   lg.init(a.lddo);
-  auto issue = [&](char* st, int t0) __attribute__((always_inline)) {
-    lq.issue<WB_QROWS>(st, qb, a.ld, t0, T);
-    lg.issue<WB_QROWS>(st + WB_QTILE, gb, a.lddo, t0, T);
+  const u16 *qp = qb + (int64_t)lo * a.ld, *gp = gb + (int64_t)lo * a.lddo;   // the next step's rows
+  const float* sp0 = (w ? db : lb) + lo;
+  const int64_t advq = WB_QROWS * a.ld, advg = WB_QROWS * a.lddo;
+  auto issue = [&](char* st, int rows) __attribute__((always_inline)) {
+    lq.issue<WB_QROWS>(st, qp, rows);
+    lg.issue<WB_QROWS>(st + WB_QTILE, gp, rows);
     if (w < 2) {
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)((w ? db : lb) + t0), (short)0, min(T - t0, WB_QROWS) * 4, 0x00020000);
+          (void*)sp0, (short)0, min(rows, WB_QROWS) * 4, 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * WB_QTILE + w * 64 * 4), 4,
                                                lane * 4, 0, 0, 0);
     }
+    qp += advq;
+    gp += advg;
+    sp0 += WB_QROWS;
   };
-  lq.issue<128>(vt, a.v + row0 * a.ld + (int64_t)h * ATT_D, a.ld, k0, T);
-  issue(st0, lo);
+  lq.issue<128>(vt, a.v + (row0 + k0) * a.ld + (int64_t)h * ATT_D, T - k0);
+  issue(st0, T - lo);
 
   bf16x8 kf[8];
   wb_frags(kf, a.k + (row0 + j) * a.ld + (int64_t)h * ATT_D, hl, j < T);
@@ -375,11 +379,10 @@ void k_window_dkv(AttnBwdArgs a) {
 
   auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
     const int tq = lo + i * WB_QROWS;
-    if (i + 1 < nsteps) issue(nxt, tq + WB_QROWS);
+    if (i + 1 < nsteps) issue(nxt, T - tq - WB_QROWS);
     const char* gt = cur + WB_QTILE;
     const float* ls = reinterpret_cast<const float*>(cur + 2 * WB_QTILE);
     if (tq + 32 > any_lo && tq < any_hi) {   // wave-uniform: some query here sees some key
-      at.fresh();
       f32x16 s, dp = f32x16{};
       if (tq < in_lo || tq + 32 > in_hi) {   // the mask as the scores' first summand
         const int base = tq + 4 * hl - lo_j;
@@ -389,9 +392,11 @@ void k_window_dkv(AttnBwdArgs a) {
       } else {
         s = f32x16{};
       }
-      // the exponentials run beside the second product, the differences beside the third
+      // The exponentials run beside the second product, the differences beside the third; a wave
+      // past its scores goes before the SIMD's other one, so that the two stay apart (631 -> 602 us).
 #pragma unroll
       for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 0, x), kf[x], s);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, at, 0, x), wb_row(vw, at, 0, x), dp);
       // element v: query tq + 8 (v / 4) + 4 hl + v % 4
@@ -423,16 +428,12 @@ void k_window_dkv(AttnBwdArgs a) {
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
         for (int d = 0; d < 4; ++d) dk[d] = wb_mma(wb_col(cur, at, 32 * d, 16 * sp), df[sp], dk[d]);
+      __builtin_amdgcn_s_setprio(0);
       WB_ORDER(WB_DS, 3);
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         WB_ORDER(WB_MFMA, 1);
         WB_ORDER(WB_DS, 1);
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        WB_ORDER(WB_MFMA, 1);
-        WB_ORDER(WB_DS, 2);
       }
     }
     __builtin_amdgcn_s_waitcnt(0);
