@@ -191,7 +191,9 @@ ttt_status ttt_window_attention_lse(const void* q, const void* k, const void* v,
  *   p = exp(scale q k - lse),  dp = dout . v,  ds = p (dp - dout . out)
  *   dq = scale sum ds k,   dk = scale sum ds q,   dv = sum p dout
  * bf16, rows of dq, dk and dv as q's with stride ld_d (they may be thirds of one buffer).
- * Scores, exponentials and sums are fp32; p and ds are rounded to bf16 for their products.
+ * (dout . out, where no row sees more than 64 tokens, is summed as p dp: there the rounding of
+ * out would weigh).  Scores, exponentials and sums are fp32; p and ds are rounded to bf16 for
+ * their products.
  * Every sum has one order: the results are the same from run to run.  work: fp32
  * [batch][heads][seq_len] workspace.  The gradients and work may not overlap the inputs or
  * each other.  All values must be finite.  Limits as for ttt_window_attention, ld_dout

@@ -21,7 +21,8 @@ e4m3 2^-4 and 2^-10 below its normal range); U = 2^-24 that of fp32 arithmetic.
   the rounded out (2^-8 sum |dout out|), fp32 parts below 2^-14 of the absolute sums:
   |dv - ref| <= H |ref| + (2^-8 + 2^-14) sum p |dout|,
   |dq - ref| <= H |ref| + scale sum_j (2^-8 |ds_j| + p_j (2^-8 e + 2^-14 (|dp_j| + e))) |k_j|
-  with e = sum |dout out|, dk the same over queries.
+  with e = sum |dout out|, dk the same over queries; the term 2^-8 e falls away where no row
+  sees more than 64 tokens (delta is then summed as p dp).
 """
 import numpy as np
 import pytest
@@ -597,7 +598,9 @@ class Window:
                 dP = dO @ V.T
                 dS = P * (dP - np.sum(P * dP, 1, keepdims=True))
                 e = np.sum(np.abs(dO * O), 1, keepdims=True)
-                es = sc * (2.0 ** -8 * np.abs(dS) + P * (2.0 ** -8 * e + 2.0 ** -14 * (np.abs(dP) + e)))
+                # where no row sees more than 64 tokens delta does not come from the rounded out
+                eo = 0 if min(self.window, T) <= 64 else 2.0 ** -8
+                es = sc * (2.0 ** -8 * np.abs(dS) + P * (eo * e + 2.0 ** -14 * (np.abs(dP) + e)))
                 refs = oa.window_attention_vjp(Q, K, V, dO, self.window, self.mode)
                 bars = es @ np.abs(K), es.T @ np.abs(Q), (2.0 ** -8 + 2.0 ** -14) * (P.T @ np.abs(dO))
                 for i, n in enumerate(("dq", "dk", "dv")):

@@ -541,7 +541,7 @@ ttt_status ttt_window_attention_backward(const void* q, const void* k, const voi
   a.ldd = ld_d;
   a.T = (int32_t)seq_len;
   a.heads = heads;
-  a.window = window;
+  a.window = (int32_t)std::min<int64_t>(window, seq_len);   // no row sees more
   a.mode = window_mode;
   a.blocks = (int32_t)((seq_len + 127) / 128);
   a.total = a.blocks * heads * batch;

@@ -112,6 +112,12 @@ __device__ __forceinline__ void wb_store(u16* row, const f32x16 (&o)[4], float f
     }
 }
 
+// SUM: delta summed from p and dp in a walk of its own over the keys instead of from dout and
+// out.  The rounding of out to bf16 moves delta by 2^-9 of |dout| |out|, which counts where a
+// window holds few tokens and out is as long as they are: with it the gradients of a window of
+// 2 are 1.7 times as far off as their own rounding alone, with the sum 1.4 times, as those of
+// long windows are.  For windows of at most one step's keys, where the walk is short.
+template <bool SUM>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void k_window_dq(AttnBwdArgs a) {
   __shared__ __attribute__((aligned(1024))) char st0[2 * WB_TILE];
@@ -177,7 +183,9 @@ void k_window_dq(AttnBwdArgs a) {
   wb_frags(qf, a.q + (row0 + t) * a.ld + (int64_t)h * ATT_D, hl, t < T);
   wb_frags(gf, a.dout + (row0 + t) * a.lddo + (int64_t)h * ATT_D, hl, t < T);
   float delta = 0.f, lse2 = 0.f;
-  {
+  const int64_t stat = ((int64_t)b * a.heads + h) * T + t;   // the row's place in lse and delta
+  if (t < T) lse2 = a.lse[stat] * 1.44269504088896341f;
+  if constexpr (!SUM) {
     const u16* orow = a.out + (row0 + t) * a.ldo + (int64_t)h * ATT_D;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
@@ -188,11 +196,6 @@ void k_window_dq(AttnBwdArgs a) {
         delta = fmaf(static_cast<float>(x[e]), static_cast<float>(gf[s][e]), delta);
     }
     delta += __shfl_xor(delta, 32);
-    if (t < T) {
-      const int64_t i = ((int64_t)b * a.heads + h) * T + t;
-      lse2 = a.lse[i] * 1.44269504088896341f;
-      if (hl == 0) a.delta[i] = delta;
-    }
   }
 
   WbAt at;
@@ -200,9 +203,47 @@ void k_window_dq(AttnBwdArgs a) {
   f32x16 dq[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dq[i] = f32x16{};
-  auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
-    const int kv0 = lo + i * WB_ROWS;
-    if (i + 1 < nsteps) issue(nxt, T - kv0 - WB_ROWS);
+  // Walks over the steps, each one's tiles loaded during the one before (the first's before the
+  // call).
+  auto walk = [&](auto work) __attribute__((always_inline)) {
+    auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
+      if (i + 1 < nsteps) issue(nxt, T - lo - (i + 1) * WB_ROWS);
+      work(cur, lo + i * WB_ROWS);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+    };
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    int i = 0;
+    for (; i + 1 < nsteps; i += 2) {
+      step(st0, st1, i);
+      step(st1, st0, i + 1);
+    }
+    if (i < nsteps) step(st0, st1, i);
+  };
+  if constexpr (SUM) {
+    walk([&](const char* cur, int kv0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        f32x16 s = f32x16{}, dp = f32x16{};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 32 * kt, x), qf[x], s);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(cur + WB_TILE, at, 32 * kt, x), gf[x], dp);
+        const int base = kv0 + 32 * kt + 4 * hl - lo_t;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          if ((unsigned)(base + 8 * (v >> 2) + (v & 3)) < (unsigned)len_t)
+            delta = fmaf(__builtin_amdgcn_exp2f(fmaf(s[v], a.scale2, -lse2)), dp[v], delta);
+      }
+    });
+    delta += __shfl_xor(delta, 32);
+    kp = kb + (int64_t)lo * a.ld;
+    vp = vb + (int64_t)lo * a.ld;
+    issue(st0, T - lo);
+  }
+  if (t < T && hl == 0) a.delta[stat] = delta;
+  walk([&](const char* cur, int kv0) __attribute__((always_inline)) {
     // The step's two halves run one behind the other, a half's exponentials beside the other's
     // products, in one stretch of straight-line code: the mask enters as the scores' first
     // summand.
@@ -279,17 +320,7 @@ void k_window_dq(AttnBwdArgs a) {
       WB_ORDER(WB_DS, 2);
     }
     WB_ORDER(WB_MFMA, 3);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-  };
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  int i = 0;
-  for (; i + 1 < nsteps; i += 2) {
-    step(st0, st1, i);
-    step(st1, st0, i + 1);
-  }
-  if (i < nsteps) step(st0, st1, i);
+  });
   if (t < T) wb_store(a.dq + (row0 + t) * a.ldd + (int64_t)h * ATT_D, dq, a.scale, hl);
 }
 
@@ -458,7 +489,8 @@ void k_window_dkv(AttnBwdArgs a) {
 
 hipError_t launch_window_bwd(const AttnBwdArgs& a, hipStream_t st) {
   if (a.total == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_window_dq, dim3(a.total), dim3(256), 0, st, a);
+  if (a.window <= WB_ROWS) hipLaunchKernelGGL(k_window_dq<true>, dim3(a.total), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(k_window_dq<false>, dim3(a.total), dim3(256), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_window_dkv, dim3(a.total), dim3(256), 0, st, a);
