@@ -73,7 +73,7 @@ ttt_status ttt_validate_rope_config(const ttt_rope_config* cfg);
  *   freq     fp32 [axes][rot_dim / 2], radians per position: a pair that turns with one axis
  *            holds zeros for the others (may be NULL with rot_dim 0)
  *   pos      int32 [axes][tokens] (may be NULL with rot_dim 0)
- * Limits: 0 <= tokens < 2^31; every ld at least heads * head_dim, at most 2^28 and such
+ * Limits: 0 <= tokens <= 2^25; every ld at least heads * head_dim, at most 2^28 and such
  * that rows stay 16-byte aligned.  tokens 0 does nothing.
  */
 ttt_status ttt_qk_norm_rope(const ttt_rope_config* cfg, const void* q, int64_t ld_q,
@@ -157,10 +157,11 @@ ttt_status ttt_qk_norm_rope_append(const ttt_rope_config* cfg, const void* q, in
  *   lse      fp32 [seqs][heads] or NULL: the log of the sum of the exponentials
  * A length below 0 counts as 0, one above max_pages * page_size as that.  Tokens whose page
  * number lies outside [0, pages) are left out.  A sequence with no token left gets out 0 and
- * lse -inf.  Places of a page past the sequence's end may hold anything, NaN too.
- * heads a multiple of kv_heads, at most 65536; head_dim 64, 128 or 256; 0 <= seqs <= 2^20;
- * max_pages >= 0, max_pages * page_size <= 2^30; window >= 0; scale 0 selects
- * 1 / sqrt(head_dim), otherwise finite and > 0.  out may not overlap q or the cache.
+ * lse -inf.  Places of a page past the sequence's end may hold anything, NaN too; an infinite
+ * value within it gives NaN.
+ * heads a multiple of kv_heads, at most 65536; head_dim 64, 128 or 256; 0 <= seqs <= 2^20,
+ * seqs * heads below 2^24; max_pages >= 0, max_pages * page_size <= 2^30; window >= 0; scale 0
+ * selects 1 / sqrt(head_dim), otherwise finite and > 0.  out may not overlap q or the cache.
  * Scores, softmax and sums are fp32; the probabilities enter the product with v as two bf16
  * numbers each (16 significant bits), so out is rounded once.
  * work: workspace of the size ttt_paged_attention_work gives for the same cache sizes, seqs,

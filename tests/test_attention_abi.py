@@ -53,7 +53,7 @@ def forward(cfg=None, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(tokens=-1), 2), (dict(tokens=1 << 31), 2), (dict(ld_q=248), 2), (dict(ld_k=127), 2),
+    (dict(tokens=-1), 2), (dict(tokens=(1 << 25) + 1), 2), (dict(tokens=1 << 31), 2), (dict(ld_q=248), 2), (dict(ld_k=127), 2),
     (dict(ld_qo=255), 2), (dict(ld_ko=132), 2), (dict(ld_q=(1 << 28) + 8), 2), (dict(q=None), 1),
     (dict(k=None), 1), (dict(qo=None), 1), (dict(ko=None), 1), (dict(freq=None), 1), (dict(pos=None), 1),
     (dict(q=P(0, 2)), 9), (dict(kw=P(3, 8)), 9), (dict(pos=P(5, 4)), 9), (dict(tokens=0, q=None), 0),
@@ -157,7 +157,7 @@ def test_paged_cache(kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(seqs=-1), 2), (dict(seqs=(1 << 20) + 1), 2), (dict(heads=3), 2), (dict(heads=0), 2),
-    (dict(heads=65538), 2), (dict(max_pages=-1), 2), (dict(max_pages=(1 << 26) + 1), 2), (dict(window=-1), 2),
+    (dict(heads=65538), 2), (dict(seqs=1 << 20, heads=16), 2), (dict(max_pages=-1), 2), (dict(max_pages=(1 << 26) + 1), 2), (dict(window=-1), 2),
     (dict(scale=-1.0), 4), (dict(scale=float("nan")), 4), (dict(scale=float("inf")), 4), (dict(ld_q=128), 2),
     (dict(ld_out=260), 2), (dict(q=None), 1), (dict(out=None), 1), (dict(lens=None), 1), (dict(table=None), 1),
     (dict(lse=P(4, 4)), 9), (dict(out=P(0)), 4), (dict(seqs=0, q=None), 0),

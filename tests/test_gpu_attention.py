@@ -267,6 +267,30 @@ def test_no_tokens_give_zero_scale_gradients():
     assert bool((a == 0).all()) and bool((b == 0).all())
 
 
+def test_norm_rope_backward_replayed():
+    r = Rope(T=3001, Hq=3, Hk=1, D=64, rot=64)
+    work = torch.empty(W.ttt_qk_norm_rope_backward_work(r.cfg, r.T), dtype=torch.uint8, device=DEV)
+    g = torch.cuda.CUDAGraph()
+    gq, gk = (torch.randn(r.T, n * r.D, generator=gen(3), device=DEV).to(r.dt) for n in (r.Hq, r.Hk))
+    dq, dk, a, b = torch.empty_like(gq), torch.empty_like(gk), torch.empty(64, device=DEV), torch.empty(64, device=DEV)
+
+    def call():
+        W.ttt_qk_norm_rope_backward(r.cfg, r.q, r.ld, r.k, r.ld, r.qw, r.kw, r.freq, r.pos, gq, r.Hq * r.D, gk,
+                                    r.Hk * r.D, dq, r.Hq * r.D, dk, r.Hk * r.D, a, b, work, r.T)
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (dq, dk, a, b)]
+    with torch.cuda.graph(g):
+        call()
+    for _ in range(3):
+        for t in (dq, dk, a, b):
+            t.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, (dq, dk, a, b)))
+        torch.randn(1000, device=DEV).sum().item()
+
+
 def test_norm_rope_backward_is_the_same_every_time():
     r = Rope(T=30011, Hq=3, Hk=1, D=64, rot=64)
     first = rope_backward(r)
@@ -481,6 +505,45 @@ def test_paged_attention_bad_pages_and_lengths():
     p.call()
     p.check()
     assert bool((p.out[2, :512] == 0).all()) and bool((p.lse[2] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("n", [50, 3000])
+def test_paged_attention_keeps_nan_to_what_sees_it(n):
+    """A NaN key reaches the query heads that share it (out and lse), a NaN value one element of
+    them; other heads and sequences are as without."""
+    p = Paged([n, 60], 4, 2, 128, 16)
+    p.call()
+    torch.cuda.synchronize()
+    clean, lse = p.out.clone(), p.lse.clone()
+    p.k[int(p.table[0, 1]), 1, 3, 7] = float("nan")      # heads 2 and 3 of sequence 0
+    p.v[int(p.table[1, 0]), 0, 2, 9] = float("nan")      # element 9 of heads 0 and 1 of sequence 1
+    p.call()
+    torch.cuda.synchronize()
+    assert bool(p.out[0, 256:512].isnan().all()) and bool(p.lse[0, 2:].isnan().all())
+    assert bool(p.out[1, 9].isnan()) and bool(p.out[1, 128 + 9].isnan())
+    p.out[0, 256:512], p.lse[0, 2:] = clean[0, 256:512], lse[0, 2:]
+    p.out[1, 9], p.out[1, 128 + 9] = clean[1, 9], clean[1, 128 + 9]
+    assert torch.equal(p.out, clean) and torch.equal(p.lse, lse)
+
+
+def test_paged_attention_one_long_sequence_among_short_ones():
+    p = Paged([20000] + [40] * 20, 4, 1, 128, 64)
+    p.call()
+    p.check()
+
+
+def test_two_streams_with_a_workspace_each():
+    """Two decoding calls in flight at once, each on its own stream with its own workspace, ten
+    times over."""
+    ps = [Paged([3000, 700], 4, 2, 128, 16, seed=s) for s in (21, 22)]
+    works = [p.work() for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, w, s in zip(ps, works, streams):
+            p.call(work=w, stream=s)
+    for p in ps:
+        p.check()
 
 
 def test_paged_attention_two_sequences_share_pages():
@@ -769,8 +832,9 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(W.TTTError) as e:
             call(**kw)
         assert e.value.status == code, kw
-    with pytest.raises(W.TTTError):
-        W.make_kv_cache(torch.zeros(2, 1, 4, 64, device=DEV), torch.zeros(2, 1, 4, 64, device=DEV))
+    for shape, dt in (((2, 1, 4, 64), torch.float32), ((0, 1, 4, 64), torch.bfloat16), ((2, 4, 64), torch.bfloat16)):
+        with pytest.raises(W.TTTError):
+            W.make_kv_cache(torch.zeros(shape, device=DEV, dtype=dt), torch.zeros(shape, device=DEV, dtype=dt))
     x = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
     W.make_kv_cache(x, x)      # one head: the same memory order
     x = torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device=DEV).transpose(1, 2)

@@ -555,8 +555,8 @@ def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
                           "dtype and layout")
     dev = torch.cuda.current_device()
     pages, heads, size, dim = k.shape
-    if not k[0].is_contiguous():
-        raise TTTError(2, "a page must be contiguous")
+    if pages < 1 or not k[0].is_contiguous():
+        raise TTTError(2, "at least one page, and each contiguous")
     dtypes = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
     if k.dtype not in dtypes:
         raise TTTError(3, f"cache of {k.dtype}: bfloat16 or float8_e4m3fn")

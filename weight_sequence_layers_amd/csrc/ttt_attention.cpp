@@ -14,7 +14,6 @@ using namespace ttt;
 
 namespace {
 
-constexpr int64_t INT31 = (int64_t)1 << 31;
 constexpr int64_t LD_MAX = (int64_t)1 << 28;   // keeps every byte offset within int64
 
 // A matrix of `rows` rows of `width` bytes, `ld` bytes apart.
@@ -58,9 +57,11 @@ ttt_status check_rope(const ttt_rope_config* c) {
 
 int act_size(const ttt_rope_config* c) { return c->act == TTT_BF16 ? 2 : 4; }
 
+// at most 2^23 workgroups of 256 threads (a block is at least 4 tokens for so many): a launch's
+// threads are counted in 32 bits
 ttt_status check_tokens(int64_t tokens) {
-  if (tokens < 0 || tokens >= INT31)
-    return failf(TTT_E_SHAPE, "tokens %lld out of range", (long long)tokens);
+  if (tokens < 0 || tokens > ((int64_t)1 << 25))
+    return failf(TTT_E_SHAPE, "tokens %lld: in [0, 2^25]", (long long)tokens);
   return TTT_OK;
 }
 
@@ -194,6 +195,9 @@ ttt_status paged_plan(const ttt_kv_cache* c, int32_t seqs, int32_t heads, int32_
   if (seqs < 0 || seqs > (1 << 20)) return failf(TTT_E_SHAPE, "seqs %d: in [0, 2^20]", seqs);
   if (heads < 1 || heads > 65536 || heads % c->kv_heads)
     return failf(TTT_E_SHAPE, "heads %d: a multiple of kv_heads %d in [1, 65536]", heads, c->kv_heads);
+  // the join's threads, 256 to a row, are counted in 32 bits
+  if ((int64_t)seqs * heads >= ((int64_t)1 << 24))
+    return failf(TTT_E_SHAPE, "seqs * heads %lld: below 2^24", (long long)seqs * heads);
   if (max_pages < 0 || (int64_t)max_pages * c->page_size > ((int64_t)1 << 30))
     return failf(TTT_E_SHAPE, "max_pages %d of %d tokens: at most 2^30 tokens", max_pages, c->page_size);
   if (window < 0) return failf(TTT_E_SHAPE, "window %d < 0", window);
@@ -203,8 +207,6 @@ ttt_status paged_plan(const ttt_kv_cache* c, int32_t seqs, int32_t heads, int32_
   if (window) span = std::min<int64_t>(span, window);
   p->splits = paged_splits((int64_t)seqs * c->kv_heads * p->htiles, span,
                            paged_per_cu(c->head_dim, c->dtype == TTT_CACHE_E4M3));
-  if ((int64_t)seqs * heads * p->splits >= INT31)
-    return failf(TTT_E_SHAPE, "seqs * heads too large");
   const int64_t parts = p->splits > 1 ? (int64_t)seqs * heads * p->splits : 0;
   p->sums = parts * c->head_dim * (int64_t)sizeof(float);
   p->bytes = p->sums + parts * 2 * (int64_t)sizeof(float);

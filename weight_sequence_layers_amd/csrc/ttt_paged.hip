@@ -277,13 +277,13 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
     }
     const int64_t head = (int64_t)kh * a.group + h0 + h;
     if (whole) {
-      const float inv = ll > 0.f ? vsc / ll : 0.f;
+      const float inv = ll == 0.f ? 0.f : vsc / ll;   // no token: zeros; a NaN stays one
       uint2 r;
       r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
       r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
       *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + head * D + d) = r;
       if (d == 0 && a.lse)
-        a.lse[(int64_t)seq * a.heads + head] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+        a.lse[(int64_t)seq * a.heads + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
     } else {
       const int64_t at = ((int64_t)seq * a.heads + head) * a.splits + sp;
       *reinterpret_cast<f32x4*>(a.po + at * D + d) = acc;
@@ -345,13 +345,13 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
     for (int v = 0; v < 4; ++v) acc[v] += f * ox[v];
   }
   const float vsc = a.vs ? a.vs[head / a.group] : 1.f;
-  const float inv = lt > 0.f ? vsc / lt : 0.f;
+  const float inv = lt == 0.f ? 0.f : vsc / lt;
   uint2 r;
   r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
   r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
   *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + (int64_t)head * D + d) = r;
   if (d == 0 && a.lse)
-    a.lse[id] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    a.lse[id] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
 }
 
 template <int D>
