@@ -8,7 +8,7 @@
 #include <cmath>
 
 #include "ttt_attention_internal.h"
-#include "ttt_host.h"
+#include "ttt_block_host.h"
 
 using namespace ttt;
 

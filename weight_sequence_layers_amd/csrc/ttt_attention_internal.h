@@ -1,5 +1,5 @@
 // Internal interface between the attention host code (ttt_attention.cpp) and its kernels
-// (ttt_rope.hip, ttt_paged.hip, ttt_window_bwd.hip).  Not part of the public ABI.
+// (ttt_attention_*.hip).  Not part of the public ABI.
 #pragma once
 
 #include "ttt_attention.h"

@@ -10,7 +10,7 @@
 #include <new>
 
 #include "ttt_block_internal.h"
-#include "ttt_host.h"
+#include "ttt_block_host.h"
 
 using namespace ttt;
 

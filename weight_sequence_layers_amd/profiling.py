@@ -53,11 +53,14 @@ STAGE_KERNELS = [
 
 def source_digest(part: str = "layer") -> str:
     """Hash of the kernel sources: part "layer" covers every file under csrc/ that the TTT
-    layer is built from, "block" the files of the block around it (ttt_block*)."""
+    layer is built from, "block" the files of the block around it (ttt_block*), "attention"
+    those of the attention calls (ttt_attention*)."""
     h = hashlib.sha256()
     csrc = os.path.join(PKG, "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.startswith("ttt_block") != (part == "block"):
+        own = ("block" if f.startswith("ttt_block") else
+               "attention" if f.startswith("ttt_attention") else "layer")
+        if own != part:
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
