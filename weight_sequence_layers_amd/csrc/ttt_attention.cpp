@@ -545,11 +545,9 @@ ttt_status ttt_window_attention_backward(const void* q, const void* k, const voi
   a.heads = heads;
   a.window = (int32_t)std::min<int64_t>(window, seq_len);   // no row sees more
   a.mode = window_mode;
-  a.blocks = (int32_t)((seq_len + 127) / 128);
-  a.total = a.blocks * heads * batch;
   a.scale = (float)(1.0 / std::sqrt((double)ATT_D));
   a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)ATT_D));
-  BLK_HIP(launch_window_bwd(a, static_cast<hipStream_t>(stream)));
+  BLK_HIP(launch_window_bwd(a, (int64_t)batch * heads, static_cast<hipStream_t>(stream)));
   return TTT_OK;
 }
 

@@ -125,6 +125,7 @@ struct AttnBwdArgs {
   float scale, scale2;   // 1 / sqrt(ATT_D), and times log2(e)
 };
 
-hipError_t launch_window_bwd(const AttnBwdArgs& a, hipStream_t st);
+// problems: batch * heads; blocks and total are filled in here
+hipError_t launch_window_bwd(AttnBwdArgs a, int64_t problems, hipStream_t st);
 
 }  // namespace ttt

@@ -19,6 +19,7 @@ namespace {
 
 constexpr int WB_ROWS = 64;                    // rows of a tile
 constexpr int WB_TILE = WB_ROWS * ATT_D * 2;   // bytes
+constexpr int64_t WB_FEW = 256;                // workgroups: one per CU
 
 // A tile keeps chunk c (16 bytes) of row r at chunk c ^ wb_swz(r) of the row: any 16
 // consecutive rows at one chunk, and the two chunks of 32 dims over 4 consecutive rows, lie on
@@ -112,14 +113,42 @@ __device__ __forceinline__ void wb_store(u16* row, const f32x16 (&o)[4], float f
     }
 }
 
+// The second halves' sums added to the first halves' (waves w and w + 2 hold the same rows),
+// 32 KB through buf.  Call from every wave.
+__device__ __forceinline__ void wb_join(f32x16 (&o)[4], int w, int half, char* buf) {
+  const int lane = threadIdx.x & 63;
+  __syncthreads();   // buf has been read
+  auto at = [&](int d, int v) __attribute__((always_inline)) {
+    return reinterpret_cast<float*>(buf) + ((w * 4 + d) * 16 + v) * 64 + lane;
+  };
+  if (half)
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) *at(d, v) = o[d][v];
+  __syncthreads();
+  if (!half)
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) o[d][v] += *at(d, v);
+}
+
+// NH 1: the four waves take 32 rows each, 128 to a workgroup.  NH 2, for launches that leave CUs
+// idle (at most WB_FEW workgroups of 64 rows): 64 rows to a workgroup and two waves to each 32,
+// which take half of every step's tile and are joined at the end: twice the workgroups, and
+// half the products in each SIMD's chain of steps, which is what such a launch waits for (one
+// head of 1024 tokens: dq 29 -> 20 us, dk and dv 42 -> 26; eight waves over 128 rows gain nothing).
+//
 // SUM: delta summed from p and dp in a walk of its own over the keys instead of from dout and
 // out.  The rounding of out to bf16 moves delta by 2^-9 of |dout| |out|, which counts where a
 // window holds few tokens and out is as long as they are: with it the gradients of a window of
 // 2 are 1.7 times as far off as their own rounding alone, with the sum 1.4 times, as those of
 // long windows are.  For windows of at most one step's keys, where the walk is short.
-template <bool SUM>
+template <bool SUM, int NH>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void k_window_dq(AttnBwdArgs a) {
+  constexpr int RG = 4 / NH, QB = 32 * RG;   // row groups, queries of a workgroup
   __shared__ __attribute__((aligned(1024))) char st0[2 * WB_TILE];
   __shared__ __attribute__((aligned(1024))) char st1[2 * WB_TILE];
   const int id = xcd_block(blockIdx.x, a.total);
@@ -127,13 +156,14 @@ void k_window_dq(AttnBwdArgs a) {
   const int bh = __builtin_amdgcn_readfirstlane(id / a.blocks);
   const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
   const int lane = threadIdx.x & 63, hl = lane >> 5;
-  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int w = wave % RG, half = wave / RG;
   const int T = a.T, W = a.window;
-  const int q0 = qb * 128, w0 = q0 + 32 * w;
+  const int q0 = qb * QB, w0 = q0 + 32 * w;
   const int t = w0 + (lane & 31);
 
   // keys the workgroup visits, the lane's own [lo_t, hi_t), and the range that needs no mask
-  const int qlast = min(q0 + 128, T) - 1, wl = min(w0 + 31, T - 1);
+  const int qlast = min(q0 + QB, T) - 1, wl = min(w0 + 31, T - 1);
   int lo, hi, lo_t, hi_t, in_lo, in_hi;
   if (a.mode == TTT_WINDOW_SLIDING) {
     lo = max(0, q0 - W + 1);
@@ -224,7 +254,8 @@ void k_window_dq(AttnBwdArgs a) {
   if constexpr (SUM) {
     walk([&](const char* cur, int kv0) __attribute__((always_inline)) {
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
+      for (int kh = 0; kh < 2 / NH; ++kh) {
+        const int kt = NH == 1 ? kh : half;
         f32x16 s = f32x16{}, dp = f32x16{};
 #pragma unroll
         for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 32 * kt, x), qf[x], s);
@@ -238,35 +269,45 @@ void k_window_dq(AttnBwdArgs a) {
       }
     });
     delta += __shfl_xor(delta, 32);
+    if constexpr (NH == 2) {   // the halves' sums
+      float* sum = reinterpret_cast<float*>(st1);
+      if (lane < 32) sum[32 * wave + lane] = delta;
+      __syncthreads();
+      delta = sum[32 * w + (lane & 31)] + sum[32 * (w + RG) + (lane & 31)];
+      __syncthreads();
+    }
     kp = kb + (int64_t)lo * a.ld;
     vp = vb + (int64_t)lo * a.ld;
     issue(st0, T - lo);
   }
-  if (t < T && hl == 0) a.delta[stat] = delta;
+  if (t < T && hl == 0 && half == 0) a.delta[stat] = delta;
   walk([&](const char* cur, int kv0) __attribute__((always_inline)) {
     // The step's two halves run one behind the other, a half's exponentials beside the other's
     // products, in one stretch of straight-line code: the mask enters as the scores' first
     // summand.
     const bool edge = kv0 < in_lo || kv0 + WB_ROWS > in_hi;
-    f32x16 s[2], dp[2];
-    bf16x8 ds[2][2];
+    constexpr int N = 2 / NH;                    // halves of this wave
+    const int r0 = NH == 1 ? 0 : 32 * half;      // its first row of the tile
+    f32x16 s[N], dp[N];
+    bf16x8 ds[N][2];
+#pragma unroll
+    for (int kt = 0; kt < N; ++kt) s[kt] = f32x16{};
     if (edge) {
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        const int base = kv0 + 32 * kt + 4 * hl - lo_t;
+      for (int kt = 0; kt < N; ++kt) {
+        const int base = kv0 + r0 + 32 * kt + 4 * hl - lo_t;
 #pragma unroll
         for (int v = 0; v < 16; ++v)
           s[kt][v] = (unsigned)(base + 8 * (v >> 2) + (v & 3)) < (unsigned)len_t ? 0.f : -INFINITY;
       }
-    } else {
-      s[0] = s[1] = f32x16{};
     }
     auto scores = [&](int kt) __attribute__((always_inline)) {
       dp[kt] = f32x16{};
+      const int row = r0 + 32 * kt;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s[kt] = wb_mma(wb_row(cur, at, 32 * kt, x), qf[x], s[kt]);
+      for (int x = 0; x < 8; ++x) s[kt] = wb_mma(wb_row(cur, at, row, x), qf[x], s[kt]);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) dp[kt] = wb_mma(wb_row(cur + WB_TILE, at, 32 * kt, x), gf[x], dp[kt]);
+      for (int x = 0; x < 8; ++x) dp[kt] = wb_mma(wb_row(cur + WB_TILE, at, row, x), gf[x], dp[kt]);
     };
     auto probs = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
@@ -280,7 +321,7 @@ void k_window_dq(AttnBwdArgs a) {
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
         for (int d = 0; d < 4; ++d)
-          dq[d] = wb_mma(wb_col(cur, at, 32 * d, 32 * kt + 16 * sp), ds[kt][sp], dq[d]);
+          dq[d] = wb_mma(wb_col(cur, at, 32 * d, r0 + 32 * kt + 16 * sp), ds[kt][sp], dq[d]);
     };
     scores(0);
     WB_ORDER(WB_DS, 4);
@@ -290,60 +331,74 @@ void k_window_dq(AttnBwdArgs a) {
       WB_ORDER(WB_DS, 1);
     }
     WB_ORDER(WB_MFMA, 4);
-    scores(1);
-    probs(0);
-    WB_ORDER(WB_DS, 4);
+    if constexpr (NH == 2) {
+      probs(0);
+      add(0);
+    } else {
+      scores(1);
+      probs(0);
+      WB_ORDER(WB_DS, 4);
 #pragma unroll
-    for (int x = 0; x < 12; ++x) {
-      WB_ORDER(WB_MFMA, 1);
-      WB_ORDER(WB_VALU, 7);
-      WB_ORDER(WB_DS, 1);
-    }
+      for (int x = 0; x < 12; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_VALU, 7);
+        WB_ORDER(WB_DS, 1);
+      }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      WB_ORDER(WB_MFMA, 1);
-      WB_ORDER(WB_VALU, 7);
-    }
-    add(0);
-    probs(1);
-    add(1);
-    WB_ORDER(WB_DS, 6);
+      for (int x = 0; x < 4; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_VALU, 7);
+      }
+      add(0);
+      probs(1);
+      add(1);
+      WB_ORDER(WB_DS, 6);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      WB_ORDER(WB_MFMA, 1);
-      WB_ORDER(WB_VALU, 13);
-      WB_ORDER(WB_DS, 2);
-    }
+      for (int x = 0; x < 8; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_VALU, 13);
+        WB_ORDER(WB_DS, 2);
+      }
 #pragma unroll
-    for (int x = 0; x < 5; ++x) {
-      WB_ORDER(WB_MFMA, 1);
-      WB_ORDER(WB_DS, 2);
+      for (int x = 0; x < 5; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_DS, 2);
+      }
+      WB_ORDER(WB_MFMA, 3);
     }
-    WB_ORDER(WB_MFMA, 3);
   });
+  if constexpr (NH == 2) {
+    wb_join(dq, w, half, st0);
+    if (half) return;
+  }
   if (t < T) wb_store(a.dq + (row0 + t) * a.ldd + (int64_t)h * ATT_D, dq, a.scale, hl);
 }
 
-// The second kernel's queries come 32 at a time: a stage is the tiles of q and dout, then the
-// rows' lse and delta (64 places each: a load of a wave).  Its 128 rows of v stay in LDS: with k
-// and v both in registers beside the two sums it spills.
-constexpr int WB_QROWS = 32, WB_QTILE = WB_QROWS * ATT_D * 2;
-constexpr int WB_STAGE = 2 * WB_QTILE + 2 * 64 * 4;
-constexpr int WB_VTILE = 128 * ATT_D * 2;
+// The second kernel's queries come 32 for each half at a time: a stage is the tiles of q and
+// dout, then the rows' lse and delta (64 places each: a load of a wave).  The workgroup's rows of
+// v stay in LDS: with k and v both in registers beside the two sums it spills.
+template <int NH>
+struct WbStage {
+  static constexpr int ROWS = 32 * NH, TILE = ROWS * ATT_D * 2, BYTES = 2 * TILE + 2 * 64 * 4;
+};
 
+template <int NH>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void k_window_dkv(AttnBwdArgs a) {
-  __shared__ __attribute__((aligned(1024))) char st0[WB_STAGE];
-  __shared__ __attribute__((aligned(1024))) char st1[WB_STAGE];
-  __shared__ __attribute__((aligned(1024))) char vt[WB_VTILE];
+  constexpr int RG = 4 / NH, KB = 32 * RG;   // row groups, keys of a workgroup
+  constexpr int QROWS = WbStage<NH>::ROWS, QTILE = WbStage<NH>::TILE;
+  __shared__ __attribute__((aligned(1024))) char st0[WbStage<NH>::BYTES];
+  __shared__ __attribute__((aligned(1024))) char st1[WbStage<NH>::BYTES];
+  __shared__ __attribute__((aligned(1024))) char vt[KB * ATT_D * 2];
   const int id = xcd_block(blockIdx.x, a.total);
   const int kb = __builtin_amdgcn_readfirstlane(id % a.blocks);
   const int bh = __builtin_amdgcn_readfirstlane(id / a.blocks);
   const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
   const int lane = threadIdx.x & 63, hl = lane >> 5;
-  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int w = wave % RG, half = wave / RG;
   const int T = a.T, W = a.window;
-  const int k0 = kb * 128, w0 = k0 + 32 * w;
+  const int k0 = kb * KB, w0 = k0 + 32 * w;
   const int j = w0 + (lane & 31);
 
   // queries the workgroup visits, the lane's own [lo_j, hi_j), and for the wave the range that
@@ -356,7 +411,7 @@ void k_window_dkv(AttnBwdArgs a) {
     return (int)min<int64_t>(T, a.mode == TTT_WINDOW_SLIDING ? (int64_t)x + W
                                                              : ((int64_t)(x / W) + 1) * W);
   };
-  const int klast = min(k0 + 128, T) - 1, wl = min(w0 + 31, T - 1);
+  const int klast = min(k0 + KB, T) - 1, wl = min(w0 + 31, T - 1);
   const int lo = uniform(first(k0)), hi = uniform(end(klast));
   int lo_j = 0, hi_j = 0, in_lo = 1, in_hi = 0, any_lo = 0, any_hi = 0;
   if (j < T) {
@@ -370,7 +425,7 @@ void k_window_dkv(AttnBwdArgs a) {
     any_hi = uniform(end(wl));
   }
   const int len_j = hi_j - lo_j;
-  const int nsteps = (hi - lo + WB_QROWS - 1) / WB_QROWS;
+  const int nsteps = (hi - lo + QROWS - 1) / QROWS;
 
   const int64_t row0 = (int64_t)b * T;
   const u16* qb = a.q + row0 * a.ld + (int64_t)h * ATT_D;
@@ -381,22 +436,22 @@ void k_window_dkv(AttnBwdArgs a) {
   lq.init(a.ld);
   lg.init(a.lddo);
   const u16 *qp = qb + (int64_t)lo * a.ld, *gp = gb + (int64_t)lo * a.lddo;   // the next step's rows
-  const float* sp0 = (w ? db : lb) + lo;
-  const int64_t advq = WB_QROWS * a.ld, advg = WB_QROWS * a.lddo;
+  const float* sp0 = (wave ? db : lb) + lo;
+  const int64_t advq = QROWS * a.ld, advg = QROWS * a.lddo;
   auto issue = [&](char* st, int rows) __attribute__((always_inline)) {
-    lq.issue<WB_QROWS>(st, qp, rows);
-    lg.issue<WB_QROWS>(st + WB_QTILE, gp, rows);
-    if (w < 2) {
+    lq.issue<QROWS>(st, qp, rows);
+    lg.issue<QROWS>(st + QTILE, gp, rows);
+    if (wave < 2) {
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)sp0, (short)0, min(rows, WB_QROWS) * 4, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * WB_QTILE + w * 64 * 4), 4,
+          (void*)sp0, (short)0, min(rows, QROWS) * 4, 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(st + 2 * QTILE + wave * 64 * 4), 4,
                                                lane * 4, 0, 0, 0);
     }
     qp += advq;
     gp += advg;
-    sp0 += WB_QROWS;
+    sp0 += QROWS;
   };
-  lq.issue<128>(vt, a.v + (row0 + k0) * a.ld + (int64_t)h * ATT_D, T - k0);
+  lq.issue<KB>(vt, a.v + (row0 + k0) * a.ld + (int64_t)h * ATT_D, T - k0);
   issue(st0, T - lo);
 
   bf16x8 kf[8];
@@ -409,10 +464,10 @@ void k_window_dkv(AttnBwdArgs a) {
   for (int i = 0; i < 4; ++i) dk[i] = dv[i] = f32x16{};
 
   auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
-    const int tq = lo + i * WB_QROWS;
-    if (i + 1 < nsteps) issue(nxt, T - tq - WB_QROWS);
-    const char* gt = cur + WB_QTILE;
-    const float* ls = reinterpret_cast<const float*>(cur + 2 * WB_QTILE);
+    if (i + 1 < nsteps) issue(nxt, T - lo - (i + 1) * QROWS);
+    const int r0 = NH == 1 ? 0 : 32 * half, tq = lo + i * QROWS + r0;   // this wave's 32 queries
+    const char* gt = cur + QTILE;
+    const float* ls = reinterpret_cast<const float*>(cur + 2 * QTILE) + r0;
     if (tq + 32 > any_lo && tq < any_hi) {   // wave-uniform: some query here sees some key
       f32x16 s, dp = f32x16{};
       if (tq < in_lo || tq + 32 > in_hi) {   // the mask as the scores' first summand
@@ -426,10 +481,10 @@ void k_window_dkv(AttnBwdArgs a) {
       // The exponentials run beside the second product, the differences beside the third; a wave
       // past its scores goes before the SIMD's other one, so that the two stay apart (631 -> 602 us).
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, 0, x), kf[x], s);
+      for (int x = 0; x < 8; ++x) s = wb_mma(wb_row(cur, at, r0, x), kf[x], s);
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, at, 0, x), wb_row(vw, at, 0, x), dp);
+      for (int x = 0; x < 8; ++x) dp = wb_mma(wb_row(gt, at, r0, x), wb_row(vw, at, 0, x), dp);
       // element v: query tq + 8 (v / 4) + 4 hl + v % 4
       bf16x8 pf[2], df[2];
 #pragma unroll
@@ -445,7 +500,7 @@ void k_window_dkv(AttnBwdArgs a) {
 #pragma unroll
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) dv[d] = wb_mma(wb_col(gt, at, 32 * d, 16 * sp), pf[sp], dv[d]);
+        for (int d = 0; d < 4; ++d) dv[d] = wb_mma(wb_col(gt, at, 32 * d, r0 + 16 * sp), pf[sp], dv[d]);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const f32x4 d4 = *reinterpret_cast<const f32x4*>(ls + 64 + 8 * g + 4 * hl);
@@ -458,7 +513,7 @@ void k_window_dkv(AttnBwdArgs a) {
 #pragma unroll
       for (int sp = 0; sp < 2; ++sp)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) dk[d] = wb_mma(wb_col(cur, at, 32 * d, 16 * sp), df[sp], dk[d]);
+        for (int d = 0; d < 4; ++d) dk[d] = wb_mma(wb_col(cur, at, 32 * d, r0 + 16 * sp), df[sp], dk[d]);
       __builtin_amdgcn_s_setprio(0);
       WB_ORDER(WB_DS, 3);
 #pragma unroll
@@ -478,6 +533,11 @@ void k_window_dkv(AttnBwdArgs a) {
     step(st1, st0, i + 1);
   }
   if (i < nsteps) step(st0, st1, i);
+  if constexpr (NH == 2) {
+    wb_join(dk, w, half, st0);
+    wb_join(dv, w, half, st1);
+    if (half) return;
+  }
   if (j < T) {
     const int64_t i0 = (row0 + j) * a.ldd + (int64_t)h * ATT_D;
     wb_store(a.dk + i0, dk, a.scale, hl);
@@ -485,16 +545,25 @@ void k_window_dkv(AttnBwdArgs a) {
   }
 }
 
-}  // namespace
-
-hipError_t launch_window_bwd(const AttnBwdArgs& a, hipStream_t st) {
-  if (a.total == 0) return hipSuccess;
-  if (a.window <= WB_ROWS) hipLaunchKernelGGL(k_window_dq<true>, dim3(a.total), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_window_dq<false>, dim3(a.total), dim3(256), 0, st, a);
+template <int NH>
+hipError_t launch_window_bwd_nh(const AttnBwdArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)a.total), block(256);
+  if (a.window <= WB_ROWS) hipLaunchKernelGGL((k_window_dq<true, NH>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_window_dq<false, NH>), grid, block, 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_window_dkv, dim3(a.total), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_window_dkv<NH>, grid, block, 0, st, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_window_bwd(AttnBwdArgs a, int64_t problems, hipStream_t st) {
+  const int64_t small = (a.T + 63) / 64 * problems;
+  const bool few = small <= WB_FEW;
+  a.blocks = few ? (a.T + 63) / 64 : (a.T + 127) / 128;
+  a.total = (int32_t)(a.blocks * problems);
+  return few ? launch_window_bwd_nh<2>(a, st) : launch_window_bwd_nh<1>(a, st);
 }
 
 }  // namespace ttt
