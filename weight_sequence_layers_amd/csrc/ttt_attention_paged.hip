@@ -8,11 +8,16 @@
 // Every cached byte is read once: the memory bounds it.  A workgroup takes one key head of one
 // sequence, the query heads that share it (up to 16, the columns of a 16 x 16 x 32 MFMA; with
 // fewer the spare columns cost nothing that counts) and one part of the tokens; its four waves
-// take 32 tokens in turn.  Per step a wave computes S^T = K Q^T with K's fragments straight
-// from memory (a lane's 16 bytes of a key row are its fragment; which dims a fragment's k index
-// means is free as long as Q's agree), so each lane holds 8 tokens of one query head and P^T is
-// already laid out as the second product's B operand; V goes through the wave's own LDS tile,
-// read transposed.  The next step's rows are loaded into registers while this one is computed.
+// take 32 tokens in turn.  A step's rows are loaded into registers in the order they lie in
+// memory while the step before is computed, and put into the wave's own LDS tiles: K is read
+// back along its rows as the A operand of S^T = K Q^T, so each lane holds 8 tokens of one query
+// head and P^T is already laid out as the second product's B operand; V is read transposed.
+//
+// Measured: one context of 131072 tokens, 8 heads: 86 us, 6.2 TB/s of cached bytes; 64 sequences
+// up to 8192 tokens, 32 query heads on 8: 192 us, 5.7 TB/s; 96 windows of 2048 in e4m3: 37 us,
+// 4.3 TB/s (4.4 us of it the join, a few the chain length - page - row of a workgroup's start).
+// The kernels read 1.001 times the cached bytes.  K's fragments straight from memory (64 bytes
+// of a row per load) read 2 to 6 % slower than through LDS.
 #include "ttt_attention_internal.h"
 
 namespace ttt {

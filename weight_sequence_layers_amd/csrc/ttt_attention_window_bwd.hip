@@ -12,6 +12,11 @@
 // tiles of 64 rows, loaded one step ahead.  As in the forward the scores are computed
 // transposed, so that a lane's elements are the B operand of the product that follows; k (or q
 // and dout) is read from the same tile both along its rows and, transposed, along its columns.
+//
+// Measured at 32768 tokens, 8 heads, a sliding window of 2048: 432 and 580 us, 923 and 917
+// TFLOP/s of the products made (the largest library product of this card, 8192 cubed, runs at
+// 1160 to 1200): the matrix cores are busy 59 and 55 % of the time, the rest goes to the
+// exponentials and the step's loads (11 %, timed with the loads left out).
 #include "ttt_attention_internal.h"
 
 namespace ttt {
