@@ -550,23 +550,25 @@ def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
     halves of one [pages, 2, ...]); the scales are fp32 [kv_heads] or None. The tensors stay
     alive with the struct."""
     import torch
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+    shape, stride = k.shape, k.stride()
+    if len(shape) != 4 or shape != v.shape or k.dtype is not v.dtype or stride != v.stride():
         raise TTTError(2, "k and v: two tensors [pages, kv_heads, page_size, head_dim] of one "
                           "dtype and layout")
-    dev = torch.cuda.current_device()
-    pages, heads, size, dim = k.shape
-    if pages < 1 or not k[0].is_contiguous():
+    pages, heads, size, dim = shape
+    if pages < 1 or not ((stride[3] == 1 or dim == 1) and (stride[2] == dim or size == 1) and
+                         (stride[1] == size * dim or heads == 1)):
         raise TTTError(2, "at least one page, and each contiguous")
-    dtypes = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
-    if k.dtype not in dtypes:
+    if k.dtype is torch.bfloat16:
+        dtype = 0
+    elif k.dtype is torch.float8_e4m3fn:
+        dtype = 1
+    else:
         raise TTTError(3, f"cache of {k.dtype}: bfloat16 or float8_e4m3fn")
-    c = ttt_kv_cache()
-    c.k, c.v = _arg(k, "k", k.dtype, 0, dev, False), _arg(v, "v", v.dtype, 0, dev, False)
-    c.k_scale = _arg(k_scale, "k_scale", torch.float32, heads, dev)
-    c.v_scale = _arg(v_scale, "v_scale", torch.float32, heads, dev)
-    c.page_stride = k.stride(0) if pages > 1 else heads * size * dim
-    c.pages, c.page_size, c.kv_heads, c.head_dim = pages, size, heads, dim
-    c.dtype, c.reserved = dtypes[k.dtype], 0
+    dev = torch.cuda.current_device()
+    c = ttt_kv_cache(_arg(k, "k", k.dtype, 0, dev, False), _arg(v, "v", k.dtype, 0, dev, False),
+                     _arg(k_scale, "k_scale", torch.float32, heads, dev),
+                     _arg(v_scale, "v_scale", torch.float32, heads, dev),
+                     stride[0] if pages > 1 else heads * size * dim, pages, size, heads, dim, dtype, 0)
     c.tensors = (k, v, k_scale, v_scale)
     return c
 
