@@ -176,10 +176,11 @@ ttt_status ttt_paged_attention(const void* q, int64_t ld_q, const ttt_kv_cache* 
                                int64_t work_bytes, void* stream);
 
 /*
- * ttt_window_attention that also stores lse [batch][heads][seq_len] (fp32): the log of each
- * row's sum of exponentials of the scaled scores, for the backward.  out equals
- * ttt_window_attention's bit for bit.  Limits as there, and ld_out at most 2^28; out and lse
- * may not overlap the inputs or each other.
+ * The window attention of ttt_window_attention for training: also stores lse
+ * [batch][heads][seq_len] (fp32), the log of each row's sum of exponentials of the scaled scores,
+ * for the backward.  Scores, softmax and sums are fp32, the probabilities are rounded to bf16 for
+ * the product with v and summed before that.  Limits as there, and ld_out at most 2^28; out and
+ * lse may not overlap the inputs or each other.  All values must be finite.
  */
 ttt_status ttt_window_attention_lse(const void* q, const void* k, const void* v, int64_t ld,
                                     void* out, int64_t ld_out, float* lse, int32_t batch,

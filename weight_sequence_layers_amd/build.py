@@ -17,7 +17,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["ttt_kernels.hip", "ttt_backward.hip", "ttt_small.hip", "ttt_noalloc.hip",
            "ttt_ns_small.hip", "ttt_block.hip", "ttt_attention_rope.hip",
-           "ttt_attention_paged.hip", "ttt_attention_window_bwd.hip", "libttt.cpp",
+           "ttt_attention_paged.hip", "ttt_attention_window.hip", "libttt.cpp",
            "ttt_block.cpp", "ttt_attention.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

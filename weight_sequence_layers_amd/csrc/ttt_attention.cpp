@@ -213,6 +213,26 @@ ttt_status paged_plan(const ttt_kv_cache* c, int32_t seqs, int32_t heads, int32_
   return TTT_OK;
 }
 
+WindowArgs window_args(const void* q, const void* k, const void* v, int64_t ld, void* out,
+                       int64_t ld_out, float* lse, int32_t heads, int64_t T, int32_t window,
+                       int32_t mode) {
+  WindowArgs a = {};
+  a.q = static_cast<const u16*>(q);
+  a.k = static_cast<const u16*>(k);
+  a.v = static_cast<const u16*>(v);
+  a.ld = ld;
+  a.out = static_cast<u16*>(out);
+  a.ldo = ld_out;
+  a.lse = lse;
+  a.T = (int32_t)T;
+  a.heads = heads;
+  a.window = (int32_t)std::min<int64_t>(window, T);   // no row sees more
+  a.mode = mode;
+  a.scale = (float)(1.0 / std::sqrt((double)ATT_D));
+  a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)ATT_D));
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -486,9 +506,8 @@ ttt_status ttt_window_attention_lse(const void* q, const void* k, const void* v,
     if (share(ro, r) || share(rl, r)) return failf(TTT_E_CONFIG, "out or lse overlaps q, k or v");
   }
   if (share(ro, rl)) return failf(TTT_E_CONFIG, "lse overlaps out");
-  AttnArgs a = attention_args(q, k, v, ld, out, ld_out, batch, heads, seq_len, window, window_mode);
-  a.lse = lse;
-  BLK_HIP(launch_window_attention(a, static_cast<hipStream_t>(stream)));
+  WindowArgs a = window_args(q, k, v, ld, out, ld_out, lse, heads, seq_len, window, window_mode);
+  BLK_HIP(launch_window_fwd(a, (int64_t)batch * heads, static_cast<hipStream_t>(stream)));
   return TTT_OK;
 }
 
@@ -526,27 +545,15 @@ ttt_status ttt_window_attention_backward(const void* q, const void* k, const voi
     for (int j = 0; j < i; ++j)
       if (share(outs[i], outs[j])) return failf(TTT_E_CONFIG, "the gradients and work overlap");
   }
-  AttnBwdArgs a = {};
-  a.q = static_cast<const u16*>(q);
-  a.k = static_cast<const u16*>(k);
-  a.v = static_cast<const u16*>(v);
-  a.out = static_cast<const u16*>(out);
+  WindowArgs a = window_args(q, k, v, ld, const_cast<void*>(out), ld_out, const_cast<float*>(lse),
+                             heads, seq_len, window, window_mode);
   a.dout = static_cast<const u16*>(dout);
-  a.lse = lse;
+  a.lddo = ld_dout;
   a.dq = static_cast<u16*>(dq);
   a.dk = static_cast<u16*>(dk);
   a.dv = static_cast<u16*>(dv);
-  a.delta = work;
-  a.ld = ld;
-  a.ldo = ld_out;
-  a.lddo = ld_dout;
   a.ldd = ld_d;
-  a.T = (int32_t)seq_len;
-  a.heads = heads;
-  a.window = (int32_t)std::min<int64_t>(window, seq_len);   // no row sees more
-  a.mode = window_mode;
-  a.scale = (float)(1.0 / std::sqrt((double)ATT_D));
-  a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)ATT_D));
+  a.delta = work;
   BLK_HIP(launch_window_bwd(a, (int64_t)batch * heads, static_cast<hipStream_t>(stream)));
   return TTT_OK;
 }

@@ -114,18 +114,23 @@ __host__ __device__ inline int32_t paged_part(int32_t n, int32_t splits) {
   return (steps + splits - 1) / splits * PG_BLOCK;
 }
 
-// ------------------------------------------------------------------------ window backward
-struct AttnBwdArgs {
-  const u16 *q, *k, *v, *out, *dout;
-  const float* lse;
+// ------------------------------------------------------------------------ window training
+struct WindowArgs {
+  const u16 *q, *k, *v;
+  int64_t ld;
+  u16* out;              // written by the forward, read by the backward
+  int64_t ldo;
+  float* lse;
+  const u16* dout;       // backward
   u16 *dq, *dk, *dv;
   float* delta;
-  int64_t ld, ldo, lddo, ldd;
+  int64_t lddo, ldd;
   int32_t T, heads, window, mode, blocks, total;
   float scale, scale2;   // 1 / sqrt(ATT_D), and times log2(e)
 };
 
 // problems: batch * heads; blocks and total are filled in here
-hipError_t launch_window_bwd(AttnBwdArgs a, int64_t problems, hipStream_t st);
+hipError_t launch_window_fwd(WindowArgs a, int64_t problems, hipStream_t st);
+hipError_t launch_window_bwd(WindowArgs a, int64_t problems, hipStream_t st);
 
 }  // namespace ttt

@@ -1,22 +1,25 @@
-// Backward of the window attention (include/ttt_attention.h; the forward is in ttt_block.hip).
+// The window attention's training form (include/ttt_attention.h): the forward that also gives
+// each row's log-sum-exp, and the backward.
 //
 // Mathematics, with c = 1 / sqrt(128), p = exp(c q k - lse), dp = dout . v, delta = dout . out:
+//   out = sum_j p v_j,
 //   ds = p (dp - delta),  dq = c sum_j ds k_j,  dk = c sum_t ds q_t,  dv = sum_t p dout_t.
 //
-// Two launches, each recomputing p and dp, so that every sum is one workgroup's in one order
-// and nothing is added by atomics: seven products of 2 * 128 operations per (query, key) pair
-// for the five that the formulas need.  The first takes 128 queries per workgroup and runs over
-// their keys (dq, and delta for the second); the second takes 128 keys and runs over their
-// queries (dk, dv).  Four waves hold 32 queries (keys) each: the operand that stays (q and dout;
-// k and v) in registers as MFMA fragments, the one that passes by (k and v; q and dout) in LDS
-// tiles of 64 rows, loaded one step ahead.  As in the forward the scores are computed
-// transposed, so that a lane's elements are the B operand of the product that follows; k (or q
-// and dout) is read from the same tile both along its rows and, transposed, along its columns.
+// The backward is two launches, each recomputing p and dp, so that every sum is one workgroup's
+// in one order and nothing is added by atomics: seven products of 2 * 128 operations per (query,
+// key) pair for the five that the formulas need.  The first takes 128 queries per workgroup and
+// runs over their keys (dq, and delta for the second), as the forward does; the second takes 128
+// keys and runs over their queries (dk, dv).  Four waves hold 32 queries (keys) each: the operand
+// that stays (q and dout; k) in registers as MFMA fragments, the one that passes by (k and v; q
+// and dout) in LDS tiles, loaded one step ahead.  The scores are computed transposed, so that a
+// lane's elements are the B operand of the product that follows; k (or q and dout) is read from
+// the same tile both along its rows and, transposed, along its columns.
 //
-// Measured at 32768 tokens, 8 heads, a sliding window of 2048: 432 and 580 us, 923 and 917
-// TFLOP/s of the products made (the largest library product of this card, 8192 cubed, runs at
-// 1160 to 1200): the matrix cores are busy 59 and 55 % of the time, the rest goes to the
-// exponentials and the step's loads (11 %, timed with the loads left out).
+// Measured at 32768 tokens, 8 heads, a sliding window of 2048: forward 340 us, backward 432 and
+// 580 us; 780, 923 and 917 TFLOP/s of the products made (the largest library product of this
+// card, 8192 cubed, runs at 1160 to 1200).  The matrix cores are busy 59 and 55 % of the
+// backward's time, the rest goes to the exponentials and the step's loads (11 %, timed with the
+// loads left out).
 #include "ttt_attention_internal.h"
 
 namespace ttt {
@@ -118,6 +121,47 @@ __device__ __forceinline__ void wb_store(u16* row, const f32x16 (&o)[4], float f
     }
 }
 
+// The keys that a workgroup's queries q0 .. qlast visit, [lo, lo + nsteps tiles), those of its
+// wave at w0 that every one of its queries sees, [in_lo, in_hi) (empty for a wave of padding
+// rows: a step wholly inside needs no mask), and the lane's query t's own, lo_t and len_t of them
+// (none for a padding row).
+struct WbKeys {
+  int lo, nsteps, in_lo, in_hi, lo_t, len_t;
+  __device__ __forceinline__ WbKeys(const WindowArgs& a, int q0, int qlast, int w0, int t) {
+    const int T = a.T, W = a.window, wl = min(w0 + 31, T - 1);
+    int hi, hi_t;
+    if (a.mode == TTT_WINDOW_SLIDING) {
+      lo = max(0, q0 - W + 1);
+      hi = qlast + 1;
+      lo_t = t - W + 1;
+      hi_t = t + 1;
+      in_lo = wl - W + 1;
+      in_hi = w0 + 1;
+    } else {
+      lo = (q0 / W) * W;
+      hi = (int)min<int64_t>(T, ((int64_t)(qlast / W) + 1) * W);
+      lo_t = (t / W) * W;
+      hi_t = (int)min<int64_t>(T, (int64_t)lo_t + W);
+      in_lo = (wl / W) * W;
+      in_hi = (int)min<int64_t>(T, ((int64_t)(w0 / W) + 1) * W);
+    }
+    // uniform values that come out of vector arithmetic (the divisions), back in scalar
+    // registers: a buffer resource made of vector registers takes a loop over the lanes for
+    // every load
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    in_lo = __builtin_amdgcn_readfirstlane(in_lo);
+    in_hi = __builtin_amdgcn_readfirstlane(in_hi);
+    if (t >= T) lo_t = hi_t = 0;
+    if (w0 >= T) {
+      in_lo = 1;
+      in_hi = 0;
+    }
+    len_t = hi_t - lo_t;
+    nsteps = (hi - lo + WB_ROWS - 1) / WB_ROWS;
+  }
+};
+
 // The second halves' sums added to the first halves' (waves w and w + 2 hold the same rows),
 // 32 KB through buf.  Call from every wave.
 __device__ __forceinline__ void wb_join(f32x16 (&o)[4], int w, int half, char* buf) {
@@ -145,14 +189,15 @@ __device__ __forceinline__ void wb_join(f32x16 (&o)[4], int w, int half, char* b
 // half the products in each SIMD's chain of steps, which is what such a launch waits for (one
 // head of 1024 tokens: dq 29 -> 20 us, dk and dv 42 -> 26; eight waves over 128 rows gain nothing).
 //
-// SUM: delta summed from p and dp in a walk of its own over the keys instead of from dout and
-// out.  The rounding of out to bf16 moves delta by 2^-9 of |dout| |out|, which counts where a
-// window holds few tokens and out is as long as they are: with it the gradients of a window of
-// 2 are 1.7 times as far off as their own rounding alone, with the sum 1.4 times, as those of
-// long windows are.  For windows of at most one step's keys, where the walk is short.
-template <bool SUM, int NH>
+// Forward with each row's log-sum-exp.  The running maximum that the exponentials refer to moves
+// only when a score passes it by more than 2^8: the sums stay far inside fp32, the rounding of
+// the probabilities to bf16 is relative, and the 64 sums of a lane are rescaled in the first
+// steps only instead of in nearly every one (a maximum over 64 more scores moves for some row
+// of 32 nearly always).  The normaliser sums the probabilities before they are rounded, as the
+// log-sum-exp has to.
+template <int NH>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
-void k_window_dq(AttnBwdArgs a) {
+void k_window_fwd(WindowArgs a) {
   constexpr int RG = 4 / NH, QB = 32 * RG;   // row groups, queries of a workgroup
   __shared__ __attribute__((aligned(1024))) char st0[2 * WB_TILE];
   __shared__ __attribute__((aligned(1024))) char st1[2 * WB_TILE];
@@ -163,41 +208,164 @@ void k_window_dq(AttnBwdArgs a) {
   const int lane = threadIdx.x & 63, hl = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int w = wave % RG, half = wave / RG;
-  const int T = a.T, W = a.window;
+  const int T = a.T;
+  const int q0 = qb * QB, w0 = q0 + 32 * w;
+  const int t = w0 + (lane & 31);
+  const WbKeys r(a, q0, min(q0 + QB, T) - 1, w0, t);
+
+  const int64_t row0 = (int64_t)b * T;
+  const u16* kb = a.k + row0 * a.ld + (int64_t)h * ATT_D;
+  const u16* vb = a.v + row0 * a.ld + (int64_t)h * ATT_D;
+  WbLoad lk;
+  lk.init(a.ld);
+  const u16 *kp = kb + (int64_t)r.lo * a.ld, *vp = vb + (int64_t)r.lo * a.ld;   // the next step's rows
+  const int64_t adv = WB_ROWS * a.ld;
+  auto issue = [&](char* st, int rows) __attribute__((always_inline)) {
+    lk.issue<WB_ROWS>(st, kp, rows);
+    lk.issue<WB_ROWS>(st + WB_TILE, vp, rows);
+    kp += adv;
+    vp += adv;
+  };
+  issue(st0, T - r.lo);
+
+  bf16x8 qf[8];
+  wb_frags(qf, a.q + (row0 + t) * a.ld + (int64_t)h * ATT_D, hl, t < T);
+  WbAt at;
+  at.init();
+  f32x16 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f32x16{};
+  float m = -INFINITY, l = 0.f;
+
+  auto step = [&](const char* cur, char* nxt, int i) __attribute__((always_inline)) {
+    const int kv0 = r.lo + i * WB_ROWS;
+    if (i + 1 < r.nsteps) issue(nxt, T - kv0 - WB_ROWS);
+    constexpr int N = 2 / NH;                    // halves of this wave
+    const int r0 = NH == 1 ? 0 : 32 * half;      // its first row of the tile
+    f32x16 s[N];
+#pragma unroll
+    for (int kt = 0; kt < N; ++kt) s[kt] = f32x16{};
+    if (kv0 < r.in_lo || kv0 + WB_ROWS > r.in_hi) {   // the mask as the scores' first summand
+#pragma unroll
+      for (int kt = 0; kt < N; ++kt) {
+        const int base = kv0 + r0 + 32 * kt + 4 * hl - r.lo_t;
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          s[kt][v] = (unsigned)(base + 8 * (v >> 2) + (v & 3)) < (unsigned)r.len_t ? 0.f : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+      for (int kt = 0; kt < N; ++kt) s[kt] = wb_mma(wb_row(cur, at, r0 + 32 * kt, x), qf[x], s[kt]);
+    if constexpr (NH == 1) {
+      WB_ORDER(WB_DS, 4);
+#pragma unroll
+      for (int x = 0; x < 12; ++x) {
+        WB_ORDER(WB_MFMA, 1);
+        WB_ORDER(WB_DS, 1);
+      }
+      WB_ORDER(WB_MFMA, 4);
+    }
+    // a wave past its scores goes before the SIMD's other one (354 -> 340 us with the order above)
+    __builtin_amdgcn_s_setprio(1);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int kt = 0; kt < N; ++kt)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kt][v]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32)) * a.scale2;
+    if (__any(mx > m + 8.f)) {   // wave-uniform
+      const float mnew = fmaxf(m, mx);
+      const float alpha = __builtin_amdgcn_exp2f(m - (mnew == -INFINITY ? 0.f : mnew));
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) o[d][v] *= alpha;
+      m = mnew;
+    }
+    const float mref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int kt = 0; kt < N; ++kt)
+#pragma unroll
+      for (int sp = 0; sp < 2; ++sp) {
+        bf16x8 pf;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[kt][8 * sp + e], a.scale2, -mref));
+          l += p;
+          pf[e] = static_cast<__bf16>(p);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          o[d] = wb_mma(wb_col(cur + WB_TILE, at, 32 * d, r0 + 32 * kt + 16 * sp), pf, o[d]);
+      }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+  };
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  int i = 0;
+  for (; i + 1 < r.nsteps; i += 2) {
+    step(st0, st1, i);
+    step(st1, st0, i + 1);
+  }
+  if (i < r.nsteps) step(st0, st1, i);
+
+  l += __shfl_xor(l, 32);
+  if constexpr (NH == 2) {   // to one reference, then the halves' sums together
+    float* ms = reinterpret_cast<float*>(st1);
+    if (lane < 32) {
+      ms[32 * wave + lane] = m;
+      ms[128 + 32 * wave + lane] = l;
+    }
+    __syncthreads();
+    const int other = 32 * (w + RG * (1 - half)) + (lane & 31);
+    const float mo = ms[other], mt = fmaxf(m, mo), mtr = mt == -INFINITY ? 0.f : mt;
+    const float f = __builtin_amdgcn_exp2f(m - mtr);
+    l = l * f + ms[128 + other] * __builtin_amdgcn_exp2f(mo - mtr);
+    m = mt;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) o[d][v] *= f;
+    wb_join(o, w, half, st0);
+    if (half) return;
+  }
+  if (t < T) {
+    wb_store(a.out + (row0 + t) * a.ldo + (int64_t)h * ATT_D, o, 1.f / l, hl);
+    if (hl == 0) a.lse[((int64_t)b * a.heads + h) * T + t] = (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+// First kernel of the backward.
+//
+// SUM: delta summed from p and dp in a walk of its own over the keys instead of from dout and
+// out.  The rounding of out to bf16 moves delta by 2^-9 of |dout| |out|, which counts where a
+// window holds few tokens and out is as long as they are: with it the gradients of a window of
+// 2 are 1.7 times as far off as their own rounding alone, with the sum 1.4 times, as those of
+// long windows are.  For windows of at most one step's keys, where the walk is short.
+template <bool SUM, int NH>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void k_window_dq(WindowArgs a) {
+  constexpr int RG = 4 / NH, QB = 32 * RG;   // row groups, queries of a workgroup
+  __shared__ __attribute__((aligned(1024))) char st0[2 * WB_TILE];
+  __shared__ __attribute__((aligned(1024))) char st1[2 * WB_TILE];
+  const int id = xcd_block(blockIdx.x, a.total);
+  const int qb = __builtin_amdgcn_readfirstlane(id % a.blocks);
+  const int bh = __builtin_amdgcn_readfirstlane(id / a.blocks);
+  const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
+  const int lane = threadIdx.x & 63, hl = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int w = wave % RG, half = wave / RG;
+  const int T = a.T;
   const int q0 = qb * QB, w0 = q0 + 32 * w;
   const int t = w0 + (lane & 31);
 
-  // keys the workgroup visits, the lane's own [lo_t, hi_t), and the range that needs no mask
-  const int qlast = min(q0 + QB, T) - 1, wl = min(w0 + 31, T - 1);
-  int lo, hi, lo_t, hi_t, in_lo, in_hi;
-  if (a.mode == TTT_WINDOW_SLIDING) {
-    lo = max(0, q0 - W + 1);
-    hi = qlast + 1;
-    lo_t = t - W + 1;
-    hi_t = t + 1;
-    in_lo = wl - W + 1;
-    in_hi = w0 + 1;
-  } else {
-    lo = (q0 / W) * W;
-    hi = (int)min<int64_t>(T, ((int64_t)(qlast / W) + 1) * W);
-    lo_t = (t / W) * W;
-    hi_t = (int)min<int64_t>(T, (int64_t)lo_t + W);
-    in_lo = (wl / W) * W;
-    in_hi = (int)min<int64_t>(T, ((int64_t)(w0 / W) + 1) * W);
-  }
-  // uniform values that come out of vector arithmetic (the divisions), back in scalar registers:
-  // a buffer resource made of vector registers takes a loop over the lanes for every load
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  in_lo = __builtin_amdgcn_readfirstlane(in_lo);
-  in_hi = __builtin_amdgcn_readfirstlane(in_hi);
-  if (t >= T) lo_t = hi_t = 0;
-  if (w0 >= T) {
-    in_lo = 1;
-    in_hi = 0;
-  }
-  const int len_t = hi_t - lo_t;
-  const int nsteps = (hi - lo + WB_ROWS - 1) / WB_ROWS;
+  const WbKeys r(a, q0, min(q0 + QB, T) - 1, w0, t);
+  const int lo = r.lo, lo_t = r.lo_t, len_t = r.len_t, in_lo = r.in_lo, in_hi = r.in_hi, nsteps = r.nsteps;
 
   const int64_t row0 = (int64_t)b * T;
   const u16* kb = a.k + row0 * a.ld + (int64_t)h * ATT_D;
@@ -389,7 +557,7 @@ struct WbStage {
 
 template <int NH>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
-void k_window_dkv(AttnBwdArgs a) {
+void k_window_dkv(WindowArgs a) {
   constexpr int RG = 4 / NH, KB = 32 * RG;   // row groups, keys of a workgroup
   constexpr int QROWS = WbStage<NH>::ROWS, QTILE = WbStage<NH>::TILE;
   __shared__ __attribute__((aligned(1024))) char st0[WbStage<NH>::BYTES];
@@ -551,7 +719,7 @@ void k_window_dkv(AttnBwdArgs a) {
 }
 
 template <int NH>
-hipError_t launch_window_bwd_nh(const AttnBwdArgs& a, hipStream_t st) {
+hipError_t launch_window_bwd_nh(const WindowArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)a.total), block(256);
   if (a.window <= WB_ROWS) hipLaunchKernelGGL((k_window_dq<true, NH>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_window_dq<false, NH>), grid, block, 0, st, a);
@@ -563,12 +731,25 @@ hipError_t launch_window_bwd_nh(const AttnBwdArgs& a, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_window_bwd(AttnBwdArgs a, int64_t problems, hipStream_t st) {
+// the form of a launch: a.blocks and a.total, and whether it leaves CUs idle
+static bool wb_form(WindowArgs& a, int64_t problems) {
   const int64_t small = (a.T + 63) / 64 * problems;
   const bool few = small <= WB_FEW;
   a.blocks = few ? (a.T + 63) / 64 : (a.T + 127) / 128;
   a.total = (int32_t)(a.blocks * problems);
-  return few ? launch_window_bwd_nh<2>(a, st) : launch_window_bwd_nh<1>(a, st);
+  return few;
+}
+
+hipError_t launch_window_fwd(WindowArgs a, int64_t problems, hipStream_t st) {
+  const bool few = wb_form(a, problems);
+  const dim3 grid((unsigned)a.total), block(256);
+  if (few) hipLaunchKernelGGL(k_window_fwd<2>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(k_window_fwd<1>, grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_window_bwd(WindowArgs a, int64_t problems, hipStream_t st) {
+  return wb_form(a, problems) ? launch_window_bwd_nh<2>(a, st) : launch_window_bwd_nh<1>(a, st);
 }
 
 }  // namespace ttt

@@ -38,6 +38,10 @@ ttt_status check_attention(int64_t ld, int64_t ld_out, int32_t batch, int32_t he
   return TTT_OK;
 }
 
+}  // namespace ttt
+
+namespace {
+
 AttnArgs attention_args(const void* q, const void* k, const void* v, int64_t ld, void* out,
                         int64_t ld_out, int32_t batch, int32_t heads, int64_t T,
                         int32_t window, int32_t mode) {
@@ -46,7 +50,6 @@ AttnArgs attention_args(const void* q, const void* k, const void* v, int64_t ld,
   a.k = static_cast<const u16*>(k);
   a.v = static_cast<const u16*>(v);
   a.out = static_cast<u16*>(out);
-  a.lse = nullptr;
   a.ld = ld;
   a.ldo = ld_out;
   a.T = (int32_t)T;
@@ -58,10 +61,6 @@ AttnArgs attention_args(const void* q, const void* k, const void* v, int64_t ld,
   a.scale2 = (float)(1.4426950408889634 / std::sqrt((double)ATT_D));
   return a;
 }
-
-}  // namespace ttt
-
-namespace {
 
 ttt_status check_linear(int64_t rows, int32_t K, int32_t N, int32_t epi) {
   if (rows < 0) return failf(TTT_E_SHAPE, "rows %lld < 0", (long long)rows);

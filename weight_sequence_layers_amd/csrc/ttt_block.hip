@@ -47,22 +47,14 @@ __device__ __forceinline__ bf16x8 read_vt_frag(const char* tile, int dim_base, i
   return __builtin_bit_cast(bf16x8, v);
 }
 
-//
-// LSE: also stores each row's log-sum-exp for the backward, from a second sum of the
-// probabilities before they are rounded (the rounded ones would put it 2^-9 off).
-template <bool LSE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void k_window_attention(AttnArgs a) {
   constexpr int NT = 256, QB = ATT_Q;
   __shared__ __attribute__((aligned(1024))) char st0[ATT_STAGE];
   __shared__ __attribute__((aligned(1024))) char st1[ATT_STAGE];
   const int id = xcd_block(blockIdx.x, a.total);
-  // uniform values that come out of vector arithmetic (the divisions) go back to scalar
-  // registers: a buffer resource made of vector registers takes a loop over the lanes for
-  // every load
-  const int qb = __builtin_amdgcn_readfirstlane(id % a.qblocks);
-  const int bh = __builtin_amdgcn_readfirstlane(id / a.qblocks);
-  const int b = __builtin_amdgcn_readfirstlane(bh / a.heads), h = bh - b * a.heads;
+  const int qb = id % a.qblocks, bh = id / a.qblocks;
+  const int h = bh % a.heads, b = bh / a.heads;
   const int lane = threadIdx.x & 63, hl = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int T = a.T, W = a.window;
@@ -83,8 +75,6 @@ void k_window_attention(AttnArgs a) {
     lo_t = (t / W) * W;
     hi_t = (int)min<int64_t>(T, (int64_t)lo_t + W);
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
   if (t >= T) lo_t = hi_t = 0;   // padding rows: every key masked, nothing stored
   const int len_t = hi_t - lo_t;
   const int nsteps = (hi - lo + ATT_KV - 1) / ATT_KV;
@@ -103,8 +93,6 @@ void k_window_attention(AttnArgs a) {
       in_lo = (wl / W) * W;
       in_hi = (int)min<int64_t>(T, ((int64_t)(w0 / W) + 1) * W);
     }
-    in_lo = __builtin_amdgcn_readfirstlane(in_lo);
-    in_hi = __builtin_amdgcn_readfirstlane(in_hi);
   }
 
   const int64_t row0 = (int64_t)b * T;
@@ -146,7 +134,7 @@ void k_window_attention(AttnArgs a) {
   f32x16 o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = f32x16{};
-  float m = -INFINITY, l = 0.f, lx = 0.f;
+  float m = -INFINITY, l = 0.f;
 
   if (nsteps > 0) issue(st0, lo);
   __builtin_amdgcn_s_waitcnt(0);
@@ -190,7 +178,6 @@ void k_window_attention(AttnArgs a) {
     if (__any(mnew != m)) {   // wave-uniform: some running maximum moved
       const float alpha = __builtin_amdgcn_exp2f(m - mref);
       l *= alpha;
-      if (LSE) lx *= alpha;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
 #pragma unroll
@@ -204,11 +191,10 @@ void k_window_attention(AttnArgs a) {
         bf16x8 pf;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = __builtin_amdgcn_exp2f(fmaf(sc[kt][8 * sp + e], a.scale2, -mref));
-          const __bf16 p = static_cast<__bf16>(x);
+          const __bf16 p = static_cast<__bf16>(
+              __builtin_amdgcn_exp2f(fmaf(sc[kt][8 * sp + e], a.scale2, -mref)));
           pf[e] = p;
           l += static_cast<float>(p);
-          if (LSE) lx += x;
         }
 #pragma unroll
         for (int d = 0; d < 4; ++d)
@@ -221,10 +207,6 @@ void k_window_attention(AttnArgs a) {
 
   // element v of o[d]: dim 32 d + 8 (v / 4) + 4 (lane / 32) + v % 4 of query t
   const float lt = l + __shfl_xor(l, 32);
-  if (LSE) {
-    const float lxt = lx + __shfl_xor(lx, 32);
-    if (t < T && hl == 0) a.lse[(int64_t)bh * T + t] = (m + log2f(lxt)) * 0.69314718055994531f;
-  }
   if (t < T) {
     const float inv = 1.f / lt;
     u16* orow = a.out + (row0 + t) * a.ldo + (int64_t)h * ATT_D + 4 * hl;
@@ -493,8 +475,7 @@ __global__ __launch_bounds__(256) void k_blk_merge(HeadMergeArgs a) {
 
 hipError_t launch_window_attention(const AttnArgs& a, hipStream_t st) {
   if (a.total == 0) return hipSuccess;
-  if (a.lse) hipLaunchKernelGGL(k_window_attention<true>, dim3(a.total), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL(k_window_attention<false>, dim3(a.total), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_window_attention, dim3(a.total), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

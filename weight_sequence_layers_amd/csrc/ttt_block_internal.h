@@ -21,7 +21,6 @@ struct AttnArgs {
   const u16* k;
   const u16* v;
   u16* out;
-  float* lse;     // [batch][heads][T] log-sum-exp of every row, or null
   int64_t ld, ldo;
   int32_t T, heads, window, mode, qblocks, total;
   float scale2;   // log2(e) / sqrt(ATT_D)
@@ -65,12 +64,9 @@ struct HeadMergeArgs {
   int32_t T, B, H, d;
 };
 
-// host checks and arguments of the window attention (ttt_block.cpp)
+// host checks of the window attention (ttt_block.cpp)
 ttt_status check_attention(int64_t ld, int64_t ld_out, int32_t batch, int32_t heads, int64_t T,
                            int32_t window, int32_t mode);
-AttnArgs attention_args(const void* q, const void* k, const void* v, int64_t ld, void* out,
-                        int64_t ld_out, int32_t batch, int32_t heads, int64_t T, int32_t window,
-                        int32_t mode);
 
 hipError_t launch_window_attention(const AttnArgs& a, hipStream_t st);
 hipError_t launch_linear(const LinearArgs& a, int epilogue, hipStream_t st);
