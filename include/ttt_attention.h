@@ -67,8 +67,8 @@ ttt_status ttt_validate_rope_config(const ttt_rope_config* cfg);
  * 64 bits, so positions anywhere in int32 keep their precision.
  *   q, k     element e of head h of token t at  t * ld + h * head_dim + e
  *   q_out, k_out  the same with ld_qo, ld_ko.  q_out may be q itself (ld_qo == ld_q) and k_out
- *            k; other overlaps of an output with an input or the other output are
- *            TTT_E_CONFIG.  q and k may be parts of one projection's rows.
+ *            k; other overlaps of an output with an input (weights, freq and pos
+ *            among them) or the other output are TTT_E_CONFIG.  q and k may be parts of one projection's rows.
  *   q_weight, k_weight  [head_dim] learned scales, or NULL for ones (must be NULL without norm)
  *   freq     fp32 [axes][rot_dim / 2], radians per position: a pair that turns with one axis
  *            holds zeros for the others (may be NULL with rot_dim 0)
@@ -88,7 +88,8 @@ ttt_status ttt_qk_norm_rope(const ttt_rope_config* cfg, const void* q, int64_t l
  * and, where a weight and its gradient pointer are given, those of the learned scales
  * (dq_weight, dk_weight, fp32 [head_dim], overwritten: the sum over all tokens and heads, in
  * an order that depends only on the sizes).  q, k, weights, freq, pos as given to the forward.
- * dq may be dq_out itself (same stride) and dk dk_out; other overlaps are TTT_E_CONFIG.
+ * dq may be dq_out itself (same stride) and dk dk_out; other overlaps of what is written (work
+ * among it) with an input or each other are TTT_E_CONFIG.
  * work: workspace of the size that ttt_qk_norm_rope_backward_work gives (0 without norm; work
  * may then be NULL).  tokens 0 writes zero weight gradients.
  */
@@ -161,7 +162,8 @@ ttt_status ttt_qk_norm_rope_append(const ttt_rope_config* cfg, const void* q, in
  * value within it gives NaN.
  * heads a multiple of kv_heads, at most 65536; head_dim 64, 128 or 256; 0 <= seqs <= 2^20,
  * seqs * heads below 2^24; max_pages >= 0, max_pages * page_size <= 2^30; window >= 0; scale 0
- * selects 1 / sqrt(head_dim), otherwise finite and > 0.  out may not overlap q or the cache.
+ * selects 1 / sqrt(head_dim), otherwise finite and > 0.  out, lse and work may not overlap the
+ * inputs, the cache or each other.
  * Scores, softmax and sums are fp32; the probabilities enter the product with v as two bf16
  * numbers each (16 significant bits), so out is rounded once.
  * work: workspace of the size ttt_paged_attention_work gives for the same cache sizes, seqs,

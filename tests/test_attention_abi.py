@@ -265,3 +265,26 @@ def test_paged_index_rules(tmp_path):
                     "-I" + B.CSRC, "-x", "hip", str(src), "-o", str(exe)], check=True, capture_output=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("call,kw", [
+    *[(forward, dict(qo=P(i))) for i in (2, 3, 4, 5)], *[(forward, dict(ko=P(i))) for i in (2, 3, 4, 5)],
+    (forward, dict(pos=P(6, 256 * 2 * 9 + 496))),     # the output's last elements
+    *[(backward, {out: P(i)}) for out in ("dqw", "dkw", "work") for i in range(10)],
+    *[(backward, {out: P(i)}) for out in ("dq", "dk") for i in (2, 3, 4, 5)],
+    (backward, dict(dqw=P(11))), (backward, dict(work=P(10))), (backward, dict(work=P(11))),
+    (backward, dict(dqw=P(11), tokens=0)),
+    *[(append, dict(qo=P(i))) for i in (4, 5, 6, 20, 21)], *[(append, {n: P(20)}) for n in ("freq", "pos", "slot", "qw")],
+    *[(paged, dict(out=P(i))) for i in (0, 1, 2, 20, 21)], *[(paged, dict(lse=P(i))) for i in (0, 1, 2, 3, 20, 21)],
+    *[(paged, dict(work=P(i), max_pages=1000)) for i in (0, 1, 2, 3, 4, 20, 21)],
+])
+def test_nothing_written_overlaps_what_is_read(call, kw):
+    assert call(**kw) == 4, W.lib().ttt_last_error()
+
+
+def test_scales_of_an_e4m3_cache_are_not_written_over():
+    for n in ("k_scale", "v_scale"):
+        assert append(cache(dtype=1, **{n: P(7).value})) == 4
+        assert append(cache(dtype=1, **{n: P(21).value})) == 4
+        for at in (3, 4):
+            assert paged(cache(dtype=1, **{n: P(at).value})) == 4

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "ttt_attention_internal.h"
 #include "ttt_block_host.h"
@@ -32,6 +33,20 @@ bool share(const Rows& a, const Rows& b) {
   const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p));
   const int64_t m = ((d % a.ld) + a.ld) % a.ld;   // b's column offset in a's rows
   return m < a.width || m + b.width > a.ld;
+}
+
+// `bytes` bytes in a row; NULL, or a call that does not touch them, is none.
+Rows flat(const void* p, int64_t bytes) { return {p, p && bytes > 0 ? 1 : 0, bytes, bytes}; }
+
+// Whether what a call writes shares a byte with the tables it reads or with its other outputs.
+bool clash(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+  for (const Rows* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Rows& r : ins)
+      if (share(*o, r)) return true;
+    for (const Rows* x = outs.begin(); x != o; ++x)
+      if (share(*o, *x)) return true;
+  }
+  return false;
 }
 
 ttt_status check_rope(const ttt_rope_config* c) {
@@ -86,6 +101,17 @@ ttt_status rope_common(const ttt_rope_config* c, const void* qw, const void* kw,
     BLK_TRY(need(pos, "pos"));
   }
   return TTT_OK;
+}
+
+// The tables that every norm-and-rotation call reads.
+struct RopeTables {
+  Rows qw, kw, freq, pos;
+};
+
+RopeTables rope_tables(const ttt_rope_config* c, const void* qw, const void* kw, const float* freq,
+                       const int32_t* pos, int64_t tokens) {
+  const int64_t w = (int64_t)c->head_dim * act_size(c), turns = c->rot_dim ? c->axes * (int64_t)4 : 0;
+  return {flat(qw, w), flat(kw, w), flat(freq, turns * (c->rot_dim / 2)), flat(pos, turns * tokens)};
 }
 
 RopeArgs rope_args(const ttt_rope_config* c, const void* qw, const void* kw, const float* freq,
@@ -263,6 +289,9 @@ ttt_status ttt_qk_norm_rope(const ttt_rope_config* cfg, const void* q, int64_t l
   if ((share(oq, rq) && !(q_out == q && ld_qo == ld_q)) || share(oq, rk) ||
       (share(ok, rk) && !(k_out == k && ld_ko == ld_k)) || share(ok, rq) || share(oq, ok))
     return failf(TTT_E_CONFIG, "an output overlaps an input or the other output");
+  const RopeTables t = rope_tables(cfg, q_weight, k_weight, freq, pos, tokens);
+  if (clash({oq, ok}, {t.qw, t.kw, t.freq, t.pos}))
+    return failf(TTT_E_CONFIG, "an output overlaps a scale, freq or pos");
   RopeArgs a = rope_args(cfg, q_weight, k_weight, freq, pos, tokens);
   a.q.x = q;
   a.q.ldx = ld_q;
@@ -312,9 +341,12 @@ ttt_status ttt_qk_norm_rope_backward(const ttt_rope_config* cfg, const void* q, 
   dw.dq = dq_weight;
   dw.dk = dk_weight;
   dw.D = cfg->head_dim;
+  const int64_t scale_bytes = (int64_t)cfg->head_dim * (int64_t)sizeof(float);
+  const Rows wq = flat(dq_weight, scale_bytes), wk = flat(dk_weight, scale_bytes);
   if (tokens == 0) {   // a sum over no rows
     if (cfg->norm == TTT_HEAD_NORM_NONE && (q_weight || k_weight))
       return failf(TTT_E_CONFIG, "learned scales without a norm");
+    if (share(wq, wk)) return failf(TTT_E_CONFIG, "dq_weight overlaps dk_weight");
     if (want) BLK_HIP(launch_rope_dw(dw, st));
     return TTT_OK;
   }
@@ -339,6 +371,10 @@ ttt_status ttt_qk_norm_rope_backward(const ttt_rope_config* cfg, const void* q, 
       share(ok, gq) || share(oq, ok) || (share(oq, gq) && !(dq == dq_out && ld_dq == ld_dqo)) ||
       (share(ok, gk) && !(dk == dk_out && ld_dk == ld_dko)))
     return failf(TTT_E_CONFIG, "a gradient overlaps an input or the other gradient");
+  const RopeTables t = rope_tables(cfg, q_weight, k_weight, freq, pos, tokens);
+  if (clash({oq, ok, wq, wk, flat(work, bytes)}, {t.qw, t.kw, t.freq, t.pos}) ||
+      clash({wq, wk, flat(work, bytes)}, {rq, rk, gq, gk}))
+    return failf(TTT_E_CONFIG, "a gradient or work overlaps an input, work or another gradient");
   RopeArgs a = rope_args(cfg, q_weight, k_weight, freq, pos, tokens);
   a.q.x = q;
   a.q.ldx = ld_q;
@@ -397,6 +433,11 @@ ttt_status ttt_qk_norm_rope_append(const ttt_rope_config* cfg, const void* q, in
   if (share(ck, cv) || share(ck, rq) || share(ck, rk) || share(ck, rv) || share(ck, oq) ||
       share(cv, rq) || share(cv, rk) || share(cv, rv) || share(cv, oq))
     return failf(TTT_E_CONFIG, "the cache's keys and values overlap each other or a tensor");
+  const RopeTables t = rope_tables(cfg, q_weight, k_weight, freq, pos, tokens);
+  const int64_t scales = (int64_t)cache->kv_heads * (int64_t)sizeof(float);
+  if (clash({oq, ck, cv}, {t.qw, t.kw, t.freq, t.pos, flat(slot, tokens * (int64_t)sizeof(int64_t)),
+                           flat(cache->k_scale, scales), flat(cache->v_scale, scales)}))
+    return failf(TTT_E_CONFIG, "q_out or the cache overlaps a scale, freq, pos or slot");
   RopeArgs a = rope_args(cfg, q_weight, k_weight, freq, pos, tokens);
   a.q.x = q;
   a.q.ldx = ld_q;
@@ -454,8 +495,12 @@ ttt_status ttt_paged_attention(const void* q, int64_t ld_q, const ttt_kv_cache* 
                    (long long)p.bytes);
   }
   const Rows rq = {q, seqs, n * 2, ld_q * 2}, ro = {out, seqs, n * 2, ld_out * 2};
-  if (share(ro, rq) || share(ro, cache_rows(cache, cache->k)) || share(ro, cache_rows(cache, cache->v)))
-    return failf(TTT_E_CONFIG, "out overlaps q or the cache");
+  const int64_t scales = (int64_t)cache->kv_heads * (int64_t)sizeof(float);
+  if (clash({ro, flat(lse, (int64_t)seqs * heads * (int64_t)sizeof(float)), flat(work, p.bytes)},
+            {rq, cache_rows(cache, cache->k), cache_rows(cache, cache->v), flat(cache->k_scale, scales),
+             flat(cache->v_scale, scales), flat(lens, (int64_t)seqs * (int64_t)sizeof(int32_t)),
+             flat(table, (int64_t)seqs * max_pages * (int64_t)sizeof(int32_t))}))
+    return failf(TTT_E_CONFIG, "out, lse or work overlaps an input or each other");
   PagedArgs a = {};
   a.q = static_cast<const u16*>(q);
   a.ldq = ld_q;
