@@ -865,3 +865,44 @@ def test_binding_refuses_wrong_tensors():
     x = torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
     with pytest.raises(W.TTTError):
         W.make_kv_cache(x, x)
+
+
+def test_binding_refuses_rows_past_the_memory():
+    """Row strides that lead past a tensor's memory, a cache or a stream of another device."""
+    r = Rope(T=4, Hq=2, Hk=1, D=64, rot=64)
+    flat = torch.zeros(3 * 256 + 128, device=DEV, dtype=torch.bfloat16)   # 4 rows 256 apart, to the element
+    ko = r.out(1)
+
+    def call(qo, ld):
+        W.ttt_qk_norm_rope(r.cfg, r.q, r.ld, r.k, r.ld, r.qw, r.kw, r.freq, r.pos, qo, ld, ko, 80, 4)
+    call(flat, 256)
+    third = torch.zeros(4, 384, device=DEV, dtype=torch.bfloat16)
+    call(third[:, 256:], 384)
+    for qo, ld in ((flat, 264), (flat[:-8], 256), (third[:, 256:], 392), (third[:, :128].contiguous(), 136)):
+        with pytest.raises(W.TTTError) as e:
+            call(qo, ld)
+        assert e.value.status == 2
+
+    kv = torch.zeros(2, 1, 4, 64, device=DEV, dtype=torch.bfloat16)
+    c = W.make_kv_cache(kv, torch.zeros_like(kv))
+    q = torch.zeros(2, 64, device=DEV, dtype=torch.bfloat16)
+    out, table = torch.ones_like(q), torch.zeros(2, 1, device=DEV, dtype=torch.int32)
+    lens = torch.zeros(2, device=DEV, dtype=torch.int32)
+
+    def attend(ld=64, **kw):
+        W.ttt_paged_attention(q, ld, c, table, lens, out, 64, None, 2, 1, 1, 0, 0.0, None, **kw)
+    attend()
+    assert not out.any()
+    x = torch.zeros(6, 128, device=DEV, dtype=torch.bfloat16)
+    stat = torch.zeros(6, device=DEV)
+
+    def window(ld, ld_out):
+        W.ttt_window_attention_lse(x, x, x, ld, torch.zeros_like(x), ld_out, stat, 2, 1, 3, 2)
+    window(128, 128)
+    other = type("Stream", (), dict(device=torch.device("cuda", c.device + 1), cuda_stream=0))
+    c.device += 1
+    for bad, code in ((lambda: attend(ld=72), 2), (attend, 4), (lambda: attend(stream=other), 4),
+                      (lambda: window(136, 128), 2), (lambda: window(128, 136), 2)):
+        with pytest.raises(W.TTTError) as e:
+            bad()
+        assert e.value.status == code

@@ -75,6 +75,7 @@ class ttt_kv_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")
     ] + [("page_stride", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
         "pages", "page_size", "kv_heads", "head_dim", "dtype", "reserved")]
+    device = None   # of the tensors, where make_kv_cache filled the struct
 
 
 HEAD_NORM = {"none": 0, "rms": 1}
@@ -440,12 +441,22 @@ def ttt_block_destroy(blk: Block) -> None:
 
 # ------------------------------------------- attention around the block (ttt_attention.h)
 def _here(stream):
-    """The current device's number and the handle of `stream` (None: its current stream)."""
+    """torch, the current device's number and the handle of `stream` (None: its current
+    stream)."""
     import torch
     dev = torch.cuda.current_device()
     if stream is None:   # the handle without a Stream object around it: 1 us less per call
-        return dev, torch._C._cuda_getCurrentRawStream(dev) or None
-    return dev, _stream(stream)
+        return torch, dev, torch._C._cuda_getCurrentRawStream(dev) or None
+    if getattr(getattr(stream, "device", None), "index", dev) != dev:
+        raise TTTError(4, f"a stream of {stream.device}, not of the current HIP device")
+    return torch, dev, _stream(stream)
+
+
+def _cache(c, dev: int):
+    """The cache as an argument; make_kv_cache noted the device of its tensors."""
+    if c.device is not None and c.device != dev:
+        raise TTTError(4, f"the cache is on cuda:{c.device}, not on the current HIP device")
+    return ctypes.byref(c)
 
 
 def _arg(t, name: str, dtype, n: int, dev: int, dense: bool = True) -> Optional[int]:
@@ -465,14 +476,24 @@ def _arg(t, name: str, dtype, n: int, dev: int, dense: bool = True) -> Optional[
     return t.data_ptr()
 
 
+def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Optional[int]:
+    """_arg of a matrix of rows ld elements apart, the last of which must end within a contiguous
+    tensor, or within the memory that another is a view of (a third of a projection's rows)."""
+    if t is None:
+        return None
+    last, have = (rows - 1) * ld + width, t.numel()
+    if have >= rows * width and t.dtype is dtype and t.get_device() == dev:
+        if not t.is_contiguous():
+            have = t.untyped_storage().nbytes() // dtype.itemsize - t.storage_offset()
+        if have >= last:
+            return t.data_ptr()
+    _arg(t, name, dtype, rows * width, dev, False)
+    raise TTTError(2, f"{name}: {rows} rows {ld} apart take {last} elements, {have} are there")
+
+
 def _work(t, dev: int):
     """Pointer and bytes of a workspace tensor of any dtype (None: none)."""
     return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0, dev), t.numel() * t.element_size())
-
-
-def _act_dtype(cfg):
-    import torch
-    return torch.bfloat16 if cfg.act == 1 else torch.float32
 
 
 def make_rope_config(*, q_heads: int, k_heads: int, head_dim: int, rot_dim: Optional[int] = None,
@@ -494,12 +515,11 @@ def ttt_validate_rope_config(cfg: ttt_rope_config) -> None:
     _check(lib().ttt_validate_rope_config(ctypes.byref(cfg)))
 
 
-def _rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev):
-    import torch
-    dt, half = _act_dtype(cfg), cfg.rot_dim // 2
-    return (_arg(q_weight, "q_weight", dt, cfg.head_dim, dev), _arg(k_weight, "k_weight", dt, cfg.head_dim, dev),
-            _arg(freq, "freq", torch.float32, cfg.axes * half, dev),
-            _arg(pos, "pos", torch.int32, cfg.axes * tokens if half else 0, dev))
+def _rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev, dt, torch):
+    D, half, axes = cfg.head_dim, cfg.rot_dim // 2, cfg.axes
+    return (_arg(q_weight, "q_weight", dt, D, dev), _arg(k_weight, "k_weight", dt, D, dev),
+            _arg(freq, "freq", torch.float32, axes * half, dev),
+            _arg(pos, "pos", torch.int32, axes * tokens if half else 0, dev))
 
 
 def ttt_qk_norm_rope(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight, k_weight, freq,
@@ -508,13 +528,15 @@ def ttt_qk_norm_rope(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight,
     """Per-head norm and position rotation of queries and keys: element (t, h, e) of q at
     t ld_q + h head_dim + e (k, q_out and k_out with theirs); freq fp32 [axes, rot_dim / 2],
     pos int32 [axes, tokens] (see include/ttt_attention.h)."""
-    dev, st = _here(stream)
-    dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
+    torch, dev, st = _here(stream)
+    D, dt = cfg.head_dim, torch.bfloat16 if cfg.act == 1 else torch.float32
+    wq, wk = cfg.q_heads * D, cfg.k_heads * D
     _check(lib().ttt_qk_norm_rope(
-        ctypes.byref(cfg), _arg(q, "q", dt, nq, dev, False), ld_q, _arg(k, "k", dt, nk, dev, False), ld_k,
-        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev),
-        _arg(q_out, "q_out", dt, nq, dev, False), ld_qo, _arg(k_out, "k_out", dt, nk, dev, False), ld_ko, tokens,
-        st))
+        ctypes.byref(cfg), _rows(q, "q", dt, tokens, wq, ld_q, dev), ld_q,
+        _rows(k, "k", dt, tokens, wk, ld_k, dev), ld_k,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev, dt, torch),
+        _rows(q_out, "q_out", dt, tokens, wq, ld_qo, dev), ld_qo,
+        _rows(k_out, "k_out", dt, tokens, wk, ld_ko, dev), ld_ko, tokens, st))
 
 
 def ttt_qk_norm_rope_backward_work(cfg: ttt_rope_config, tokens: int) -> int:
@@ -531,16 +553,19 @@ def ttt_qk_norm_rope_backward(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, 
     """Backward of ttt_qk_norm_rope: dq, dk (activation dtype) and dq_weight, dk_weight (fp32
     [head_dim], or None); work: device tensor of at least ttt_qk_norm_rope_backward_work bytes
     (see include/ttt_attention.h)."""
-    import torch
-    dev, st = _here(stream)
-    dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
+    torch, dev, st = _here(stream)
+    D, dt = cfg.head_dim, torch.bfloat16 if cfg.act == 1 else torch.float32
+    wq, wk = cfg.q_heads * D, cfg.k_heads * D
     f32 = torch.float32
     _check(lib().ttt_qk_norm_rope_backward(
-        ctypes.byref(cfg), _arg(q, "q", dt, nq, dev, False), ld_q, _arg(k, "k", dt, nk, dev, False), ld_k,
-        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev),
-        _arg(dq_out, "dq_out", dt, nq, dev, False), ld_dqo, _arg(dk_out, "dk_out", dt, nk, dev, False), ld_dko,
-        _arg(dq, "dq", dt, nq, dev, False), ld_dq, _arg(dk, "dk", dt, nk, dev, False), ld_dk,
-        _arg(dq_weight, "dq_weight", f32, cfg.head_dim, dev), _arg(dk_weight, "dk_weight", f32, cfg.head_dim, dev),
+        ctypes.byref(cfg), _rows(q, "q", dt, tokens, wq, ld_q, dev), ld_q,
+        _rows(k, "k", dt, tokens, wk, ld_k, dev), ld_k,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev, dt, torch),
+        _rows(dq_out, "dq_out", dt, tokens, wq, ld_dqo, dev), ld_dqo,
+        _rows(dk_out, "dk_out", dt, tokens, wk, ld_dko, dev), ld_dko,
+        _rows(dq, "dq", dt, tokens, wq, ld_dq, dev), ld_dq,
+        _rows(dk, "dk", dt, tokens, wk, ld_dk, dev), ld_dk,
+        _arg(dq_weight, "dq_weight", f32, D, dev), _arg(dk_weight, "dk_weight", f32, D, dev),
         *_work(work, dev), tokens, st))
 
 
@@ -570,6 +595,7 @@ def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
                      _arg(v_scale, "v_scale", torch.float32, heads, dev),
                      stride[0] if pages > 1 else heads * size * dim, pages, size, heads, dim, dtype, 0)
     c.tensors = (k, v, k_scale, v_scale)
+    c.device = dev
     return c
 
 
@@ -579,14 +605,16 @@ def ttt_qk_norm_rope_append(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, v,
     """ttt_qk_norm_rope of new tokens, keys and values going to the cache: slot int64 [tokens],
     page * page_size + place, or negative for a token that is not stored
     (see include/ttt_attention.h)."""
-    import torch
-    dev, st = _here(stream)
-    dt, nq, nk = _act_dtype(cfg), tokens * cfg.q_heads * cfg.head_dim, tokens * cfg.k_heads * cfg.head_dim
+    torch, dev, st = _here(stream)
+    D, dt = cfg.head_dim, torch.bfloat16 if cfg.act == 1 else torch.float32
+    wq, wk = cfg.q_heads * D, cfg.k_heads * D
     _check(lib().ttt_qk_norm_rope_append(
-        ctypes.byref(cfg), _arg(q, "q", dt, nq, dev, False), ld_q, _arg(k, "k", dt, nk, dev, False), ld_k,
-        _arg(v, "v", dt, nk, dev, False), ld_v, *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev),
-        ctypes.byref(cache), _arg(slot, "slot", torch.int64, tokens, dev), _arg(q_out, "q_out", dt, nq, dev, False),
-        ld_qo, tokens, st))
+        ctypes.byref(cfg), _rows(q, "q", dt, tokens, wq, ld_q, dev), ld_q,
+        _rows(k, "k", dt, tokens, wk, ld_k, dev), ld_k,
+        _rows(v, "v", dt, tokens, wk, ld_v, dev), ld_v,
+        *_rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev, dt, torch),
+        _cache(cache, dev), _arg(slot, "slot", torch.int64, tokens, dev),
+        _rows(q_out, "q_out", dt, tokens, wq, ld_qo, dev), ld_qo, tokens, st))
 
 
 def ttt_paged_attention_work(cache: ttt_kv_cache, seqs: int, heads: int, max_pages: int,
@@ -604,29 +632,28 @@ def ttt_paged_attention(q, ld_q: int, cache: ttt_kv_cache, table, lens, out, ld_
     """Attention of one new token per sequence over its cached tokens: table int32
     [seqs, max_pages], lens int32 [seqs]; window 0: all of them; scale 0: 1 / sqrt(head_dim);
     lse fp32 [seqs, heads] or None (see include/ttt_attention.h)."""
-    import torch
-    dev, st = _here(stream)
-    bf, n = torch.bfloat16, seqs * heads * cache.head_dim
+    torch, dev, st = _here(stream)
+    bf, n = torch.bfloat16, heads * cache.head_dim
     _check(lib().ttt_paged_attention(
-        _arg(q, "q", bf, n, dev, False), ld_q, ctypes.byref(cache),
+        _rows(q, "q", bf, seqs, n, ld_q, dev), ld_q, _cache(cache, dev),
         _arg(table, "table", torch.int32, seqs * max_pages, dev), _arg(lens, "lens", torch.int32, seqs, dev),
-        _arg(out, "out", bf, n, dev, False), ld_out, _arg(lse, "lse", torch.float32, seqs * heads, dev), seqs,
-        heads, max_pages, window, scale, *_work(work, dev), st))
+        _rows(out, "out", bf, seqs, n, ld_out, dev), ld_out,
+        _arg(lse, "lse", torch.float32, seqs * heads, dev), seqs, heads, max_pages, window, scale,
+        *_work(work, dev), st))
 
 
 def ttt_window_attention_lse(q, k, v, ld: int, out, ld_out: int, lse, batch: int, heads: int,
                              seq_len: int, window: int, mode="sliding", stream=None) -> None:
     """ttt_window_attention that also stores lse, fp32 [batch, heads, seq_len], for the backward
     (see include/ttt_attention.h)."""
-    import torch
     m = WINDOW[mode] if isinstance(mode, str) else int(mode)
-    dev, st = _here(stream)
-    bf, rows = torch.bfloat16, batch * heads * seq_len
-    n = rows * ATTN_HEAD_DIM
+    torch, dev, st = _here(stream)
+    bf, rows, n = torch.bfloat16, batch * seq_len, heads * ATTN_HEAD_DIM
     _check(lib().ttt_window_attention_lse(
-        _arg(q, "q", bf, n, dev, False), _arg(k, "k", bf, n, dev, False), _arg(v, "v", bf, n, dev, False), ld,
-        _arg(out, "out", bf, n, dev, False), ld_out, _arg(lse, "lse", torch.float32, rows, dev), batch, heads,
-        seq_len, window, m, st))
+        _rows(q, "q", bf, rows, n, ld, dev), _rows(k, "k", bf, rows, n, ld, dev),
+        _rows(v, "v", bf, rows, n, ld, dev), ld,
+        _rows(out, "out", bf, rows, n, ld_out, dev), ld_out,
+        _arg(lse, "lse", torch.float32, rows * heads, dev), batch, heads, seq_len, window, m, st))
 
 
 def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout, ld_dout: int, dq,
@@ -634,14 +661,13 @@ def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout,
                                   window: int, mode="sliding", stream=None) -> None:
     """Backward of ttt_window_attention: dq, dk, dv with row stride ld_d; work fp32
     [batch, heads, seq_len] (see include/ttt_attention.h)."""
-    import torch
     m = WINDOW[mode] if isinstance(mode, str) else int(mode)
-    dev, st = _here(stream)
-    bf, f32, rows = torch.bfloat16, torch.float32, batch * heads * seq_len
-    n = rows * ATTN_HEAD_DIM
+    torch, dev, st = _here(stream)
+    bf, f32, rows, n = torch.bfloat16, torch.float32, batch * seq_len, heads * ATTN_HEAD_DIM
     _check(lib().ttt_window_attention_backward(
-        _arg(q, "q", bf, n, dev, False), _arg(k, "k", bf, n, dev, False), _arg(v, "v", bf, n, dev, False), ld,
-        _arg(out, "out", bf, n, dev, False), ld_out, _arg(lse, "lse", f32, rows, dev),
-        _arg(dout, "dout", bf, n, dev, False), ld_dout, _arg(dq, "dq", bf, n, dev, False),
-        _arg(dk, "dk", bf, n, dev, False), _arg(dv, "dv", bf, n, dev, False), ld_d, _arg(work, "work", f32, rows, dev),
-        batch, heads, seq_len, window, m, st))
+        _rows(q, "q", bf, rows, n, ld, dev), _rows(k, "k", bf, rows, n, ld, dev),
+        _rows(v, "v", bf, rows, n, ld, dev), ld,
+        _rows(out, "out", bf, rows, n, ld_out, dev), ld_out, _arg(lse, "lse", f32, rows * heads, dev),
+        _rows(dout, "dout", bf, rows, n, ld_dout, dev), ld_dout, _rows(dq, "dq", bf, rows, n, ld_d, dev),
+        _rows(dk, "dk", bf, rows, n, ld_d, dev), _rows(dv, "dv", bf, rows, n, ld_d, dev), ld_d,
+        _arg(work, "work", f32, rows * heads, dev), batch, heads, seq_len, window, m, st))
