@@ -190,16 +190,18 @@ int64_t bwd_work_bytes(const ttt_rope_config* c, int64_t tokens) {
 
 // Parts that each sequence's tokens are split into, at most.  The lengths are on the device, so
 // the rule goes by the longest span a sequence may have.
-//   - enough workgroups to fill the CUs once, as many to a CU as the kernel's registers and LDS
-//     let in (paged_per_cu): more parts than that only make the join longer (one 131072-token
-//     sequence of 8 heads: 99 us at 512 workgroups, 106 at 2048);
+//   - enough workgroups to fill the CUs once, as many to a CU as keep the memory busy
+//     (paged_per_cu): more parts than that only make the join longer (one 131072-token sequence
+//     of 8 heads: 99 us at 512 workgroups, 106 at 2048).  Room is for one more of heads of 64 and
+//     of bf16 heads of 256 (one sequence of 131072 tokens, heads of 64: 46.5 us, 49.3 with three
+//     to a CU; of 65536, heads of 256: 49.6 us, 54.0 with two);
 //   - no part above PG_MAX_PART tokens, so that one long sequence among short ones is not left
 //     to a few workgroups (64 sequences up to 8192 tokens: 213 us, against 219 unsplit), while
 //     the launch stays below PG_WGS_MOST workgroups, most of which a ragged batch leaves empty;
 //   - no part below PG_MIN_PART tokens: two steps of every wave.
 constexpr int64_t PG_MAX_PART = 2048, PG_MIN_PART = 256, PG_WGS_MOST = 16384, NUM_CU = 256;
 
-int64_t paged_per_cu(int32_t D, bool e4m3) { return D == 64 ? 3 : D == 128 ? (e4m3 ? 3 : 2) : 1; }
+int64_t paged_per_cu(int32_t D, bool e4m3) { return D == 128 ? (e4m3 ? 3 : 2) : D == 64 || e4m3 ? 2 : 1; }
 
 int32_t paged_splits(int64_t wgs, int64_t span, int64_t per_cu) {
   if (wgs == 0) return 1;

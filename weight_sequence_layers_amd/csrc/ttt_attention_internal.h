@@ -67,8 +67,7 @@ hipError_t launch_rope_dw(const RopeDwArgs& a, hipStream_t st);
 
 // ------------------------------------------------------------------------ paged attention
 constexpr int PG_NT = 256, PG_WAVES = 4;
-constexpr int PG_STEP = 32;                      // keys of a wave's step
-constexpr int PG_BLOCK = PG_STEP * PG_WAVES;     // keys of a workgroup's step
+constexpr int PG_BLOCK = 128;                    // tokens of a part: a multiple of this
 constexpr int PG_HEADS = 16;                     // query heads of a workgroup
 
 struct PagedArgs {
@@ -108,7 +107,7 @@ __host__ __device__ inline int64_t paged_row(int32_t page, int32_t pages, int64_
 }
 
 // Tokens that each part of a sequence's span takes when n tokens are split into at most
-// `splits` parts: whole workgroup steps.
+// `splits` parts: whole steps of a workgroup.
 __host__ __device__ inline int32_t paged_part(int32_t n, int32_t splits) {
   const int32_t steps = (n + PG_BLOCK - 1) / PG_BLOCK;
   return (steps + splits - 1) / splits * PG_BLOCK;

@@ -8,7 +8,7 @@
 // Every cached byte is read once: the memory bounds it.  A workgroup takes one key head of one
 // sequence, the query heads that share it (up to 16, the columns of a 16 x 16 x 32 MFMA; with
 // fewer the spare columns cost nothing that counts) and one part of the tokens; its four waves
-// take 32 tokens in turn.  A step's rows are loaded into registers in the order they lie in
+// take 32 tokens in turn (16 of heads of 256).  A step's rows are loaded into registers in the order they lie in
 // memory while the step before is computed, and put into the wave's own LDS tiles: K is read
 // back along its rows as the A operand of S^T = K Q^T, so each lane holds 8 tokens of one query
 // head and P^T is already laid out as the second product's B operand; V is read transposed.
@@ -62,22 +62,33 @@ __device__ __forceinline__ int kt_chunk(int r, int c) {
   return c ^ (r & 15);
 }
 
+// the first four of a lane's eight probabilities
+__device__ __forceinline__ s16x4 low4(bf16x8 p) {
+  const s16x8 x = __builtin_bit_cast(s16x8, p);
+  return __builtin_shufflevector(x, x, 0, 1, 2, 3);
+}
+
 template <int D, bool E4>
 struct PagedShape {
   static constexpr int RB = D * (E4 ? 1 : 2);         // bytes of a cached row
-  static constexpr int KL = PG_STEP * RB / 16 / 64;   // 16-byte loads per lane of 32 rows
+  static constexpr int STEP = D == 256 ? 16 : 32;     // tokens of a wave's step
+  static constexpr int BLOCK = STEP * PG_WAVES;       // and of the workgroup's
+  static_assert(PG_BLOCK % BLOCK == 0, "a part is whole steps");
+  static constexpr int KL = STEP * RB / 16 / 64;      // 16-byte loads per lane of a step's rows
   static constexpr int LR = RB / 16;                  // lanes of a row
   static constexpr int RPI = 64 / LR;                 // rows per load
   static constexpr int KS = D / 32;                   // MFMA steps along D
-  static constexpr int KT = PG_STEP * RB;             // bytes of a wave's K tile, as cached
-  static constexpr int VT = PG_STEP * D * 2;          // bytes of a wave's V tile, bf16
+  static constexpr int KT = STEP * RB;                // bytes of a wave's K tile, as cached
+  static constexpr int VT = STEP * D * 2;             // bytes of a wave's V tile, bf16
 };
 
 // Registers held to three waves per SIMD for e4m3 heads of 128 (the compiler takes two's worth
 // by itself): half the bytes per step leave too few in flight with two (96 windows of 2048:
-// 47.7 -> 42.2 us).
+// 47.7 -> 42.2 us).  For heads of 256 to two, with steps of 16 tokens: steps of 32 fill the LDS
+// and the registers with one (16 sequences up to 8192 tokens, 4 key heads: bf16 64.8 -> 59.7 us,
+// e4m3 49.1 -> 39.7 us; one of 65536: bf16 53.6 -> 49.6 us).
 template <int D, bool E4>
-__global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedArgs a) {
+__global__ __launch_bounds__(PG_NT, D == 256 ? 2 : D == 128 && E4 ? 3 : 1) void k_paged(PagedArgs a) {
   using S = PagedShape<D, E4>;
   // the waves' K and V tiles, and after the loop their sums
   constexpr int JOIN = PG_WAVES * PG_HEADS * D * 4;
@@ -120,14 +131,14 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
 
   const int32_t* tab = a.table + (int64_t)seq * a.max_pages;
   const char* zero = reinterpret_cast<const char*>(&k_zero_row);
-  // lane l < 32 of a step at token k0: the page of token k0 + l, and its row's byte offset (-1
+  // lane l < STEP of a step at token k0: the page of token k0 + l, and its row's byte offset (-1
   // for none)
   auto page_of = [&](int k0) __attribute__((always_inline)) {
-    const int key = k0 + (lane & 31);
+    const int key = k0 + (lane & (S::STEP - 1));
     return key < b1 ? tab[key / a.page_size] : -1;
   };
   auto row_of = [&](int page, int k0) __attribute__((always_inline)) {
-    return paged_row(page, a.pages, a.page_bytes, kh, a.page_size, (k0 + (lane & 31)) % a.page_size, S::RB);
+    return paged_row(page, a.pages, a.page_bytes, kh, a.page_size, (k0 + (lane & (S::STEP - 1))) % a.page_size, S::RB);
   };
   auto at_lane = [](int64_t x, int l) __attribute__((always_inline)) {
     const int lo32 = __shfl((int)(uint32_t)x, l, 64), hi32 = __shfl((int)(x >> 32), l, 64);
@@ -153,14 +164,14 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
   char* kt = lds + w * (S::KT + S::VT);
   char* vt = kt + S::KT;
 
-  int k0 = b0 + w * PG_STEP;
+  int k0 = b0 + w * S::STEP;
   // Page numbers are loaded before the rows of the step ahead of theirs: loads return in order,
   // so waiting for them does not wait for rows still on their way.
   const int page0 = page_of(k0);
-  int npage = page_of(k0 + PG_BLOCK);
+  int npage = page_of(k0 + S::BLOCK);
   int64_t row = row_of(page0, k0);
   load(row);
-  for (; k0 < b1; k0 += PG_BLOCK) {
+  for (; k0 < b1; k0 += S::BLOCK) {
     // this step's rows into the wave's tiles, the next step's on their way
 #pragma unroll
     for (int i = 0; i < S::KL; ++i) {
@@ -180,17 +191,19 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
     }
     // tokens without a row (past the end, a page outside the cache) are left out
     const uint32_t have = (uint32_t)__ballot(row >= 0);
-    row = row_of(npage, k0 + PG_BLOCK);
-    npage = page_of(k0 + 2 * PG_BLOCK);
+    row = row_of(npage, k0 + S::BLOCK);
+    npage = page_of(k0 + 2 * S::BLOCK);
     load(row);
     wave_order();
     // scores: element v of tile t is token k0 + 16 t + 4 g + v of query head n
-    f32x4 sc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    constexpr int NT = S::STEP / 16;
+    f32x4 sc[NT];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < NT; ++t) {
       const int r = 16 * t + n;
+      sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < S::KL / 2; ++s) {
+      for (int s = 0; s < S::RB / 64; ++s) {
         const u32x4 x = *reinterpret_cast<const u32x4*>(kt + r * S::RB + (kt_chunk<S::RB>(r, 4 * s + g) << 4));
         if constexpr (E4) {
           sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -204,7 +217,7 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
     }
     float mx = -INFINITY;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         sc[t][v] = (have >> (16 * t + 4 * g + v)) & 1 ? sc[t][v] * c2 : -INFINITY;
@@ -225,7 +238,7 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
     // two bf16 numbers per probability: what the first leaves, the second holds, 16 bits in all
     bf16x8 ph, pl;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const float p = __builtin_amdgcn_exp2f(sc[t][v] - mref);
@@ -239,15 +252,20 @@ __global__ __launch_bounds__(PG_NT, D == 128 && E4 ? 3 : 1) void k_paged(PagedAr
     for (int mt = 0; mt < D / 16; ++mt) {
       s16x4 part2[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < NT; ++t) {
         const int r = 16 * t + 4 * g + (n >> 2), d = 16 * mt + 4 * (n & 3);
         const char* p = vt + r * D * 2 + (vt_chunk<D>(r, d >> 3) << 4) + (d & 7) * 2;
         part2[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
       }
-      const s16x8 vv = __builtin_shufflevector(part2[0], part2[1], 0, 1, 2, 3, 4, 5, 6, 7);
-      const bf16x8 vf = __builtin_bit_cast(bf16x8, vv);
-      o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph, o[mt], 0, 0, 0);
-      o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, o[mt], 0, 0, 0);
+      if constexpr (NT == 2) {
+        const s16x8 vv = __builtin_shufflevector(part2[0], part2[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, vv);
+        o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, ph, o[mt], 0, 0, 0);
+        o[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pl, o[mt], 0, 0, 0);
+      } else {
+        o[mt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(part2[0], low4(ph), o[mt], 0, 0, 0);
+        o[mt] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(part2[0], low4(pl), o[mt], 0, 0, 0);
+      }
     }
     wave_order();
   }
