@@ -308,7 +308,7 @@ __global__ __launch_bounds__(ROPE_NT) void k_rope_bwd(RopeArgs a) {
   }
   if (!a.part) return;
   // the groups' sums: 16 values per thread through LDS (cs and sn hold 16 * 256 floats
-  // together), then one thread per column adds the groups' values in order, in 64 bits: 32 to 256
+  // together), then one thread per column adds the groups' values in order, in 64 bits: up to 256
   // roundings of a growing sum in fp32 are most of the error (32768 tokens, 8 heads of 128: 1.6e-7
   // of the gradient's norm, 1.1e-7 with this sum in 64 bits, at the same time)
   __syncthreads();
