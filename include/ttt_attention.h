@@ -68,7 +68,8 @@ ttt_status ttt_validate_rope_config(const ttt_rope_config* cfg);
  *   q, k     element e of head h of token t at  t * ld + h * head_dim + e
  *   q_out, k_out  the same with ld_qo, ld_ko.  q_out may be q itself (ld_qo == ld_q) and k_out
  *            k; other overlaps of an output with an input (weights, freq and pos
- *            among them) or the other output are TTT_E_CONFIG.  q and k may be parts of one projection's rows.
+ *            among them) or the other output are TTT_E_CONFIG.  q and k may be parts of one
+ *            projection's rows.
  *   q_weight, k_weight  [head_dim] learned scales, or NULL for ones (must be NULL without norm)
  *   freq     fp32 [axes][rot_dim / 2], radians per position: a pair that turns with one axis
  *            holds zeros for the others (may be NULL with rot_dim 0)
@@ -182,7 +183,8 @@ ttt_status ttt_paged_attention(const void* q, int64_t ld_q, const ttt_kv_cache* 
  * [batch][heads][seq_len] (fp32), the log of each row's sum of exponentials of the scaled scores,
  * for the backward.  Scores, softmax and sums are fp32, the probabilities are rounded to bf16 for
  * the product with v and summed before that.  Limits as there, and ld_out at most 2^28; out and
- * lse may not overlap the inputs or each other.  All values must be finite.
+ * lse may not overlap the inputs or each other.  All values, and the scores they give, must be
+ * finite.
  */
 ttt_status ttt_window_attention_lse(const void* q, const void* k, const void* v, int64_t ld,
                                     void* out, int64_t ld_out, float* lse, int32_t batch,
@@ -200,8 +202,8 @@ ttt_status ttt_window_attention_lse(const void* q, const void* k, const void* v,
  * their products.
  * Every sum has one order: the results are the same from run to run.  work: fp32
  * [batch][heads][seq_len] workspace.  The gradients and work may not overlap the inputs or
- * each other.  All values must be finite.  Limits as for ttt_window_attention, ld_dout
- * as ld; ld_out and ld_d at most 2^28.
+ * each other.  All values, and the scores they give, must be finite.  Limits as for
+ * ttt_window_attention, ld_dout as ld; ld_out and ld_d at most 2^28.
  */
 ttt_status ttt_window_attention_backward(const void* q, const void* k, const void* v,
                                          int64_t ld, const void* out, int64_t ld_out,
