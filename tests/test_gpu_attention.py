@@ -475,6 +475,17 @@ def test_paged_attention_matches_oracle(kw, window):
     p.check(window)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window", [0, 1, 17, 64])
+def test_paged_attention_heads_of_256_around_a_step(dtype, window):
+    """Lengths around the 16 tokens of a wave's step and the 64 of a workgroup's, whose last page
+    numbers lie outside the cache for one of them."""
+    p = Paged([0, 1, 15, 16, 17, 31, 63, 64, 65, 129, 400], 4, 2, 256, 7, dtype=dtype)
+    p.table[9, 18] = -1        # tokens 126 .. 128
+    p.call(window)
+    p.check(window)
+
+
 def test_paged_attention_large_scores_and_own_scale():
     p = Paged([700, 40], 4, 2, 128, 16, qscale=30.0)
     p.call(scale=0.3)
