@@ -46,10 +46,11 @@ typedef enum { TTT_WINDOW_SLIDING = 0, TTT_WINDOW_BLOCK = 1 } ttt_window_mode;
  * out + (b * seq_len + t) * ld_out + h * 128 + e  for the output (bf16), so q, k and v
  * may be thirds of one projection's output rows; out may not overlap them (TTT_E_CONFIG).
  * Limits: batch, heads >= 1; window >= 1;
- * 0 <= seq_len < 2^31; ld, ld_out >= heads * 128 and multiples of 8; ld < 2^24.  The
- * scores and their softmax are fp32; the probabilities are rounded to bf16 for the
- * product with v, and the normaliser sums the rounded values, so each output is a convex
- * combination of the values in its window.
+ * 0 <= seq_len < 2^31; ceil(seq_len / 128) * batch * heads below 2^24 (a launch's threads
+ * are counted in 32 bits); ld, ld_out >= heads * 128 and multiples of 8; ld < 2^24.  The
+ * scores and their softmax are fp32; the probabilities are rounded to bf16 for the product
+ * with v, and the normaliser sums the rounded values, so each output is a convex combination
+ * of the values in its window.
  */
 ttt_status ttt_window_attention(const void* q, const void* k, const void* v, int64_t ld,
                                 void* out, int64_t ld_out, int32_t batch, int32_t heads,

@@ -288,3 +288,22 @@ def test_scales_of_an_e4m3_cache_are_not_written_over():
         assert append(cache(dtype=1, **{n: P(21).value})) == 4
         for at in (3, 4):
             assert paged(cache(dtype=1, **{n: P(at).value})) == 4
+
+
+@pytest.mark.parametrize("fn", ["lse", "backward", ""])
+@pytest.mark.parametrize("batch,heads,seq_len,code", [
+    ((1 << 24) - 1, 1, 128, 1), (1 << 24, 1, 1, 2), ((1 << 23) + 1, 1, 129, 2), (1 << 12, 1 << 12, 1, 2),
+    ((1 << 12) - 1, 1 << 12, 1, 1), (1, 1, (1 << 31) - 128, 1), (1, 1, (1 << 31) - 127, 2),
+    (1 << 24, 1 << 16, (1 << 31) - 1, 2),     # the product of the three passes 64 bits
+    ((1 << 31) - 1, (1 << 17) - 1, (1 << 31) - 1, 2), ((1 << 31) - 1, 1, 0, 0),
+])
+def test_window_launches_count_their_threads_in_32_bits(fn, batch, heads, seq_len, code):
+    """256 threads to every 128 rows of a head: 2^24 such workgroups are refused before any launch,
+    one fewer passes on to the pointers (code 1: q is NULL)."""
+    ld = heads * 128
+    kw = dict(q=None, ld=ld, ld_out=ld, batch=batch, heads=heads, seq_len=seq_len)
+    if fn == "":
+        got = W.lib().ttt_window_attention(None, P(0), P(0), ld, P(1), ld, batch, heads, seq_len, 8, 0, None)
+    else:
+        got = window(fn, **kw, **(dict(ld_dout=ld, ld_d=ld) if fn == "backward" else {}))
+    assert got == code, W.lib().ttt_last_error()

@@ -16,6 +16,7 @@ using namespace ttt;
 
 namespace {
 constexpr int64_t INT31 = (int64_t)1 << 31;
+constexpr int64_t ATT_WGS = (int64_t)1 << 24;   // workgroups of 256 threads, fewer than these
 }
 
 namespace ttt {
@@ -33,8 +34,11 @@ ttt_status check_attention(int64_t ld, int64_t ld_out, int32_t batch, int32_t he
   if (ld_out < (int64_t)heads * ATT_D || ld_out % 8)
     return failf(TTT_E_SHAPE, "ld_out %lld: at least heads * 128 and a multiple of 8",
                  (long long)ld_out);
-  const int64_t total = (T + ATT_Q - 1) / ATT_Q * heads * batch;
-  if (total >= INT31) return failf(TTT_E_SHAPE, "batch * heads * seq_len too large");
+  // 256 threads to a workgroup of ATT_Q rows, and a launch's threads are counted in 32 bits; by
+  // division, since the three factors' product may pass 64
+  const int64_t blocks = (T + ATT_Q - 1) / ATT_Q;
+  if (blocks && batch > (ATT_WGS - 1) / blocks / heads)
+    return failf(TTT_E_SHAPE, "ceil(seq_len / 128) * batch * heads: below 2^24");
   return TTT_OK;
 }
 
