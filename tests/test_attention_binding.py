@@ -1,0 +1,45 @@
+"""The binding's own checks of tensor layouts, on CPU tensors (device number -1): what the
+library would read with other strides than the tensor has is refused."""
+import pytest
+import torch
+
+import weight_sequence_layers_amd as W
+
+CPU = -1
+
+
+def table(got, shape):
+    t = torch.zeros(got, dtype=torch.int32)
+    return W._table(t, "table", torch.int32, shape, CPU), t.data_ptr()
+
+
+@pytest.mark.parametrize("got,shape", [
+    ((4, 7), (4, 7)), ((28,), (4, 7)), ((30,), (4, 7)), ((6, 7), (4, 7)), ((1, 28), (4, 7)), ((1, 4, 7), (4, 7)),
+    ((1, 9), (1, 7)), ((9, 1), (1, 7)), ((2, 5), (1, 7)), ((3, 2, 7), (3, 14)), ((5, 1), (5, 1)),
+    ((2, 3, 5), (2, 3, 5)), ((6, 5), (2, 3, 5)), ((30,), (2, 3, 5)), ((7, 3, 5), (2, 3, 5)), ((2, 1, 5), (2, 1, 5)),
+    ((2, 5), (2, 1, 5)), ((4, 9), (0, 7)), ((4, 9), (4, 0)),
+])
+def test_tables_read_as_they_lie(got, shape):
+    p, want = table(got, shape)
+    assert p == want
+
+
+@pytest.mark.parametrize("got,shape", [
+    ((4, 8), (4, 7)),           # a page table wider than max_pages
+    ((7, 4), (4, 7)), ((2, 9), (2, 7)), ((3, 9), (3, 7)),     # positions behind the last token
+    ((5, 2), (2, 5)), ((2, 5, 3), (2, 3, 5)), ((3, 2, 5), (2, 3, 5)), ((2, 4, 5), (2, 3, 5)), ((6, 8), (2, 3, 5)),
+    ((5, 6), (2, 3, 5)), ((4, 6, 5), (4, 3, 5)),
+])
+def test_tables_of_another_layout_are_refused(got, shape):
+    with pytest.raises(W.TTTError) as e:
+        table(got, shape)
+    assert e.value.status == 2 and str(list(got)) in str(e.value) and str(list(shape)) in str(e.value)
+
+
+def test_tables_too_small_or_of_another_type_are_refused():
+    for t, code in ((torch.zeros(27, dtype=torch.int32), 2), (torch.zeros(4, 7), 3),
+                    (torch.zeros(4, 14, dtype=torch.int32)[:, ::2], 2)):
+        with pytest.raises(W.TTTError) as e:
+            W._table(t, "table", torch.int32, (4, 7), CPU)
+        assert e.value.status == code
+    assert W._table(None, "table", torch.int32, (4, 7), CPU) is None

@@ -917,3 +917,40 @@ def test_binding_refuses_rows_past_the_memory():
         with pytest.raises(W.TTTError) as e:
             bad()
         assert e.value.status == code
+
+
+def test_binding_refuses_tables_of_another_layout():
+    """Tables whose rows would be read with another length than they have: a page table wider than
+    max_pages, positions for more tokens than the call's, statistics with their axes turned."""
+    p = Paged([40, 33, 20], 4, 2, 64, 16)
+    wide = torch.nn.functional.pad(p.table, (0, 5), value=-1).contiguous()
+    turned = torch.zeros(4, 3, device=DEV)
+    r = Rope(T=4, Hq=2, Hk=1, D=64, rot=64, axes=2)
+    w = Window(2, 3, 5, 2, "sliding")
+    stat, pos, lse = torch.zeros(2, 5, 3, device=DEV), torch.cat((r.pos, r.pos), 1).contiguous(), p.lse
+
+    def attend(table, lse):
+        W.ttt_paged_attention(p.q, p.q.stride(0), p.cache, table, p.lens, p.out, p.out.stride(0), lse, 3, 4,
+                              p.width, 0, 0.0, p.work())
+
+    def bad_pos():
+        r.pos = pos
+        r.call()
+
+    def bad_stat(call):
+        w.lse = stat
+        call()
+    p.call()
+    w.forward()
+    for bad in (lambda: attend(wide, lse), lambda: attend(p.table, turned), bad_pos, lambda: bad_stat(w.forward),
+                lambda: bad_stat(w.backward)):
+        with pytest.raises(W.TTTError) as e:
+            bad()
+        assert e.value.status == 2
+    attend(p.table.flatten(), lse)
+    p.check()
+    # one sequence: the rest of its row is not read
+    one = Paged([40], 4, 2, 64, 16)
+    W.ttt_paged_attention(one.q, one.q.stride(0), one.cache, torch.nn.functional.pad(one.table, (0, 5)), one.lens,
+                          one.out, one.out.stride(0), one.lse, 1, 4, one.width, 0, 0.0, one.work())
+    one.check()

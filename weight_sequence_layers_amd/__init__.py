@@ -476,6 +476,30 @@ def _arg(t, name: str, dtype, n: int, dev: int, dense: bool = True) -> Optional[
     return t.data_ptr()
 
 
+def _table(t, name: str, dtype, shape, dev: int) -> Optional[int]:
+    """_arg of a table read as `shape`: flat, or of a shape whose rows fall where those of `shape`
+    do (more rows may follow). A wider table, or one with its axes in another order, would be
+    read with the wrong row length."""
+    n = 1
+    for x in shape:
+        n *= x
+    p = _arg(t, name, dtype, n, dev)
+    if p is not None and n and t.dim() > 1 and t.shape != shape:
+        def apart(dims):   # elements between neighbours along each dim of more than one
+            at, m = [], 1
+            for x in reversed(dims):
+                if x > 1:
+                    at.append(m)
+                    m *= x
+            return at
+        have, want = apart(t.shape), apart(shape)
+        if len(have) < len(want):
+            want = want[:len(have)]   # flat, or some of the outer dims as one
+        if not set(have).issuperset(want):
+            raise TTTError(2, f"{name} is {list(t.shape)}, read as {list(shape)}")
+    return p
+
+
 def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Optional[int]:
     """_arg of a matrix of rows ld elements apart, the last of which must end within a contiguous
     tensor, or within the memory that another is a view of (a third of a projection's rows)."""
@@ -518,8 +542,8 @@ def ttt_validate_rope_config(cfg: ttt_rope_config) -> None:
 def _rope_inputs(cfg, q_weight, k_weight, freq, pos, tokens, dev, dt, torch):
     D, half, axes = cfg.head_dim, cfg.rot_dim // 2, cfg.axes
     return (_arg(q_weight, "q_weight", dt, D, dev), _arg(k_weight, "k_weight", dt, D, dev),
-            _arg(freq, "freq", torch.float32, axes * half, dev),
-            _arg(pos, "pos", torch.int32, axes * tokens if half else 0, dev))
+            _table(freq, "freq", torch.float32, (axes, half), dev),
+            _table(pos, "pos", torch.int32, (axes, tokens if half else 0), dev))
 
 
 def ttt_qk_norm_rope(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, q_weight, k_weight, freq,
@@ -636,9 +660,9 @@ def ttt_paged_attention(q, ld_q: int, cache: ttt_kv_cache, table, lens, out, ld_
     bf, n = torch.bfloat16, heads * cache.head_dim
     _check(lib().ttt_paged_attention(
         _rows(q, "q", bf, seqs, n, ld_q, dev), ld_q, _cache(cache, dev),
-        _arg(table, "table", torch.int32, seqs * max_pages, dev), _arg(lens, "lens", torch.int32, seqs, dev),
+        _table(table, "table", torch.int32, (seqs, max_pages), dev), _arg(lens, "lens", torch.int32, seqs, dev),
         _rows(out, "out", bf, seqs, n, ld_out, dev), ld_out,
-        _arg(lse, "lse", torch.float32, seqs * heads, dev), seqs, heads, max_pages, window, scale,
+        _table(lse, "lse", torch.float32, (seqs, heads), dev), seqs, heads, max_pages, window, scale,
         *_work(work, dev), st))
 
 
@@ -653,7 +677,7 @@ def ttt_window_attention_lse(q, k, v, ld: int, out, ld_out: int, lse, batch: int
         _rows(q, "q", bf, rows, n, ld, dev), _rows(k, "k", bf, rows, n, ld, dev),
         _rows(v, "v", bf, rows, n, ld, dev), ld,
         _rows(out, "out", bf, rows, n, ld_out, dev), ld_out,
-        _arg(lse, "lse", torch.float32, rows * heads, dev), batch, heads, seq_len, window, m, st))
+        _table(lse, "lse", torch.float32, (batch, heads, seq_len), dev), batch, heads, seq_len, window, m, st))
 
 
 def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout, ld_dout: int, dq,
@@ -667,7 +691,8 @@ def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout,
     _check(lib().ttt_window_attention_backward(
         _rows(q, "q", bf, rows, n, ld, dev), _rows(k, "k", bf, rows, n, ld, dev),
         _rows(v, "v", bf, rows, n, ld, dev), ld,
-        _rows(out, "out", bf, rows, n, ld_out, dev), ld_out, _arg(lse, "lse", f32, rows * heads, dev),
+        _rows(out, "out", bf, rows, n, ld_out, dev), ld_out,
+        _table(lse, "lse", f32, (batch, heads, seq_len), dev),
         _rows(dout, "dout", bf, rows, n, ld_dout, dev), ld_dout, _rows(dq, "dq", bf, rows, n, ld_d, dev),
         _rows(dk, "dk", bf, rows, n, ld_d, dev), _rows(dv, "dv", bf, rows, n, ld_d, dev), ld_d,
         _arg(work, "work", f32, rows * heads, dev), batch, heads, seq_len, window, m, st))
