@@ -43,3 +43,35 @@ def test_tables_too_small_or_of_another_type_are_refused():
             W._table(t, "table", torch.int32, (4, 7), CPU)
         assert e.value.status == code
     assert W._table(None, "table", torch.int32, (4, 7), CPU) is None
+
+
+def rows(t, n, width, ld):
+    return W._rows(t, "x", t.dtype, n, width, ld, CPU)
+
+
+def test_rows_read_as_they_lie():
+    x = torch.zeros(5, 48)
+    for t, n, width, ld in (
+            (x, 5, 48, 48), (x, 5, 16, 48), (x[:, 16:], 5, 16, 48), (x[:, 32:], 5, 16, 48), (x[1:3, :16], 2, 16, 48),
+            (x.view(5, 3, 16), 5, 48, 48), (x.view(5, 3, 16)[:, 1], 5, 16, 48), (x.view(5, 3, 16)[:, 1:], 5, 32, 48),
+            (x.view(15, 16), 15, 16, 16), (x.view(5, 3, 16), 15, 16, 16), (x.flatten(), 5, 16, 48),
+            (x.flatten(), 3, 40, 60), (x.view(1, 5, 48)[..., 16:], 5, 32, 48), (x[:1], 1, 16, 1000), (x[2:3, 8:24], 1, 16, 48),
+            (torch.zeros(2, 5, 48)[..., 16:], 10, 32, 48), (torch.zeros(2, 5, 3, 16)[:, :, 1], 10, 16, 48),
+            (torch.zeros(2, 1, 48)[..., 16:], 2, 32, 48), (torch.zeros(5, 16, 1)[:, :, 0], 5, 16, 16), (x, 0, 48, 64)):
+        assert rows(t, n, width, ld) == t.data_ptr()
+    assert W._rows(None, "x", torch.float32, 5, 48, 48, CPU) is None
+
+
+def test_rows_of_another_layout_are_refused():
+    x = torch.zeros(6, 6, 16)
+    for t, n, width, ld in (
+            (x.transpose(0, 1), 6, 96, 96),                 # [heads, tokens, dim] as [tokens, heads, dim]
+            (torch.zeros(96, 6).t(), 6, 96, 96),            # columns for rows
+            (torch.zeros(6, 192)[:, ::2], 6, 96, 96), (torch.zeros(6, 192)[:, ::2], 6, 96, 192),
+            (torch.zeros(12, 96)[::2], 6, 96, 96),          # every second row
+            (torch.zeros(6, 192), 6, 96, 96),               # wider rows than said
+            (torch.zeros(4, 5, 96)[:, :3], 12, 96, 96),     # sequences further apart than their rows
+            (torch.zeros(1000, 96)[:1].expand(6, 96), 6, 96, 96), (torch.zeros(6, 96, 2)[..., 0], 6, 96, 96)):
+        with pytest.raises(W.TTTError) as e:
+            rows(t, n, width, ld)
+        assert e.value.status == 2 and str(ld) in str(e.value)

@@ -954,3 +954,22 @@ def test_binding_refuses_tables_of_another_layout():
     W.ttt_paged_attention(one.q, one.q.stride(0), one.cache, torch.nn.functional.pad(one.table, (0, 5)), one.lens,
                           one.out, one.out.stride(0), one.lse, 1, 4, one.width, 0, 0.0, one.work())
     one.check()
+
+
+def test_binding_refuses_rows_of_another_layout():
+    """Tensors whose own rows are not ld apart, which would be read as if they were."""
+    T, Hn, D = 4, 4, 64     # as many tokens as heads: every count fits
+    r = Rope(T=T, Hq=Hn, Hk=Hn, D=D, rot=64)
+    n = Hn * D
+    qo, ko = (torch.zeros(T, n, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    x = r.x[:, :n].contiguous().view(T, Hn, D)
+
+    def call(q, qo):
+        W.ttt_qk_norm_rope(r.cfg, q, n, r.k, r.ld, r.qw, r.kw, r.freq, r.pos, qo, n, ko, n, T)
+    call(x, qo)
+    r.check(torch.cat((qo, torch.full_like(qo, 7.0))), torch.cat((ko, torch.full_like(ko, 7.0))))
+    turned = torch.zeros(Hn, T, D, dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    for q, o in ((x.transpose(0, 1), qo), (x, turned), (torch.zeros(T, 2 * n, dtype=torch.bfloat16, device=DEV), qo)):
+        with pytest.raises(W.TTTError) as e:
+            call(q, o)
+        assert e.value.status == 2

@@ -480,11 +480,13 @@ def _table(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     """_arg of a table read as `shape`: flat, or of a shape whose rows fall where those of `shape`
     do (more rows may follow). A wider table, or one with its axes in another order, would be
     read with the wrong row length."""
+    if t is not None and t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     n = 1
     for x in shape:
         n *= x
     p = _arg(t, name, dtype, n, dev)
-    if p is not None and n and t.dim() > 1 and t.shape != shape:
+    if p is not None and n and t.dim() > 1:
         def apart(dims):   # elements between neighbours along each dim of more than one
             at, m = [], 1
             for x in reversed(dims):
@@ -500,13 +502,35 @@ def _table(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     return p
 
 
+def _rows_apart(t, ld: int) -> bool:
+    """Whether t's elements lie in rows ld apart: flat, or dims that are dense up to a row, then
+    one of stride ld, and dense in rows before it."""
+    at, found, dims = 1, False, 0
+    for n, s in zip(reversed(t.shape), reversed(t.stride())):
+        if n > 1:
+            dims += 1
+            if not found and s == ld and ld >= at:
+                at, found = ld, True
+            if s != at:
+                return False
+            at *= n
+    return found or dims < 2
+
+
 def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Optional[int]:
-    """_arg of a matrix of rows ld elements apart, the last of which must end within a contiguous
-    tensor, or within the memory that another is a view of (a third of a projection's rows)."""
+    """_arg of a matrix of rows ld elements apart: a flat tensor, or one whose own rows are. The
+    last must end within a contiguous tensor, or within the memory that another is a view of (a
+    third of a projection's rows)."""
     if t is None:
         return None
+    here = t.dtype is dtype and t.get_device() == dev
+    shape = t.shape
+    if here and len(shape) == 2 and rows <= shape[0] and width <= shape[1] and t.stride() == (ld, 1):
+        return t.data_ptr()   # most calls: the tests below cost 0.2 us a tensor
     last, have = (rows - 1) * ld + width, t.numel()
-    if have >= rows * width and t.dtype is dtype and t.get_device() == dev:
+    if here and have >= rows * width:
+        if rows > 1 and not _rows_apart(t, ld):
+            raise TTTError(2, f"{name}: {list(shape)} of strides {list(t.stride())}, read in rows {ld} apart")
         if not t.is_contiguous():
             have = t.untyped_storage().nbytes() // dtype.itemsize - t.storage_offset()
         if have >= last:
@@ -517,7 +541,7 @@ def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Opti
 
 def _work(t, dev: int):
     """Pointer and bytes of a workspace tensor of any dtype (None: none)."""
-    return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0, dev), t.numel() * t.element_size())
+    return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0, dev), t.nbytes)
 
 
 def make_rope_config(*, q_heads: int, k_heads: int, head_dim: int, rot_dim: Optional[int] = None,
