@@ -75,3 +75,49 @@ def test_rows_of_another_layout_are_refused():
         with pytest.raises(W.TTTError) as e:
             rows(t, n, width, ld)
         assert e.value.status == 2 and str(ld) in str(e.value)
+
+
+BIG = (1 << 32) + 4    # 4, once it has been cut to 32 bits
+
+
+@pytest.mark.parametrize("field", ["q_heads", "k_heads", "head_dim", "rot_dim", "axes"])
+@pytest.mark.parametrize("value", [1 << 31, BIG, (1 << 32) + 64])
+def test_config_numbers_past_32_bits_are_refused(field, value):
+    with pytest.raises(W.TTTError) as e:
+        W.make_rope_config(**{**dict(q_heads=4, k_heads=2, head_dim=64), field: value})
+    assert e.value.status == 2
+    assert W.make_rope_config(q_heads=-1, k_heads=2, head_dim=64).q_heads == -1    # the library's to refuse
+
+
+@pytest.mark.parametrize("at", range(4))
+def test_cache_sizes_past_32_bits_are_refused(at):
+    shape = [1, 1, 1, 16]
+    shape[at] = BIG
+    k = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(W.TTTError) as e:
+        W.make_kv_cache(k, k)
+    assert e.value.status == 2
+
+
+@pytest.mark.parametrize("at", range(4))
+def test_call_numbers_past_32_bits_are_refused(at):
+    x = [1, 4, 1, 2]
+    x[at] = BIG
+    paged = x[0], x[1], x[2], x[3]
+    calls = [lambda: W.ttt_paged_attention_work(W.ttt_kv_cache(), *paged),
+             lambda: W.ttt_paged_attention(None, 512, W.ttt_kv_cache(), None, None, None, 512, None, *paged, 0.0, None)]
+    if at != 2:    # seq_len is a 64-bit number
+        calls += [lambda: W.ttt_window_attention_lse(None, None, None, 512, None, 512, None, x[0], x[1], 1, x[3]),
+                  lambda: W.ttt_window_attention_backward(*[None] * 3, 512, None, 512, None, None, 512, *[None] * 3, 512,
+                                                          None, x[0], x[1], 1, x[3])]
+    for call in calls:
+        with pytest.raises(W.TTTError) as e:
+            call()
+        assert e.value.status == 2 and "2^31" in str(e.value)
+
+
+@pytest.mark.parametrize("scale", [1e-50, 2.0 ** -150, -1e-300])
+def test_a_scale_that_32_bits_make_zero_is_refused(scale):
+    with pytest.raises(W.TTTError) as e:
+        W.ttt_paged_attention(None, 512, W.ttt_kv_cache(), None, None, None, 512, None, 1, 4, 1, 0, scale, None)
+    assert e.value.status == 4

@@ -539,6 +539,13 @@ def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Opti
     raise TTTError(2, f"{name}: {rows} rows {ld} apart take {last} elements, {have} are there")
 
 
+def _int32(x: int) -> None:
+    """Refuses what ctypes would wrap: x is the bitwise or of numbers passed as int32 (a negative
+    one among them is the library's to refuse)."""
+    if x >> 31 > 0:
+        raise TTTError(2, "a number of 2^31 or more")
+
+
 def _work(t, dev: int):
     """Pointer and bytes of a workspace tensor of any dtype (None: none)."""
     return (None, 0) if t is None else (_arg(t, "work", t.dtype, 0, dev), t.nbytes)
@@ -548,6 +555,7 @@ def make_rope_config(*, q_heads: int, k_heads: int, head_dim: int, rot_dim: Opti
                      axes: int = 1, pairing="halves", norm="rms", act="bf16",
                      eps: float = 1e-6) -> ttt_rope_config:
     """ttt_rope_config; rot_dim None rotates whole heads."""
+    _int32(int(q_heads) | int(k_heads) | int(head_dim) | int(rot_dim or 0) | int(axes))
     c = ttt_rope_config()
     c.q_heads, c.k_heads, c.head_dim = int(q_heads), int(k_heads), int(head_dim)
     c.rot_dim = int(head_dim if rot_dim is None else rot_dim)
@@ -628,6 +636,7 @@ def make_kv_cache(k, v, *, k_scale=None, v_scale=None) -> ttt_kv_cache:
         raise TTTError(2, "k and v: two tensors [pages, kv_heads, page_size, head_dim] of one "
                           "dtype and layout")
     pages, heads, size, dim = shape
+    _int32(pages | heads | size | dim)
     if pages < 1 or not ((stride[3] == 1 or dim == 1) and (stride[2] == dim or size == 1) and
                          (stride[1] == size * dim or heads == 1)):
         raise TTTError(2, "at least one page, and each contiguous")
@@ -668,6 +677,7 @@ def ttt_qk_norm_rope_append(cfg: ttt_rope_config, q, ld_q: int, k, ld_k: int, v,
 def ttt_paged_attention_work(cache: ttt_kv_cache, seqs: int, heads: int, max_pages: int,
                              window: int) -> int:
     """Bytes of the workspace that ttt_paged_attention takes."""
+    _int32(seqs | heads | max_pages | window)
     n = ctypes.c_int64()
     _check(lib().ttt_paged_attention_work(ctypes.byref(cache), seqs, heads, max_pages, window,
                                           ctypes.byref(n)))
@@ -680,6 +690,9 @@ def ttt_paged_attention(q, ld_q: int, cache: ttt_kv_cache, table, lens, out, ld_
     """Attention of one new token per sequence over its cached tokens: table int32
     [seqs, max_pages], lens int32 [seqs]; window 0: all of them; scale 0: 1 / sqrt(head_dim);
     lse fp32 [seqs, heads] or None (see include/ttt_attention.h)."""
+    _int32(seqs | heads | max_pages | window)
+    if scale and -2.0 ** -150 <= scale <= 2.0 ** -150:
+        raise TTTError(4, f"scale {scale} is 0 in 32 bits, which selects another")
     torch, dev, st = _here(stream)
     bf, n = torch.bfloat16, heads * cache.head_dim
     _check(lib().ttt_paged_attention(
@@ -694,6 +707,7 @@ def ttt_window_attention_lse(q, k, v, ld: int, out, ld_out: int, lse, batch: int
                              seq_len: int, window: int, mode="sliding", stream=None) -> None:
     """ttt_window_attention that also stores lse, fp32 [batch, heads, seq_len], for the backward
     (see include/ttt_attention.h)."""
+    _int32(batch | heads | window)
     m = WINDOW[mode] if isinstance(mode, str) else int(mode)
     torch, dev, st = _here(stream)
     bf, rows, n = torch.bfloat16, batch * seq_len, heads * ATTN_HEAD_DIM
@@ -709,6 +723,7 @@ def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout,
                                   window: int, mode="sliding", stream=None) -> None:
     """Backward of ttt_window_attention: dq, dk, dv with row stride ld_d; work fp32
     [batch, heads, seq_len] (see include/ttt_attention.h)."""
+    _int32(batch | heads | window)
     m = WINDOW[mode] if isinstance(mode, str) else int(mode)
     torch, dev, st = _here(stream)
     bf, f32, rows, n = torch.bfloat16, torch.float32, batch * seq_len, heads * ATTN_HEAD_DIM
