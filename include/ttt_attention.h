@@ -159,8 +159,10 @@ ttt_status ttt_qk_norm_rope_append(const ttt_rope_config* cfg, const void* q, in
  *   lse      fp32 [seqs][heads] or NULL: the log of the sum of the exponentials
  * A length below 0 counts as 0, one above max_pages * page_size as that.  Tokens whose page
  * number lies outside [0, pages) are left out.  A sequence with no token left gets out 0 and
- * lse -inf.  Places of a page past the sequence's end may hold anything, NaN too; an infinite
- * value within it gives NaN.
+ * lse -inf.  Cached tokens that the new token does not see may hold anything, NaN and infinities
+ * too.  Of those it sees, a key that is infinite or NaN in some element gives its query heads
+ * NaN for out and lse, a value its own element of their out; so does a sum of p v past fp32's
+ * range (p at most 1).
  * heads a multiple of kv_heads, at most 65536; head_dim 64, 128 or 256; 0 <= seqs <= 2^20,
  * seqs * heads below 2^24; max_pages >= 0, max_pages * page_size <= 2^30; window >= 0; scale 0
  * selects 1 / sqrt(head_dim), otherwise finite and > 0.  out, lse and work may not overlap the

@@ -973,3 +973,57 @@ def test_binding_refuses_rows_of_another_layout():
         with pytest.raises(W.TTTError) as e:
             call(q, o)
         assert e.value.status == 2
+
+
+@pytest.mark.parametrize("n,window,D,size", [(50, 0, 128, 16), (3000, 0, 128, 16), (3000, 700, 64, 24), (400, 0, 256, 7)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_paged_attention_keeps_infinities_to_what_sees_them(bad, n, window, D, size):
+    """An infinite key, whose scores are +inf for one query head and -inf for another, gives NaN
+    for both, out and lse; an infinite value NaN in its element; tokens outside the window, other
+    heads and other sequences are as without."""
+    p = Paged([n, 60, 60, 0], 4, 2, D, size)
+    at = n - 20                                       # a token of sequence 0 that the window holds
+    p.q[0, 2 * D + 5], p.q[0, 3 * D + 5] = 1.0, -1.0
+    p.call(window)
+    torch.cuda.synchronize()
+    clean, lse = p.out.clone(), p.lse.clone()
+    p.k[int(p.table[0, at // size]), 1, at % size, 5] = bad              # heads 2 and 3 of sequence 0
+    for j in (0, 7, 59):                                                 # elements of weights of all sizes
+        p.v[int(p.table[1, j // size]), 0, j % size, j] = bad            # heads 0 and 1 of sequence 1
+    if window:
+        p.k[int(p.table[0, 1]), 0, 3, 5] = p.v[int(p.table[0, 1]), 0, 4, 5] = bad    # before the window
+    p.call(window)
+    torch.cuda.synchronize()
+    h2 = slice(2 * D, 4 * D)
+    assert bool(p.out[0, h2].isnan().all()) and bool(p.lse[0, 2:].isnan().all())
+    p.out[0, h2], p.lse[0, 2:] = clean[0, h2], lse[0, 2:]
+    for j in (0, 7, 59):
+        for h in (0, 1):
+            assert bool(p.out[1, h * D + j].isnan()), (j, h)
+            p.out[1, h * D + j] = clean[1, h * D + j]
+    assert torch.equal(p.out, clean) and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("n", [3, 3000])
+def test_paged_attention_of_keys_that_are_all_infinite_is_not_an_empty_sequence(n):
+    p = Paged([n, 0], 2, 2, 64, 16)
+    p.q[0, 5], p.q[0, 64 + 5] = 1.0, -1.0
+    for i in range(-(-n // 16)):
+        p.k[int(p.table[0, i]), :, :, 5] = -float("inf")
+    p.call()
+    torch.cuda.synchronize()
+    assert bool(p.out[0, :128].isnan().all()) and bool(p.lse[0].isnan().all())
+    assert bool((p.out[1, :128] == 0).all()) and bool((p.lse[1] == -float("inf")).all())
+
+
+def test_paged_attention_of_an_infinite_query_is_nan():
+    p = Paged([50, 60], 4, 2, 128, 16)
+    p.call()
+    torch.cuda.synchronize()
+    clean, lse = p.out.clone(), p.lse.clone()
+    p.q[0, 128 + 3] = float("inf")
+    p.call()
+    torch.cuda.synchronize()
+    assert bool(p.out[0, 128:256].isnan().all()) and bool(p.lse[0, 1].isnan())
+    p.out[0, 128:256], p.lse[0, 1] = clean[0, 128:256], lse[0, 1]
+    assert torch.equal(p.out, clean) and torch.equal(p.lse, lse)

@@ -62,6 +62,18 @@ __device__ __forceinline__ int kt_chunk(int r, int c) {
   return c ^ (r & 15);
 }
 
+// Four of an output row: sums times inv, an infinite one (of an infinite value) as NaN.  The two
+// parts of its probability alone would make it an infinity or a NaN by their low bits.
+__device__ __forceinline__ uint2 out4(const f32x4& acc, float inv) {
+  float x[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const float y = acc[v] * inv;
+    x[v] = fmaf(y, 0.f, y);
+  }
+  return uint2{f2bf(x[0]) | ((uint32_t)f2bf(x[1]) << 16), f2bf(x[2]) | ((uint32_t)f2bf(x[3]) << 16)};
+}
+
 // the first four of a lane's eight probabilities
 __device__ __forceinline__ s16x4 low4(bf16x8 p) {
   const s16x8 x = __builtin_bit_cast(s16x8, p);
@@ -220,7 +232,8 @@ __global__ __launch_bounds__(PG_NT, D == 256 ? 2 : D == 128 && E4 ? 3 : 1) void 
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        sc[t][v] = (have >> (16 * t + 4 * g + v)) & 1 ? sc[t][v] * c2 : -INFINITY;
+        // x - x: a score of -inf is a NaN, not a token left out
+        sc[t][v] = (have >> (16 * t + 4 * g + v)) & 1 ? fmaf(sc[t][v], c2, sc[t][v] - sc[t][v]) : -INFINITY;
         mx = fmaxf(mx, sc[t][v]);
       }
     mx = fmaxf(mx, __shfl_xor(mx, 16));
@@ -301,10 +314,7 @@ __global__ __launch_bounds__(PG_NT, D == 256 ? 2 : D == 128 && E4 ? 3 : 1) void 
     const int64_t head = (int64_t)kh * a.group + h0 + h;
     if (whole) {
       const float inv = ll == 0.f ? 0.f : vsc / ll;   // no token: zeros; a NaN stays one
-      uint2 r;
-      r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
-      r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
-      *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + head * D + d) = r;
+      *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + head * D + d) = out4(acc, inv);
       if (d == 0 && a.lse)
         a.lse[(int64_t)seq * a.heads + head] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
     } else {
@@ -369,10 +379,7 @@ __global__ __launch_bounds__(256) void k_paged_join(PagedArgs a) {
   }
   const float vsc = a.vs ? a.vs[head / a.group] : 1.f;
   const float inv = lt == 0.f ? 0.f : vsc / lt;
-  uint2 r;
-  r.x = f2bf(acc[0] * inv) | ((uint32_t)f2bf(acc[1] * inv) << 16);
-  r.y = f2bf(acc[2] * inv) | ((uint32_t)f2bf(acc[3] * inv) << 16);
-  *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + (int64_t)head * D + d) = r;
+  *reinterpret_cast<uint2*>(a.out + (int64_t)seq * a.ldo + (int64_t)head * D + d) = out4(acc, inv);
   if (d == 0 && a.lse)
     a.lse[id] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
 }
