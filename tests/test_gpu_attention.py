@@ -28,6 +28,7 @@ import numpy as np
 import pytest
 import torch
 
+import attention_bars as bars
 import oracle.ttt_attention as oa
 import oracle.ttt_block as blk
 import weight_sequence_layers_amd as W
@@ -1027,3 +1028,26 @@ def test_paged_attention_of_an_infinite_query_is_nan():
     assert bool(p.out[0, 128:256].isnan().all()) and bool(p.lse[0, 1].isnan())
     p.out[0, 128:256], p.lse[0, 1] = clean[0, 128:256], lse[0, 1]
     assert torch.equal(p.out, clean) and torch.equal(p.lse, lse)
+
+
+# ------------------------------------------------------------------------ bars from the launch's own sums
+@pytest.mark.parametrize("kw", [
+    dict(T=5003, Hq=2, Hk=1, D=64, rot=64), dict(T=40001, Hq=1, Hk=1, D=32, rot=32, axes=3, act="f32"),
+    dict(T=6001, Hq=3, Hk=2, D=128, rot=64, pairing="pairs"), dict(T=33000, Hq=2, Hk=1, D=64, rot=0, act="f32"),
+    dict(T=9001, Hq=1, Hk=5, D=80, rot=32, axes=2, act="f32"), dict(T=2500, Hq=1, Hk=2, D=1024, rot=1024),
+    dict(T=700, Hq=33, Hk=7, D=48, rot=48, act="f32")])
+def test_scale_gradients_within_the_bar_of_their_chains(kw):
+    """The scales' gradients against a bar that losing one token exceeds (the bar of the other
+    tests grows with the tokens)."""
+    r = Rope(**kw)
+    refs, _, _, dqw, dkw = rope_backward(r)
+    torch.cuda.synchronize()
+    for which, dy, dw in (("q", refs[0], dqw), ("k", refs[1], dkw)):
+        x = r.heads(which)
+        _, ref = oa.norm_rope_vjp(x, r.weight(which), r.ang, r.pairing, r.eps, dy)
+        xh = np.abs(x) / np.sqrt(np.mean(x * x, -1, keepdims=True) + r.eps)
+        case, sizes, err = (r.T, x.shape[1], r.D, r.rot), r.both(dy) * xh, np64(dw) - ref
+        worst = float(np.max(np.abs(err) / bars.scale_grad_bar(*case, np.sum(sizes, axis=(0, 1)), ref)))
+        norm = float(np.linalg.norm(err) / bars.scale_grad_norm_bar(*case, np.sum(sizes ** 2, axis=(0, 1))))
+        say("  error / bar", which, round(worst, 4), "of the norms", round(norm, 4))
+        assert worst <= 1 and norm <= 1
