@@ -2,9 +2,14 @@
 planted here in the oracle, exceed them, and the roundings that the kernels make do not."""
 import numpy as np
 import pytest
+import torch
 
 import attention_bars as bars
 import oracle.ttt_attention as oa
+
+
+def bf16(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).bfloat16().double().numpy()
 
 
 def scale_terms(T, H, D, rot, seed=1):
@@ -46,3 +51,52 @@ def test_scale_gradient_bar_catches_what_a_launch_may_lose(T, H, D, rot):
     norm = bars.scale_grad_norm_bar(T, H, D, rot, (sizes ** 2).sum((0, 1)))
     assert np.linalg.norm(err) <= norm < 1e-5 * np.linalg.norm(ref)
     assert np.linalg.norm(terms[:1, :1]) > 20 * norm
+
+
+def head(T, window, mode, seed=2):
+    rng = np.random.default_rng(seed)
+    Q, K, V, dO = (bf16(rng.standard_normal((T, 128))) for _ in range(4))
+    return Q, K, V, dO, oa.window_probs(Q, K, window, mode)
+
+
+def grads(Q, K, V, dO, P, delta):
+    c = 1 / np.sqrt(128)
+    dS = P * (dO @ V.T - delta)
+    return c * (dS @ K), c * (dS.T @ Q), P.T @ dO
+
+
+@pytest.mark.parametrize("T,window,mode", [(2100, 4000, "sliding"), (2100, 500, "sliding"), (1400, 700, "block"),
+                                           (300, 37, "sliding"), (300, 1, "sliding"), (520, 128, "block")])
+def test_window_models_hold_for_the_roundings_and_catch_one_key(T, window, mode):
+    Q, K, V, dO, P = head(T, window, mode)
+    out, summed = P @ V, min(window, T) <= 64
+    delta = np.sum(dO * out, 1, keepdims=True)
+    refs = (out, *grads(Q, K, V, dO, P, delta))
+    model = bars.window_models(Q, K, V, dO, P, out, summed)
+    # the kernels' roundings: p, ds and the results to bf16, delta of the rounded out
+    o16 = bf16(bf16(P) @ V)
+    d16 = delta if summed else np.sum(dO * o16, 1, keepdims=True)
+    c = 1 / np.sqrt(128)
+    dS = bf16(P * (dO @ V.T - d16))
+    got = (o16, bf16(c * (dS @ K)), bf16(c * (dS.T @ Q)), bf16(bf16(P).T @ dO))
+    assert np.all(np.abs(o16 - out) <= bars.window_out_bar(P, V, out))
+    for g, r, m in zip(got, refs, model):
+        assert bars.worst_block(g, r, m) <= 1
+    if window == 1:
+        return
+    # one key left out of the products, for the rows of the last block that see it; one query left
+    # out of a key's sums
+    t0 = T - 32
+    lost = P.copy()
+    j = T - 33 if mode == "sliding" else T - 40
+    lost[t0:, j] = 0
+    assert bars.worst_block(lost @ V, out, model[0]) > 2
+    assert bars.worst_block(grads(Q, K, V, dO, lost, delta)[0], refs[1], model[1]) > 2
+    lost = P.copy()
+    lost[T - 20, T - 32:] = 0
+    for i, x in enumerate(grads(Q, K, V, dO, lost, delta)[1:]):
+        assert bars.worst_block(x, refs[2 + i], model[2 + i]) > 2
+    # a row's mask one token short
+    shifted = oa.window_probs(Q, K, max(1, min(window, T) - 1), mode) if mode == "sliding" and window < T else None
+    if shifted is not None:
+        assert bars.worst_block(shifted @ V, out, model[0]) > 2

@@ -1051,3 +1051,55 @@ def test_scale_gradients_within_the_bar_of_their_chains(kw):
         norm = float(np.linalg.norm(err) / bars.scale_grad_norm_bar(*case, np.sum(sizes ** 2, axis=(0, 1))))
         say("  error / bar", which, round(worst, 4), "of the norms", round(norm, 4))
         assert worst <= 1 and norm <= 1
+
+
+@pytest.mark.parametrize("B,Hn,T,window,mode,problems", [
+    (1, 1, 2100, 4000, "sliding", [(0, 0)]), (1, 1, 2100, 500, "sliding", [(0, 0)]),     # the form of few workgroups
+    (1, 2, 700, 300, "block", [(0, 1)]), (1, 1, 300, 37, "sliding", [(0, 0)]), (1, 1, 65, 64, "sliding", [(0, 0)]),
+    (2, 4, 2100, 4000, "sliding", [(0, 0), (1, 3)]), (2, 4, 2100, 500, "sliding", [(1, 2)]),    # of full launches
+    (2, 4, 2100, 700, "block", [(0, 1)]), (2, 4, 2100, 50, "sliding", [(1, 3)]), (2, 4, 2100, 33, "block", [(0, 3)]),
+    (2, 4, 2177, 2177, "block", [(1, 0)]),
+])
+def test_window_training_errors_are_those_of_its_roundings(B, Hn, T, window, mode, problems):
+    """Every block of 32 rows of out, dq, dk and dv is as far off in the 2-norm as the bf16 roundings
+    make it; one key or query left out is several times that."""
+    w = Window(B, Hn, T, window, mode)
+    w.forward()
+    w.backward()
+    torch.cuda.synchronize()
+    D = w.D
+    x, go, o, dx = np64(w.x), np64(w.go), np64(w.out), np64(w.dx[:B * T]).reshape(B, T, -1)
+    for b, h in problems:
+        cols = slice(h * 128, h * 128 + 128)
+        Q, K, V = (x[b, :, i * D:(i + 1) * D][:, cols] for i in range(3))
+        dO, P = go[b, :, cols], oa.window_probs(Q, K, window, mode)
+        out = P @ V
+        refs = (out, *oa.window_attention_vjp(Q, K, V, dO, window, mode))
+        models = bars.window_models(Q, K, V, dO, P, out, min(window, T) <= 64)
+        got = (o[b, :, cols], *(dx[b, :, i * D:(i + 1) * D][:, cols] for i in range(3)))
+        assert np.all(np.abs(got[0] - out) <= bars.window_out_bar(P, V, out))
+        worst = {n: bars.worst_block(*a) for n, *a in zip(("out", "dq", "dk", "dv"), got, refs, models)}
+        say("  worst block / bar", {n: round(v, 3) for n, v in worst.items()})
+        assert max(worst.values()) <= 1
+
+
+@pytest.mark.parametrize("B,T,window,mode", [(2, 1000, 300, "sliding"), (2, 1000, 300, "block"), (4, 2200, 900, "sliding")])
+def test_window_lse_output_and_the_window_attentions_differ_by_their_roundings(B, T, window, mode):
+    """The training forward and the block's window attention: each within its roundings of the exact
+    rows (the block's normaliser sums the rounded probabilities: their errors count once more)."""
+    w = Window(B, 2, T, window, mode)
+    w.forward()
+    plain = torch.empty_like(w.out)
+    D = w.D
+    W.ttt_window_attention(w.x, w.x[..., D:], w.x[..., 2 * D:], 3 * D + 8, plain, D, B, 2, T, window, mode)
+    torch.cuda.synchronize()
+    x = np64(w.x[B - 1])
+    Q, K, V = (x[:, i * D + 128:i * D + 256] for i in range(3))
+    P = oa.window_probs(Q, K, window, mode)
+    out = P @ V
+    model = bars.window_models(Q, K, V, V, P, out, True)[0]
+    norm = bars.R / np.sqrt(3) * np.sqrt(np.sum(P * P, 1, keepdims=True)) * np.abs(out)
+    a, b = np64(w.out[B - 1, :, 128:256]), np64(plain[B - 1, :, 128:256])
+    assert bars.worst_block(a, out, model) <= 1
+    assert bars.worst_block(b, out, np.hypot(model, norm)) <= 1
+    assert bars.worst_block(a, b, np.sqrt(2) * np.hypot(model, norm)) <= 1
