@@ -1103,3 +1103,20 @@ def test_window_lse_output_and_the_window_attentions_differ_by_their_roundings(B
     assert bars.worst_block(a, out, model) <= 1
     assert bars.worst_block(b, out, np.hypot(model, norm)) <= 1
     assert bars.worst_block(a, b, np.sqrt(2) * np.hypot(model, norm)) <= 1
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (64, "e4m3"), (128, "bf16"), (128, "e4m3"), (256, "bf16"), (256, "e4m3")])
+@pytest.mark.parametrize("window", [0, 9001])
+def test_paged_attention_counts_every_token_of_a_long_sequence(D, dtype, window):
+    """Small scores: every token weighs about one part in its sequence's length, and the bar of
+    lse, which goes with the scores' size, is below a third of what a lost token moves it by."""
+    lens = [20011, 4097, 2049, 2048, 2047, 513, 0]
+    p = Paged(lens, 4, 2, D, 24, dtype=dtype, qscale=0.01)
+    q = np64(p.q[:, :4 * D]).reshape(-1, 4, D)
+    kmax = np.sqrt(np.nansum(p.values()[0] ** 2, -1).max())
+    d = np.sqrt(np.sum(q * q, -1).max()) * kmax * (D + 4) * U / np.sqrt(D)     # as check() has it
+    longest = min(lens[0], window or lens[0])
+    least = np.exp(-2 * np.sqrt(np.sum(q * q, -1).max()) * kmax / np.sqrt(D)) / longest
+    assert d + 4 * U * (np.log(longest) + 2) < least / 3
+    p.call(window)
+    p.check(window)
