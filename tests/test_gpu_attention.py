@@ -1120,3 +1120,22 @@ def test_paged_attention_counts_every_token_of_a_long_sequence(D, dtype, window)
     assert d + 4 * U * (np.log(longest) + 2) < least / 3
     p.call(window)
     p.check(window)
+
+
+def test_rotation_angles_keep_more_than_32_bits():
+    """Unit pairs (1, 0) turn into (cos, sin) of their angles. Bar, in half steps U of fp32 at 1: the
+    sine and cosine of a 32-bit angle are within one unit in the last place (1 U), the turn by
+    the rest of the angle rounds once more (U / 2); the rounding of the angle itself (up to pi / 2
+    U) must not be seen."""
+    T, D = 4000, 128
+    r = Rope(T=T, Hq=1, Hk=1, D=D, rot=D, axes=2, act="f32", norm="none")
+    r.x.zero_()
+    r.x[:, :D // 2], r.x[:, D:D + D // 2] = 1, 1
+    qo, ko = r.call()
+    torch.cuda.synchronize()
+    for o in (qo, ko):
+        y = np64(o[:T, :D])
+        for got, want in ((y[:, :D // 2], np.cos(r.ang)), (y[:, D // 2:], np.sin(r.ang))):
+            worst = float(np.abs(got - want).max() / U)
+            say("  worst half steps", round(worst, 3))
+            assert worst <= 1.75

@@ -76,7 +76,10 @@ __device__ __forceinline__ float head_sum(float v, int lph) {
 }
 
 // cos and sin of the block's angles: entry t * (rot / 2) + j.  The angle in turns is reduced
-// in 64 bits before it is rounded.
+// in 64 bits; sine and cosine are taken of it rounded to 32 and turned by the rest d:
+// (c - d s, s + d c), d d / 2 being below 2^-50.  Measured: up to 1.3 half steps of fp32 off,
+// without the rest 1.9 and more (64320 tokens in 32 bits: outputs 6.4e-8 of their norm off, without
+// 6.7e-8, at the same time; sines and cosines in 64 bits 6.3e-8, and 3 to 5 % slower backward).
 __device__ __forceinline__ void turns(const RopeArgs& a, int64_t t0, int nt, float* cs, float* sn) {
   const int half = a.rot >> 1, n = nt * half;
   for (int i = threadIdx.x; i < n; i += ROPE_NT) {
@@ -87,9 +90,10 @@ __device__ __forceinline__ void turns(const RopeArgs& a, int64_t t0, int nt, flo
     ang *= 0.15915494309189533577;   // 1 / (2 pi)
     ang -= rint(ang);
     float s, c;
-    sincospif(2.f * (float)ang, &s, &c);
-    cs[i] = c;
-    sn[i] = s;
+    const float turn = (float)ang, d = 6.28318530717958648f * (float)(ang - (double)turn);
+    sincospif(2.f * turn, &s, &c);
+    cs[i] = fmaf(-d, s, c);
+    sn[i] = fmaf(d, c, s);
   }
 }
 
