@@ -121,3 +121,23 @@ def test_a_scale_that_32_bits_make_zero_is_refused(scale):
     with pytest.raises(W.TTTError) as e:
         W.ttt_paged_attention(None, 512, W.ttt_kv_cache(), None, None, None, 512, None, 1, 4, 1, 0, scale, None)
     assert e.value.status == 4
+
+
+def test_heads_given_as_rows_of_their_own_are_the_same_memory():
+    x = torch.zeros(20, 16)
+    y = torch.zeros(4, 5, 96)[:, :3]                # the first of several sequences
+    assert rows(y, 3, 96, 96) == y.data_ptr()
+    assert rows(x, 5, 64, 64) == x.data_ptr()       # [tokens * heads, dim]
+    with pytest.raises(W.TTTError):
+        rows(x, 4, 64, 80)                          # with a gap that it does not have
+
+
+def test_rows_outside_the_view_are_refused():
+    """A view's rows end where the view does, however large the memory behind it is; one row has to
+    be dense."""
+    x = torch.zeros(8, 128)
+    for t, n, width, ld in ((x[:2, :96], 3, 48, 128), (x[:4, :16], 2, 32, 128), (x.view(8, 2, 64)[:2, 0], 3, 32, 128),
+                            (x[:, 0], 1, 8, 128), (x[:, ::2], 1, 64, 128), (x.t(), 1, 8, 8), (x[:2, :32], 1, 48, 128)):
+        with pytest.raises(W.TTTError) as e:
+            rows(t, n, width, ld)
+        assert e.value.status == 2

@@ -502,19 +502,26 @@ def _table(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     return p
 
 
-def _rows_apart(t, ld: int) -> bool:
-    """Whether t's elements lie in rows ld apart: flat, or dims that are dense up to a row, then
-    one of stride ld, and dense in rows before it."""
-    at, found, dims = 1, False, 0
+def _rows_fit(t, rows: int, width: int, ld: int) -> bool:
+    """Whether t holds `rows` rows of `width` elements ld apart as its own strides have it: dims
+    that are dense up to a row, then one of stride ld, and dense in rows before it; or dense
+    rows given flat or with the row's dims among the outer ones. One row needs to be dense."""
+    at, inner, outer, dims, dense = 1, 1, 1, 0, True
     for n, s in zip(reversed(t.shape), reversed(t.stride())):
         if n > 1:
             dims += 1
-            if not found and s == ld and ld >= at:
-                at, found = ld, True
+            if dense and rows > 1 and s == ld and ld >= at:
+                at, dense = ld, False
             if s != at:
-                return False
+                return inner >= width and (outer >= rows if not dense else rows <= 1)
             at *= n
-    return found or dims < 2
+            if dense:
+                inner *= n
+            else:
+                outer *= n
+    if not dense:
+        return outer >= rows and inner >= width
+    return rows <= 1 or dims < 2 or (dims == 2 and ld == width and ld % t.shape[-1] == 0)
 
 
 def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Optional[int]:
@@ -529,8 +536,9 @@ def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Opti
         return t.data_ptr()   # most calls: the tests below cost 0.2 us a tensor
     last, have = (rows - 1) * ld + width, t.numel()
     if here and have >= rows * width:
-        if rows > 1 and not _rows_apart(t, ld):
-            raise TTTError(2, f"{name}: {list(shape)} of strides {list(t.stride())}, read in rows {ld} apart")
+        if rows > 0 and not _rows_fit(t, rows, width, ld):
+            raise TTTError(2, f"{name}: {list(shape)} of strides {list(t.stride())}, read as {rows} rows of {width}, "
+                              f"{ld} apart")
         if not t.is_contiguous():
             have = t.untyped_storage().nbytes() // dtype.itemsize - t.storage_offset()
         if have >= last:
