@@ -132,8 +132,10 @@ RopeArgs rope_args(const ttt_rope_config* c, const void* qw, const void* kw, con
   a.eps = c->eps;
   a.lph = 1;
   while (a.lph * 16 < a.D) a.lph *= 2;
-  // tokens per workgroup: enough workgroups for eight to a CU first, then up to 16 tokens (the
-  // angles are shared by a token's heads only, so more gain nothing) that fit the LDS table
+  // tokens per workgroup: enough workgroups for eight to a CU first, then up to 16 tokens that fit
+  // the LDS table (the angles are shared by a token's heads only).  A side of few small heads then
+  // has fewer heads in a block than the workgroup's groups: with one query and one key head of 64,
+  // 131072 tokens take 23 us and the backward 63, against 14 and 20 at a copy's rate.
   const int fit = a.rot ? std::min(ROPE_MAX_TB, ROPE_TURNS / (a.rot / 2)) : ROPE_MAX_TB;
   a.tb = (int32_t)std::max<int64_t>(1, std::min<int64_t>(fit, tokens / 2048));
   return a;
@@ -192,11 +194,11 @@ int64_t bwd_work_bytes(const ttt_rope_config* c, int64_t tokens) {
 // the rule goes by the longest span a sequence may have.
 //   - enough workgroups to fill the CUs once, as many to a CU as keep the memory busy
 //     (paged_per_cu): more parts than that only make the join longer (one 131072-token sequence
-//     of 8 heads: 99 us at 512 workgroups, 106 at 2048).  Room is for one more of heads of 64 and
-//     of bf16 heads of 256 (one sequence of 131072 tokens, heads of 64: 46.5 us, 49.3 with three
-//     to a CU; of 65536, heads of 256: 49.6 us, 54.0 with two);
+//     of 8 heads: 90.5 us at 512 workgroups, 95.7 at 2048).  Room is for one more of heads of 64 and
+//     of bf16 heads of 256 (8 heads, one sequence of 131072 tokens, heads of 64: 49.2 us, 50.9 with
+//     three to a CU; of 65536, heads of 256: 91.0 us, 92.5 with two);
 //   - no part above PG_MAX_PART tokens, so that one long sequence among short ones is not left
-//     to a few workgroups (64 sequences up to 8192 tokens: 213 us, against 219 unsplit), while
+//     to a few workgroups (64 sequences up to 8192 tokens: 193.5 us, against 199.8 unsplit), while
 //     the launch stays below PG_WGS_MOST workgroups, most of which a ragged batch leaves empty;
 //   - no part below PG_MIN_PART tokens: two steps of every wave.
 constexpr int64_t PG_MAX_PART = 2048, PG_MIN_PART = 256, PG_WGS_MOST = 16384, NUM_CU = 256;

@@ -13,11 +13,15 @@
 // back along its rows as the A operand of S^T = K Q^T, so each lane holds 8 tokens of one query
 // head and P^T is already laid out as the second product's B operand; V is read transposed.
 //
-// Measured: one context of 131072 tokens, 8 heads: 86 us, 6.2 TB/s of cached bytes; 64 sequences
-// up to 8192 tokens, 32 query heads on 8: 192 us, 5.7 TB/s; 96 windows of 2048 in e4m3: 37 us,
-// 4.3 TB/s (4.4 us of it the join, a few the chain length - page - row of a workgroup's start).
-// The kernels read 1.001 times the cached bytes.  K's fragments straight from memory (64 bytes
-// of a row per load) read 2 to 6 % slower than through LDS.
+// Measured, with the join: one context of 131072 tokens, 8 heads: 86 to 91 us, 6.0 TB/s of cached
+// bytes (reading alone, 4 GB in 16-byte loads, reaches 6.5 to 6.8); 64 sequences up to 8192 tokens,
+// 32 query heads on 8: 193 us, 5.7 TB/s; 96 windows of 2048 in e4m3: 37 to 39 us, 4.2 TB/s (4.7 us
+// of it the join, a few the chain length - page - row of a workgroup's start).  e4m3 halves the
+// bytes under way, not the latency: one context takes 53 us, heads of 256 93 (79 at the rate of
+// reading), bf16 heads of 256 174 (158); 16 ragged sequences of e4m3 heads of 256, 4 key heads, 39
+// us (20), whose registers leave two waves to a SIMD.  The kernels read 1.001 times the cached
+// bytes.  K's fragments straight from memory (64 bytes of a row per load) read 2 to 6 % slower than
+// through LDS.
 #include "ttt_attention_internal.h"
 
 namespace ttt {

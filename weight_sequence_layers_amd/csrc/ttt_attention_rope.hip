@@ -13,9 +13,9 @@
 // both members of a pair are its own: the rotation needs no exchange, the norm a few shuffles
 // among the head's lanes.
 //
-// Measured (a copy of 4 GB reads and writes 4.7 TB/s on the same card): forward, 64320 tokens of
+// Measured (a copy of 4 GB reads and writes 4.8 to 5.0 TB/s on the same card): forward, 64320 tokens of
 // 12 heads of 128 in 32 bits, three axes: 181 us, 4.4 TB/s; backward, 32768 tokens of 16 heads
-// in bf16: 84 us with the scales' sums (79 + 5), 4.8 TB/s.  It moves its least bytes to within
+// in bf16: 84 to 87 us with the scales' sums (4.7 of it), 4.7 TB/s.  It moves its least bytes to within
 // 1 %.  Non-temporal stores gain 2 to 15 % in bf16, whose runs fill whole lines, and lose 20 % in
 // 32 bits with a rotation of 96 of 128, whose runs do not: ordinary ones stay.  The smallest
 // calls take 3.6 us on the GPU, what any launch takes, and 10.8 us of the host.

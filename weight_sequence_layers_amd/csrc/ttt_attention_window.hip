@@ -15,13 +15,21 @@
 // lane's elements are the B operand of the product that follows; k (or q and dout) is read from
 // the same tile both along its rows and, transposed, along its columns.
 //
-// Measured at 32768 tokens, 8 heads, a sliding window of 2048: forward 340 us, backward 432 and
-// 580 us; 780, 923 and 917 TFLOP/s of the products made (the largest library product of this
-// card, 8192 cubed, runs at 1160 to 1200).  The matrix cores are busy 49, 59 and 55 % of the
-// cycles, the LDS 26 to 43 %; but the card's clock falls to 1.5 to 1.8 GHz in these kernels (2.1
-// to 2.2 where the memory bounds): power is what bounds them, and filling more of the cycles gains
-// little.  The forward with the next step's scores computed beside this step's exponentials, in
-// the same wave: 315 to 320 us against 317 in turn.
+// p and ds enter their products as one bf16 number each, ds with the delta of the rounded out (but
+// see SUM below); scores, exponentials, statistics and sums are fp32. That is a choice: against 64
+// bits out is 2.3e-3 of its norm off and the gradients 2.4e-3, where rounding the exact values to
+// bf16 gives 1.65e-3. Two bf16 numbers apiece reach that (1.65e-3, 1.68e-3) and take a training
+// step at 32768 tokens from 1190 to 1600 us, the forward in it from 288 to 384: the matrix cores
+// take no mixed operands, and fp16 does not hold the range of v, k, q and dout.
+//
+// Measured at 32768 tokens, 8 heads, a sliding window of 2048, in a run of 180 steps: forward
+// 294 us, backward 385 and 513 us, the step 1192; 906, 1037 and 1038 TFLOP/s of the products made
+// (the largest library product of this card, 8192 cubed, runs at 1160 to 1200). The first
+// launches after a pause take up to a third longer. The matrix cores are busy 49, 59 and 55 % of
+// the cycles, the LDS 25, 30 and 41 %, at a clock of 1.6 to 1.7 GHz (2.1 to 2.2 where the memory
+// bounds): power is what bounds them, and filling more of the cycles gains little. The forward
+// with the next step's scores computed beside this step's exponentials, in the same wave: 315 to
+// 320 us against 317 in turn.
 #include "ttt_attention_internal.h"
 
 namespace ttt {
@@ -123,6 +131,10 @@ __device__ __forceinline__ void wb_store(u16* row, const f32x16 (&o)[4], float f
     }
 }
 
+// With TTT_WINDOW_BLOCK the rows of a workgroup start at multiples of their number, not of the
+// window: one that straddles a boundary walks both windows, and the forward and dq compute steps
+// that are masked for all of a wave (windows of 250: up to 8 steps of 64 keys for 4).
+//
 // The keys that a workgroup's queries q0 .. qlast visit, [lo, lo + nsteps tiles), those of its
 // wave at w0 that every one of its queries sees, [in_lo, in_hi) (empty for a wave of padding
 // rows: a step wholly inside needs no mask), and the lane's query t's own, lo_t and len_t of them
@@ -185,11 +197,14 @@ __device__ __forceinline__ void wb_join(f32x16 (&o)[4], int w, int half, char* b
       for (int v = 0; v < 16; ++v) o[d][v] += *at(d, v);
 }
 
-// NH 1: the four waves take 32 rows each, 128 to a workgroup.  NH 2, for launches that leave CUs
-// idle (at most WB_FEW workgroups of 64 rows): 64 rows to a workgroup and two waves to each 32,
-// which take half of every step's tile and are joined at the end: twice the workgroups, and
-// half the products in each SIMD's chain of steps, which is what such a launch waits for (one
-// head of 1024 tokens: dq 29 -> 20 us, dk and dv 42 -> 26; eight waves over 128 rows gain nothing).
+// NH 1: the four waves take 32 rows each, 128 to a workgroup.  NH 2, for launches of at most
+// WB_FEW workgroups of 64 rows: 64 rows to a workgroup and two waves to each 32, which take half
+// of every step's tile and are joined at the end: twice the workgroups, and half the products in
+// each SIMD's chain of steps, which is what such a launch waits for (one head of 1024 tokens: dq
+// 29 -> 20 us, dk and dv 42 -> 26; eight waves over 128 rows gain nothing).  WB_FEW is one
+// workgroup to a CU. The rule leaves time where it ends: 8 heads, a window of 2048, take 110 us a
+// training step at 2048 tokens (256 blocks of 64) and 173 at 2112, where NH 1 launches 136
+// workgroups on 256 CUs.
 //
 // Forward with each row's log-sum-exp.  The running maximum that the exponentials refer to moves
 // only when a score passes it by more than 2^8: the sums stay far inside fp32, the rounding of
