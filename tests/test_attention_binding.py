@@ -63,9 +63,8 @@ def test_rows_read_as_they_lie():
 
 
 def test_rows_of_another_layout_are_refused():
-    x = torch.zeros(6, 6, 16)
     for t, n, width, ld in (
-            (x.transpose(0, 1), 6, 96, 96),                 # [heads, tokens, dim] as [tokens, heads, dim]
+            (torch.zeros(7, 6, 16).transpose(0, 1), 6, 112, 112),    # [heads, tokens, dim] as [tokens, heads, dim]
             (torch.zeros(96, 6).t(), 6, 96, 96),            # columns for rows
             (torch.zeros(6, 192)[:, ::2], 6, 96, 96), (torch.zeros(6, 192)[:, ::2], 6, 96, 192),
             (torch.zeros(12, 96)[::2], 6, 96, 96),          # every second row
@@ -141,3 +140,16 @@ def test_rows_outside_the_view_are_refused():
         with pytest.raises(W.TTTError) as e:
             rows(t, n, width, ld)
         assert e.value.status == 2
+
+
+def test_rows_whose_heads_are_named_before_their_tokens_are_the_same_memory():
+    B, T, H, D = 2, 5, 3, 16
+    x = torch.zeros(B, T, 3, H, D)
+    for i in range(3):
+        for t in (x[:, :, i], x[:, :, i].transpose(1, 2), x.permute(2, 0, 3, 1, 4)[i]):     # [B, H, T, D]
+            assert rows(t, B * T, H * D, 3 * H * D) == t.data_ptr()
+    y = torch.zeros(T, H, D)
+    assert rows(y.transpose(0, 1), T, H * D, H * D) == y.data_ptr()
+    for t, ld in ((torch.zeros(B, H, T, D), H * D), (torch.zeros(B, H, T, D).transpose(1, 2), H * D)):
+        with pytest.raises(W.TTTError):
+            rows(t, B * T, H * D, ld)           # heads outermost in the memory itself

@@ -959,7 +959,7 @@ def test_binding_refuses_tables_of_another_layout():
 
 def test_binding_refuses_rows_of_another_layout():
     """Tensors whose own rows are not ld apart, which would be read as if they were."""
-    T, Hn, D = 4, 4, 64     # as many tokens as heads: every count fits
+    T, Hn, D = 6, 4, 64
     r = Rope(T=T, Hq=Hn, Hk=Hn, D=D, rot=64)
     n = Hn * D
     qo, ko = (torch.zeros(T, n, dtype=torch.bfloat16, device=DEV) for _ in range(2))
@@ -969,8 +969,12 @@ def test_binding_refuses_rows_of_another_layout():
         W.ttt_qk_norm_rope(r.cfg, q, n, r.k, r.ld, r.qw, r.kw, r.freq, r.pos, qo, n, ko, n, T)
     call(x, qo)
     r.check(torch.cat((qo, torch.full_like(qo, 7.0))), torch.cat((ko, torch.full_like(ko, 7.0))))
+    first = qo.clone()
+    call(x.transpose(0, 1), qo)     # the heads named before the tokens: the same memory
+    torch.cuda.synchronize()
+    assert torch.equal(qo, first)
     turned = torch.zeros(Hn, T, D, dtype=torch.bfloat16, device=DEV).transpose(0, 1)
-    for q, o in ((x.transpose(0, 1), qo), (x, turned), (torch.zeros(T, 2 * n, dtype=torch.bfloat16, device=DEV), qo)):
+    for q, o in ((turned, qo), (x, turned), (torch.zeros(T, 2 * n, dtype=torch.bfloat16, device=DEV), qo)):
         with pytest.raises(W.TTTError) as e:
             call(q, o)
         assert e.value.status == 2

@@ -504,24 +504,27 @@ def _table(t, name: str, dtype, shape, dev: int) -> Optional[int]:
 
 def _rows_fit(t, rows: int, width: int, ld: int) -> bool:
     """Whether t holds `rows` rows of `width` elements ld apart as its own strides have it: dims
-    that are dense up to a row, then one of stride ld, and dense in rows before it; or dense
-    rows given flat or with the row's dims among the outer ones. One row needs to be dense."""
-    at, inner, outer, dims, dense = 1, 1, 1, 0, True
-    for n, s in zip(reversed(t.shape), reversed(t.stride())):
-        if n > 1:
-            dims += 1
-            if dense and rows > 1 and s == ld and ld >= at:
-                at, dense = ld, False
-            if s != at:
-                return inner >= width and (outer >= rows if not dense else rows <= 1)
-            at *= n
-            if dense:
-                inner *= n
-            else:
-                outer *= n
+    that are dense up to a row, then one of stride ld, and dense in rows before it, in whatever
+    order the tensor names them (heads before tokens: the same memory); or contiguous rows given
+    flat or with the row's dims among the outer ones. One row needs to be dense."""
+    dims = [(s, n) for n, s in zip(reversed(t.shape), reversed(t.stride())) if n > 1]
+    if rows > 1:
+        dims.sort()
+    at, inner, outer, dense = 1, 1, 1, True
+    for s, n in dims:
+        if dense and rows > 1 and s == ld and ld >= at:
+            at, dense = ld, False
+        if s != at:
+            return inner >= width and (outer >= rows if not dense else rows <= 1)
+        at *= n
+        if dense:
+            inner *= n
+        else:
+            outer *= n
     if not dense:
         return outer >= rows and inner >= width
-    return rows <= 1 or dims < 2 or (dims == 2 and ld == width and ld % t.shape[-1] == 0)
+    return rows <= 1 or len(dims) < 2 or (
+        len(dims) == 2 and ld == width and ld % dims[0][1] == 0 and t.is_contiguous())
 
 
 def _rows(t, name: str, dtype, rows: int, width: int, ld: int, dev: int) -> Optional[int]:
