@@ -1143,3 +1143,118 @@ def test_rotation_angles_keep_more_than_32_bits():
             worst = float(np.abs(got - want).max() / U)
             say("  worst half steps", round(worst, 3))
             assert worst <= 1.75
+
+
+# ------------------------------------------------------------------------ whole steps in a graph
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_a_decoding_step_captured_once_serves_every_token(dtype):
+    """Append and attention of one new token for three sequences in one graph, replayed with the
+    tokens, positions, slots and lengths changed in place, beside the same calls made eagerly on
+    caches of their own, on another stream; a sequence that pauses has slot -1."""
+    S, Hq, Hk, D, size, width, steps = 3, 4, 2, 128, 7, 40, 9
+    r = Rope(T=S * steps, Hq=Hq, Hk=Hk, D=D, rot=D, seed=31)
+    ct = torch.bfloat16 if dtype == "bf16" else torch.float8_e4m3fn
+    scale = (0.02 + 0.02 * torch.rand(Hk, generator=gen(32), device=DEV)) if dtype == "e4m3" else None
+    pages = S * width
+    order = torch.randperm(pages, generator=gen(33), device=DEV).to(torch.int32).view(S, width)
+    start = torch.tensor([270, 0, 13], dtype=torch.int32, device=DEV)
+    fill = [torch.randn(pages, Hk, size, D, generator=gen(34 + i), device=DEV).to(ct) for i in range(2)]
+
+    class Side:
+        def __init__(self):
+            self.kv = [f.clone() for f in fill]
+            self.cache = W.make_kv_cache(*self.kv, k_scale=scale, v_scale=scale)
+            self.x = torch.zeros(S, r.ld, dtype=r.dt, device=DEV)
+            self.pos = torch.zeros(1, S, dtype=torch.int32, device=DEV)
+            self.slot = torch.zeros(S, dtype=torch.int64, device=DEV)
+            self.lens = start.clone()
+            self.q, self.out = (torch.empty(S, Hq * D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+            self.lse = torch.empty(S, Hq, device=DEV)
+            self.work = torch.empty(max(1, W.ttt_paged_attention_work(self.cache, S, Hq, width, 0)),
+                                    dtype=torch.uint8, device=DEV)
+
+        def step(self, i):
+            """The next token's inputs; sequence 1 pauses at step 4."""
+            self.x.copy_(r.x[S * i:S * i + S])
+            self.pos.copy_(self.lens[None])
+            at = self.lens.long()
+            page = order.gather(1, (at // size)[:, None])[:, 0].long()
+            self.slot.copy_(page * size + at % size)
+            self.lens.add_(1)
+            if i == 4:
+                self.slot[1] = -1
+                self.lens[1] -= 1
+
+        def call(self, **kw):
+            n = Hq * D
+            W.ttt_qk_norm_rope_append(r.cfg, self.x, r.ld, self.x[:, n:], r.ld, self.x[:, n + Hk * D:], r.ld, r.qw, r.kw,
+                                      r.freq, self.pos, self.cache, self.slot, self.q, n, S, **kw)
+            W.ttt_paged_attention(self.q, n, self.cache, order, self.lens, self.out, n, self.lse, S, Hq, width, 0, 0.0,
+                                  self.work, **kw)
+
+        def results(self):
+            return [t.view(torch.uint8) if t.element_size() == 1 else t for t in (self.q, self.out, self.lse, *self.kv)]
+
+    eager, replayed = Side(), Side()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        replayed.call()
+    for i in range(steps):
+        eager.step(i)
+        side.wait_stream(torch.cuda.current_stream())
+        eager.call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        replayed.step(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager.results(), replayed.results()):
+            assert torch.equal(a, b), i
+        torch.randn(1000, device=DEV).sum().item()
+    assert bool(eager.out.isfinite().all())
+
+
+@pytest.mark.parametrize("T,window,mode", [(300, 90, "sliding"), (3000, 40, "block")])
+def test_a_training_step_captured_serves_other_inputs(T, window, mode):
+    """Norm and rotation, window attention and both backwards in one graph on one projection's rows,
+    replayed with other inputs, against the calls made eagerly on a stream of their own."""
+    Hn, D = 6, 128
+    n = Hn * D
+    r = Rope(T=T, Hq=Hn, Hk=Hn, D=D, rot=D, seed=41)
+    go = torch.empty(T, n, dtype=r.dt, device=DEV)
+
+    def side():
+        t = dict(qkv=torch.empty(T, 3 * n, dtype=r.dt, device=DEV), out=torch.empty(T, n, dtype=r.dt, device=DEV),
+                 lse=torch.empty(1, Hn, T, device=DEV), g=torch.empty(T, 3 * n, dtype=r.dt, device=DEV),
+                 dqw=torch.empty(D, device=DEV), dkw=torch.empty(D, device=DEV))
+        stat = torch.empty(1, Hn, T, device=DEV)
+        work = torch.empty(W.ttt_qk_norm_rope_backward_work(r.cfg, T), dtype=torch.uint8, device=DEV)
+
+        def call(**kw):
+            q, g = t["qkv"], t["g"]
+            W.ttt_qk_norm_rope(r.cfg, r.q, r.ld, r.k, r.ld, r.qw, r.kw, r.freq, r.pos, q, 3 * n, q[:, n:], 3 * n, T, **kw)
+            W.ttt_window_attention_lse(q, q[:, n:], q[:, 2 * n:], 3 * n, t["out"], n, t["lse"], 1, Hn, T, window, mode, **kw)
+            W.ttt_window_attention_backward(q, q[:, n:], q[:, 2 * n:], 3 * n, t["out"], n, t["lse"], go, n, g, g[:, n:],
+                                            g[:, 2 * n:], 3 * n, stat, 1, Hn, T, window, mode, **kw)
+            W.ttt_qk_norm_rope_backward(r.cfg, r.q, r.ld, r.k, r.ld, r.qw, r.kw, r.freq, r.pos, g, 3 * n, g[:, n:], 3 * n,
+                                        g, 3 * n, g[:, n:], 3 * n, t["dqw"], t["dkw"], work, T, **kw)
+        return t, call
+    (a, eager), (b, captured) = side(), side()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured()
+    for i in range(4):
+        r.x.copy_(torch.randn(r.x.shape, generator=gen(50 + i), device=DEV))
+        go.copy_(torch.randn(go.shape, generator=gen(60 + i), device=DEV))
+        for t in (a, b):
+            t["qkv"][:, 2 * n:] = r.v[:, :n]
+        stream.wait_stream(torch.cuda.current_stream())
+        eager(stream=stream)
+        torch.cuda.current_stream().wait_stream(stream)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in a:
+            assert torch.equal(a[k], b[k]) and bool(a[k].isfinite().all()), (i, k)
+        torch.randn(1000, device=DEV).sum().item()
