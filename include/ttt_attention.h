@@ -63,9 +63,9 @@ ttt_status ttt_validate_rope_config(const ttt_rope_config* cfg);
  *   angle_j = sum_a pos[a][t] freq[a][j],          j < rot_dim / 2
  *   y = n with every pair (n0, n1) of index j turned by its angle:
  *       (n0 cos - n1 sin, n0 sin + n1 cos)
- * rounded once to the activation dtype; everything before is fp32, the angles are summed and
- * reduced in 64 bits (positions anywhere in int32 keep their precision), and their sines and
- * cosines are within two half steps of fp32.  The sum of squares is fp32 too: a head whose
+ * rounded once to the activation dtype; everything before is fp32, but the angles are summed and
+ * reduced in 64 bits with what those round off: sines and cosines are within two half steps of
+ * fp32 at positions anywhere in int32.  The sum of squares is fp32 too: a head whose
  * squares add up past its range (values of about 1e18 and more) comes out as zeros.
  *   q, k     element e of head h of token t at  t * ld + h * head_dim + e
  *   q_out, k_out  the same with ld_qo, ld_ko.  q_out may be q itself (ld_qo == ld_q) and k_out

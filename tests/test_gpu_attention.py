@@ -1258,3 +1258,31 @@ def test_a_training_step_captured_serves_other_inputs(T, window, mode):
         for k in a:
             assert torch.equal(a[k], b[k]) and bool(a[k].isfinite().all()), (i, k)
         torch.randn(1000, device=DEV).sum().item()
+
+
+@pytest.mark.parametrize("axes", [1, 2, 4])
+def test_rotation_angles_of_far_positions(axes):
+    """Positions anywhere in int32 against angles in 60 decimal digits (64 bits leave up to 2^-22
+    radians of 2^31): the bar of near ones, and 2^-30 for the reference's own steps."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    tau = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    T, rot = 60, 64
+    r = Rope(T=T, Hq=1, Hk=1, D=rot, rot=rot, axes=axes, act="f32", norm="none", far=True)
+    r.freq[:, ::3] = torch.rand(r.freq[:, ::3].shape, generator=gen(71), device=DEV) * 0.5 + 0.5
+    r.pos[:, :2], r.pos[:, 2:4] = 2 ** 31 - 1, -2 ** 31
+    r.x.zero_()
+    r.x[:, :rot // 2], r.x[:, rot:rot + rot // 2] = 1, 1
+    pos, freq = r.pos.cpu().tolist(), [[Decimal(x) for x in row] for row in r.freq.double().cpu().tolist()]
+    ang = np.empty((T, rot // 2))
+    for t in range(T):
+        for j in range(rot // 2):
+            x = sum(pos[a][t] * freq[a][j] for a in range(axes)) / tau
+            ang[t, j] = float((x - x.to_integral_value()) * tau)
+    qo, ko = r.call()
+    torch.cuda.synchronize()
+    for o in (qo, ko):
+        y = np64(o[:T, :rot])
+        worst = max(float(np.abs(y[:, :rot // 2] - np.cos(ang)).max()), float(np.abs(y[:, rot // 2:] - np.sin(ang)).max()))
+        say("  worst half steps", round(worst / U, 3))
+        assert worst <= 1.75 * U + 2.0 ** -30

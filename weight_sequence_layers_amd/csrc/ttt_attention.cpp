@@ -135,7 +135,7 @@ RopeArgs rope_args(const ttt_rope_config* c, const void* qw, const void* kw, con
   // tokens per workgroup: enough workgroups for eight to a CU first, then up to 16 tokens that fit
   // the LDS table (the angles are shared by a token's heads only).  A side of few small heads then
   // has fewer heads in a block than the workgroup's groups: with one query and one key head of 64,
-  // 131072 tokens take 23 us and the backward 63, against 14 and 20 at a copy's rate.
+  // 131072 tokens take 24 us and the backward 64, against 14 and 20 at a copy's rate.
   const int fit = a.rot ? std::min(ROPE_MAX_TB, ROPE_TURNS / (a.rot / 2)) : ROPE_MAX_TB;
   a.tb = (int32_t)std::max<int64_t>(1, std::min<int64_t>(fit, tokens / 2048));
   return a;

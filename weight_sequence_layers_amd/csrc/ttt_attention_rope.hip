@@ -75,22 +75,33 @@ __device__ __forceinline__ float head_sum(float v, int lph) {
   return v;
 }
 
-// cos and sin of the block's angles: entry t * (rot / 2) + j.  The angle in turns is reduced
-// in 64 bits; sine and cosine are taken of it rounded to 32 and turned by the rest d:
-// (c - d s, s + d c), d d / 2 being below 2^-50.  Measured: up to 1.3 half steps of fp32 off,
-// without the rest 1.9 and more (64320 tokens in 32 bits: outputs 6.4e-8 of their norm off, without
-// 6.7e-8, at the same time; sines and cosines in 64 bits 6.3e-8, and 3 to 5 % slower backward).
+// cos and sin of the block's angles: entry t * (rot / 2) + j.  A product of a position and a
+// frequency has up to 55 bits, and 2^31 radians in 64 bits are 2^-22 off: the products, their sum
+// over the axes and the turn's reduction keep what each rounds off (a fused product or a two-term
+// sum gives it exactly).  Sine and cosine are taken of the reduced turn rounded to 32 bits and
+// turned by the rest d: (c - d s, s + d c), d d / 2 being below 2^-50.  Measured: up to 1.3 half
+// steps of fp32 off at positions anywhere in int32; in plain 64-bit steps 6 to 22 at far ones, by
+// the axes; without the rest d 1.9 at any.  64320 tokens in 32 bits: outputs 6.4e-8 of their norm
+// off, without d 6.7e-8, at the same time; sines and cosines in 64 bits 6.3e-8, and 3 to 5 % slower
+// backward.
 __device__ __forceinline__ void turns(const RopeArgs& a, int64_t t0, int nt, float* cs, float* sn) {
+#pragma clang fp contract(off)   // the differences below are of rounded sums and products
   const int half = a.rot >> 1, n = nt * half;
+  constexpr double C = 0.15915494309189535, CL = -9.839338337591243e-18;   // 1 / (2 pi) = C + CL
   for (int i = threadIdx.x; i < n; i += ROPE_NT) {
     const int t = i / half, j = i - t * half;
-    double ang = 0.0;
-    for (int x = 0; x < a.axes; ++x)
-      ang += (double)a.pos[(int64_t)x * a.tokens + t0 + t] * (double)a.freq[x * half + j];
-    ang *= 0.15915494309189533577;   // 1 / (2 pi)
-    ang -= rint(ang);
+    const double p0 = (double)a.pos[t0 + t], f0 = (double)a.freq[j];
+    double ang = p0 * f0, low = fma(p0, f0, -ang);
+    for (int x = 1; x < a.axes; ++x) {
+      const double p = (double)a.pos[(int64_t)x * a.tokens + t0 + t], f = (double)a.freq[x * half + j];
+      const double y = p * f, sum = ang + y, part = sum - ang;
+      low += fma(p, f, -y) + ((ang - (sum - part)) + (y - part));
+      ang = sum;
+    }
+    const double u = ang * C;
+    const double r = (u - rint(u)) + fma(low, C, fma(ang, CL, fma(ang, C, -u)));
     float s, c;
-    const float turn = (float)ang, d = 6.28318530717958648f * (float)(ang - (double)turn);
+    const float turn = (float)r, d = 6.28318530717958648f * (float)(r - (double)turn);
     sincospif(2.f * turn, &s, &c);
     cs[i] = fmaf(-d, s, c);
     sn[i] = fmaf(d, c, s);
