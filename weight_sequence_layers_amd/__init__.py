@@ -78,7 +78,17 @@ class ttt_kv_cache(ctypes.Structure):
     device = None   # of the tensors, where make_kv_cache filled the struct
 
 
+class ttt_linear_attention_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "dim_k", "dim_v")] + [("scale", ctypes.c_float)]
+
+
+class ttt_residual_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dim", "groups", "norm_y", "gate", "act")
+    ] + [("eps", ctypes.c_float)]
+
+
 HEAD_NORM = {"none": 0, "rms": 1}
+GATE = {"none": 0, "sigmoid": 1, "silu": 2}
 PAIRING = {"halves": 0, "pairs": 1}
 WINDOW = {"sliding": 0, "block": 1}
 LINEAR_EPI = {"plain": 0, "residual": 1, "gelu": 2}
@@ -97,6 +107,8 @@ def lib() -> ctypes.CDLL:
         cfgp, vp, i64 = ctypes.POINTER(ttt_config), ctypes.c_void_p, ctypes.c_int64
         i32 = ctypes.c_int32
         ropep, cachep = ctypes.POINTER(ttt_rope_config), ctypes.POINTER(ttt_kv_cache)
+        linp, normp = (ctypes.POINTER(ttt_linear_attention_config),
+                       ctypes.POINTER(ttt_residual_norm_config))
         sig = {
             "ttt_validate_config": [cfgp],
             "ttt_state_numel": [cfgp, ctypes.POINTER(i64)],
@@ -134,6 +146,23 @@ def lib() -> ctypes.CDLL:
                                          vp],
             "ttt_window_attention_backward": [vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, vp,
                                               i64, vp, i32, i32, i64, i32, i32, vp],
+            "ttt_validate_linear_attention_config": [linp],
+            "ttt_linear_attention_work": [linp, i32, i64, ctypes.POINTER(i64)],
+            "ttt_linear_attention": [linp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp,
+                                     i64, i64, i32, i64, vp, i64, vp],
+            "ttt_linear_attention_backward_work": [linp, i32, i64, ctypes.POINTER(i64)],
+            "ttt_linear_attention_backward": [linp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64,
+                                              vp, vp, i64, vp, i64, vp, i64, vp, i64, i32, i64,
+                                              vp, i64, vp],
+            "ttt_linear_attention_step": [linp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, vp,
+                                          i64, i32, vp],
+            "ttt_validate_residual_norm_config": [normp],
+            "ttt_residual_norm": [normp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64,
+                                  i64, vp],
+            "ttt_residual_norm_backward_work": [normp, i64, ctypes.POINTER(i64)],
+            "ttt_residual_norm_backward": [normp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp,
+                                           i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, i64,
+                                           vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -746,3 +775,170 @@ def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout,
         _rows(dout, "dout", bf, rows, n, ld_dout, dev), ld_dout, _rows(dq, "dq", bf, rows, n, ld_d, dev),
         _rows(dk, "dk", bf, rows, n, ld_d, dev), _rows(dv, "dv", bf, rows, n, ld_d, dev), ld_d,
         _arg(work, "work", f32, rows * heads, dev), batch, heads, seq_len, window, m, st))
+
+
+# --------------------------------- linear attention, norms between sub-layers (ttt_mixer.h)
+def make_linear_attention_config(*, heads: int, dim_k: int, dim_v: Optional[int] = None,
+                                 scale: float = 0.0) -> ttt_linear_attention_config:
+    """ttt_linear_attention_config; dim_v None: dim_k; scale 0: 1 / sqrt(dim_k)."""
+    dim_v = dim_k if dim_v is None else dim_v
+    _int32(int(heads) | int(dim_k) | int(dim_v))
+    _scale(scale)
+    return ttt_linear_attention_config(int(heads), int(dim_k), int(dim_v), float(scale))
+
+
+def _scale(scale: float) -> None:
+    if scale and -2.0 ** -150 <= scale <= 2.0 ** -150:
+        raise TTTError(4, f"scale {scale} is 0 in 32 bits, which selects another")
+
+
+def ttt_validate_linear_attention_config(cfg: ttt_linear_attention_config) -> None:
+    _check(lib().ttt_validate_linear_attention_config(ctypes.byref(cfg)))
+
+
+def _pool(t, name: str, cfg, dev: int, torch):
+    """Pointer and number of entries of a pool of states [slots, heads, dim_k, dim_v] (None: none)."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if len(shape) != 4 or tuple(shape[1:]) != (cfg.heads, cfg.dim_k, cfg.dim_v):
+        raise TTTError(2, f"{name} is {list(shape)}, [slots, {cfg.heads}, {cfg.dim_k}, {cfg.dim_v}] is read")
+    _int32(shape[0])
+    return _arg(t, name, torch.float32, 0, dev), shape[0]
+
+
+def _pools(state_in, state_out, cfg, dev: int, torch):
+    """Pointers of the two pools and their number of entries."""
+    (pi, ni), (po, no) = _pool(state_in, "state_in", cfg, dev, torch), _pool(state_out, "state_out", cfg, dev, torch)
+    if state_in is not None and state_out is not None and ni != no:
+        raise TTTError(2, f"state_in of {ni} entries, state_out of {no}")
+    return pi, po, max(ni, no)
+
+
+def ttt_linear_attention_work(cfg: ttt_linear_attention_config, batch: int, seq_len: int) -> int:
+    """Bytes of the workspace that ttt_linear_attention takes."""
+    _int32(batch)
+    n = ctypes.c_int64()
+    _check(lib().ttt_linear_attention_work(ctypes.byref(cfg), batch, seq_len, ctypes.byref(n)))
+    return n.value
+
+
+def ttt_linear_attention(cfg: ttt_linear_attention_config, q, ld_q: int, k, ld_k: int, v, ld_v: int,
+                         decay, starts, state_in, state_out, slot, out, ld_out: int, tokens: int,
+                         batch: int, seq_len: int, work, stream=None) -> None:
+    """Linear attention with a decay per head (fp32 [heads]) over whole sequences: rows b seq_len ..
+    or, with starts (int32 [batch + 1]), starts[b] .. starts[b + 1] - 1 of q, k, v and out; state_in,
+    state_out fp32 [slots, heads, dim_k, dim_v] or None, slot int32 [batch] or None
+    (see include/ttt_mixer.h)."""
+    _int32(batch)
+    torch, dev, st = _here(stream)
+    bf, i32, kn, vn = torch.bfloat16, torch.int32, cfg.heads * cfg.dim_k, cfg.heads * cfg.dim_v
+    pi, po, slots = _pools(state_in, state_out, cfg, dev, torch)
+    _check(lib().ttt_linear_attention(
+        ctypes.byref(cfg), _rows(q, "q", bf, tokens, kn, ld_q, dev), ld_q,
+        _rows(k, "k", bf, tokens, kn, ld_k, dev), ld_k, _rows(v, "v", bf, tokens, vn, ld_v, dev), ld_v,
+        _arg(decay, "decay", torch.float32, cfg.heads, dev), _arg(starts, "starts", i32, batch + 1, dev),
+        pi, po, _arg(slot, "slot", i32, batch, dev), slots, _rows(out, "out", bf, tokens, vn, ld_out, dev),
+        ld_out, tokens, batch, seq_len, *_work(work, dev), st))
+
+
+def ttt_linear_attention_backward_work(cfg: ttt_linear_attention_config, batch: int, seq_len: int) -> int:
+    """Bytes of the workspace that ttt_linear_attention_backward takes."""
+    _int32(batch)
+    n = ctypes.c_int64()
+    _check(lib().ttt_linear_attention_backward_work(ctypes.byref(cfg), batch, seq_len, ctypes.byref(n)))
+    return n.value
+
+
+def ttt_linear_attention_backward(cfg: ttt_linear_attention_config, q, ld_q: int, k, ld_k: int, v, ld_v: int,
+                                  decay, starts, state_in, dout, ld_dout: int, dstate_out, dq, ld_dq: int,
+                                  dk, ld_dk: int, dv, ld_dv: int, dstate_in, tokens: int, batch: int,
+                                  seq_len: int, work, stream=None) -> None:
+    """Backward of ttt_linear_attention: state_in, dstate_out and dstate_in fp32
+    [batch, heads, dim_k, dim_v] or None (see include/ttt_mixer.h)."""
+    _int32(batch)
+    torch, dev, st = _here(stream)
+    bf, kn, vn = torch.bfloat16, cfg.heads * cfg.dim_k, cfg.heads * cfg.dim_v
+
+    def states(t, name):
+        p, n = _pool(t, name, cfg, dev, torch)
+        if t is not None and n < batch:
+            raise TTTError(2, f"{name} of {n} entries for {batch} sequences")
+        return p
+    _check(lib().ttt_linear_attention_backward(
+        ctypes.byref(cfg), _rows(q, "q", bf, tokens, kn, ld_q, dev), ld_q,
+        _rows(k, "k", bf, tokens, kn, ld_k, dev), ld_k, _rows(v, "v", bf, tokens, vn, ld_v, dev), ld_v,
+        _arg(decay, "decay", torch.float32, cfg.heads, dev), _arg(starts, "starts", torch.int32, batch + 1, dev),
+        states(state_in, "state_in"), _rows(dout, "dout", bf, tokens, vn, ld_dout, dev), ld_dout,
+        states(dstate_out, "dstate_out"), _rows(dq, "dq", bf, tokens, kn, ld_dq, dev), ld_dq,
+        _rows(dk, "dk", bf, tokens, kn, ld_dk, dev), ld_dk, _rows(dv, "dv", bf, tokens, vn, ld_dv, dev), ld_dv,
+        states(dstate_in, "dstate_in"), tokens, batch, seq_len, *_work(work, dev), st))
+
+
+def ttt_linear_attention_step(cfg: ttt_linear_attention_config, q, ld_q: int, k, ld_k: int, v, ld_v: int, decay,
+                              state_in, state_out, slot, out, ld_out: int, seqs: int, stream=None) -> None:
+    """One token of each sequence: row s of q, k, v and out, the state in entry slot[s] (or s) of the
+    pools (see include/ttt_mixer.h)."""
+    _int32(seqs)
+    torch, dev, st = _here(stream)
+    bf, kn, vn = torch.bfloat16, cfg.heads * cfg.dim_k, cfg.heads * cfg.dim_v
+    pi, po, slots = _pools(state_in, state_out, cfg, dev, torch)
+    _check(lib().ttt_linear_attention_step(
+        ctypes.byref(cfg), _rows(q, "q", bf, seqs, kn, ld_q, dev), ld_q, _rows(k, "k", bf, seqs, kn, ld_k, dev), ld_k,
+        _rows(v, "v", bf, seqs, vn, ld_v, dev), ld_v, _arg(decay, "decay", torch.float32, cfg.heads, dev), pi, po,
+        _arg(slot, "slot", torch.int32, seqs, dev), slots, _rows(out, "out", bf, seqs, vn, ld_out, dev), ld_out, seqs,
+        st))
+
+
+def make_residual_norm_config(*, dim: int, groups: int = 1, norm_y: bool = False, gate="none", act="bf16",
+                              eps: float = 1e-6) -> ttt_residual_norm_config:
+    _int32(int(dim) | int(groups))
+    return ttt_residual_norm_config(int(dim), int(groups), int(norm_y),
+                                    GATE[gate] if isinstance(gate, str) else int(gate),
+                                    ACT[act] if isinstance(act, str) else int(act), float(eps))
+
+
+def ttt_validate_residual_norm_config(cfg: ttt_residual_norm_config) -> None:
+    _check(lib().ttt_validate_residual_norm_config(ctypes.byref(cfg)))
+
+
+def ttt_residual_norm(cfg: ttt_residual_norm_config, h, ld_h: int, y, ld_y: int, gate, ld_gate: int, y_weight,
+                      res_scale, n_weight, h_out, ld_ho: int, n_out, ld_n: int, tokens: int, stream=None) -> None:
+    """h_out = h + res_scale norm(y) act(gate) and n_out = norm(h_out) over rows of dim elements; what
+    a layer does without is None (see include/ttt_mixer.h)."""
+    torch, dev, st = _here(stream)
+    D, dt = cfg.dim, torch.bfloat16 if cfg.act == 1 else torch.float32
+    _check(lib().ttt_residual_norm(
+        ctypes.byref(cfg), _rows(h, "h", dt, tokens, D, ld_h, dev), ld_h, _rows(y, "y", dt, tokens, D, ld_y, dev), ld_y,
+        _rows(gate, "gate", dt, tokens, D, ld_gate, dev), ld_gate, _arg(y_weight, "y_weight", dt, D, dev),
+        _arg(res_scale, "res_scale", dt, D, dev), _arg(n_weight, "n_weight", dt, D, dev),
+        _rows(h_out, "h_out", dt, tokens, D, ld_ho, dev), ld_ho, _rows(n_out, "n_out", dt, tokens, D, ld_n, dev), ld_n,
+        tokens, st))
+
+
+def ttt_residual_norm_backward_work(cfg: ttt_residual_norm_config, tokens: int) -> int:
+    """Bytes of the workspace that ttt_residual_norm_backward takes where a scale's gradient is wanted."""
+    n = ctypes.c_int64()
+    _check(lib().ttt_residual_norm_backward_work(ctypes.byref(cfg), tokens, ctypes.byref(n)))
+    return n.value
+
+
+def ttt_residual_norm_backward(cfg: ttt_residual_norm_config, h, ld_h: int, y, ld_y: int, gate, ld_gate: int,
+                               y_weight, res_scale, n_weight, dh_out, ld_dho: int, dn, ld_dn: int, dh, ld_dh: int, dy,
+                               ld_dy: int, dgate, ld_dgate: int, dy_weight, dres_scale, dn_weight, work, tokens: int,
+                               stream=None) -> None:
+    """Backward of ttt_residual_norm: dh, dy, dgate (activation dtype) and dy_weight, dres_scale, dn_weight
+    (fp32 [dim]), each None where not wanted; work: device tensor of at least
+    ttt_residual_norm_backward_work bytes (see include/ttt_mixer.h)."""
+    torch, dev, st = _here(stream)
+    D, dt, f32 = cfg.dim, torch.bfloat16 if cfg.act == 1 else torch.float32, torch.float32
+
+    def rows(t, name, ld):
+        return _rows(t, name, dt, tokens, D, ld, dev)
+    _check(lib().ttt_residual_norm_backward(
+        ctypes.byref(cfg), rows(h, "h", ld_h), ld_h, rows(y, "y", ld_y), ld_y, rows(gate, "gate", ld_gate), ld_gate,
+        _arg(y_weight, "y_weight", dt, D, dev), _arg(res_scale, "res_scale", dt, D, dev),
+        _arg(n_weight, "n_weight", dt, D, dev), rows(dh_out, "dh_out", ld_dho), ld_dho, rows(dn, "dn", ld_dn), ld_dn,
+        rows(dh, "dh", ld_dh), ld_dh, rows(dy, "dy", ld_dy), ld_dy, rows(dgate, "dgate", ld_dgate), ld_dgate,
+        _arg(dy_weight, "dy_weight", f32, D, dev), _arg(dres_scale, "dres_scale", f32, D, dev),
+        _arg(dn_weight, "dn_weight", f32, D, dev), *_work(work, dev), tokens, st))

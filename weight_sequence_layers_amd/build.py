@@ -17,8 +17,9 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["ttt_kernels.hip", "ttt_backward.hip", "ttt_small.hip", "ttt_noalloc.hip",
            "ttt_ns_small.hip", "ttt_block.hip", "ttt_attention_rope.hip",
-           "ttt_attention_paged.hip", "ttt_attention_window.hip", "libttt.cpp",
-           "ttt_block.cpp", "ttt_attention.cpp"]
+           "ttt_attention_paged.hip", "ttt_attention_window.hip", "ttt_mixer_linear.hip",
+           "ttt_mixer_step.hip", "ttt_mixer_norm.hip", "libttt.cpp", "ttt_block.cpp",
+           "ttt_attention.cpp", "ttt_mixer.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # no packed-fp32 instructions in device code
