@@ -79,27 +79,58 @@ __host__ __device__ inline int norm_lanes(int D) {
   return n;
 }
 
-// Sum over the n lanes (a power of two) that hold a row or a group.
+// Sum over the n neighbouring lanes (a power of two, the same in every lane) that hold a row or a group,
+// in vector instructions: through the LDS a row's four sums are 24 round trips in a row, more
+// than its loads.  Every lane adds the same two halves at each step, so all get the same sum.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
 __device__ __forceinline__ float lanes_sum(float v, int n) {
-  for (int off = n >> 1; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  if (n > 1) v += dpp<0xB1>(v);     // of pairs: lane ^ 1
+  if (n > 2) v += dpp<0x4E>(v);     // lane ^ 2
+  if (n > 4) v += dpp<0x141>(v);    // the mirrored lane of 8
+  if (n > 8) v += dpp<0x140>(v);    // of 16
+  if (n > 16) {                     // rows of 16 lanes swapped in pairs
+    const uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    v = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+  }
+  if (n > 32) {                     // halves of the wave
+    const uint32_t x = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    v = __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+  }
   return v;
 }
 
+// Sums over a row.  Of a workgroup's row each call takes the other half of `scratch` in turn, so that one
+// barrier keeps its readers from the next call's writers.
 template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float v, int lanes, float* scratch) {
-  if constexpr (BLOCK) return block_sum(v, scratch);
-  else return lanes_sum(v, lanes);
-}
+struct RowSum {
+  float (*scratch)[4];
+  int lanes, turn = 0;
+  __device__ __forceinline__ float operator()(float v) {
+    v = lanes_sum(v, BLOCK ? 64 : lanes);
+    if constexpr (BLOCK) {
+      float* s = scratch[turn];
+      turn ^= 1;
+      if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+      lds_barrier();
+      v = s[0] + s[1] + s[2] + s[3];
+    }
+    return v;
+  }
+};
 
 // 1 / root mean square of each vector's group (or of the row).
 template <bool BLOCK, int NV>
-__device__ __forceinline__ void inv_rms(const float (&ss)[NV], float (&r)[NV], const NormArgs& a, int lanes,
-                                        float* scratch) {
+__device__ __forceinline__ void inv_rms(const float (&ss)[NV], float (&r)[NV], const NormArgs& a, RowSum<BLOCK>& sum) {
   if (a.gw == a.D) {
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) s += ss[v];
-    s = 1.f / sqrtf(row_sum<BLOCK>(s, lanes, scratch) / (float)a.D + a.eps);
+    s = 1.f / sqrtf(sum(s) / (float)a.D + a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) r[v] = s;
   } else {
@@ -108,13 +139,16 @@ __device__ __forceinline__ void inv_rms(const float (&ss)[NV], float (&r)[NV], c
   }
 }
 
-template <typename T, bool BLOCK, int NV>
+// GATE: whether there is a gate; its kind is one select an element.
+template <typename T, bool BLOCK, int NV, bool GATE>
 __global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
-  __shared__ float scratch[4];
+  __shared__ float scratch[2][4];
   const int lanes = BLOCK ? NORM_NT : norm_lanes(a.D);
+  RowSum<BLOCK> sum{scratch, lanes};
   const int lane = (int)threadIdx.x % lanes;
   const int64_t t = BLOCK ? blockIdx.x : (int64_t)blockIdx.x * (NORM_NT / lanes) + threadIdx.x / lanes;
-  const bool in = t < a.tokens;       // the shuffles need a wave's lanes together
+  const bool in = t < a.tokens;       // the sums need a wave's lanes together
+  const bool silu = a.gate_kind == TTT_GATE_SILU;
   Raw8<T> y[NV], h[NV], g[NV];
   int col[NV];
   bool on[NV];
@@ -128,7 +162,7 @@ __global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
     if (on[v]) {
       y[v].load(static_cast<const T*>(a.y) + t * a.ldy + col[v]);
       if (a.h) h[v].load(static_cast<const T*>(a.h) + t * a.ldh + col[v]);
-      if (a.gate_kind) g[v].load(static_cast<const T*>(a.gate) + t * a.ldg + col[v]);
+      if (GATE) g[v].load(static_cast<const T*>(a.gate) + t * a.ldg + col[v]);
     }
   }
   float r[NV];
@@ -142,7 +176,7 @@ __global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss[v] = fmaf(y[v][e], y[v][e], ss[v]);
     }
-    inv_rms<BLOCK, NV>(ss, r, a, lanes, scratch);
+    inv_rms<BLOCK, NV>(ss, r, a, sum);
   }
   float x[NV][8], hh = 0.f;
 #pragma unroll
@@ -155,10 +189,7 @@ __global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float z = y[v][e] * r[v] * w[e];
-      if (a.gate_kind) {
-        const float sg = sigmoid(g[v][e]);
-        z *= a.gate_kind == TTT_GATE_SILU ? g[v][e] * sg : sg;
-      }
+      if (GATE) z *= sigmoid(g[v][e]) * (silu ? g[v][e] : 1.f);
       x[v][e] = fmaf(s[e], z, h[v][e]);
       hh = fmaf(x[v][e], x[v][e], hh);
     }
@@ -168,7 +199,7 @@ __global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
     for (int v = 0; v < NV; ++v)
       if (on[v]) store8(static_cast<T*>(a.ho) + t * a.ldho + col[v], x[v]);
   if (a.n) {
-    const float p = 1.f / sqrtf(row_sum<BLOCK>(hh, lanes, scratch) / (float)a.D + a.eps);
+    const float p = 1.f / sqrtf(sum(hh) / (float)a.D + a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (on[v]) {
@@ -184,12 +215,14 @@ __global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
 
 // Backward: the workgroups walk over the rows, so that the partial sums of the scales' gradients are
 // few; a second launch adds them up in order.
-template <typename T, bool BLOCK, int NV>
+template <typename T, bool BLOCK, int NV, bool GATE>
 __global__ __launch_bounds__(NORM_NT) void k_norm_bwd(NormArgs a) {
-  __shared__ float scratch[4];
+  __shared__ float scratch[2][4];
   __shared__ __attribute__((aligned(16))) float red[NORM_NT * 8];
   const int lanes = BLOCK ? NORM_NT : norm_lanes(a.D);
+  RowSum<BLOCK> sum{scratch, lanes};
   const int lane = (int)threadIdx.x % lanes, rows = NORM_NT / lanes;
+  const bool silu = a.gate_kind == TTT_GATE_SILU;
   int col[NV];
   bool has[NV];
   Raw8<T> wy[NV], rs[NV], wn[NV];
@@ -226,7 +259,7 @@ __global__ __launch_bounds__(NORM_NT) void k_norm_bwd(NormArgs a) {
       if (in && has[v]) {
         y[v].load(static_cast<const T*>(a.y) + t * a.ldy + col[v]);
         if (a.h) h[v].load(static_cast<const T*>(a.h) + t * a.ldh + col[v]);
-        if (a.gate_kind) g[v].load(static_cast<const T*>(a.gate) + t * a.ldg + col[v]);
+        if (GATE) g[v].load(static_cast<const T*>(a.gate) + t * a.ldg + col[v]);
         if (a.dho) dho[v].load(static_cast<const T*>(a.dho) + t * a.lddho + col[v]);
         if (a.dn) dn[v].load(static_cast<const T*>(a.dn) + t * a.lddn + col[v]);
       }
@@ -242,35 +275,36 @@ __global__ __launch_bounds__(NORM_NT) void k_norm_bwd(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss[v] = fmaf(y[v][e], y[v][e], ss[v]);
       }
-      inv_rms<BLOCK, NV>(ss, r, a, lanes, scratch);
+      inv_rms<BLOCK, NV>(ss, r, a, sum);
     }
-    // d: the gradient of h'; z, and the gate's value
-    float z[NV][8], act[NV][8], d[NV][8];
-    float hh = 0.f, ax = 0.f;
+    // the gate's sigmoid, and d, the gradient of h'
+    float sg[NV][8], d[NV][8];
+    if (GATE)
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        act[v][e] = 1.f;
-        if (a.gate_kind) {
-          const float sg = sigmoid(g[v][e]);
-          act[v][e] = a.gate_kind == TTT_GATE_SILU ? g[v][e] * sg : sg;
-        }
-        z[v][e] = y[v][e] * r[v] * wy[v][e] * act[v][e];
-        if (a.dn) {
-          const float x = fmaf(rs[v][e], z[v][e], h[v][e]);
-          hh = fmaf(x, x, hh);
-          ax = fmaf(dn[v][e] * wn[v][e], x, ax);
-        }
-      }
+        for (int e = 0; e < 8; ++e) sg[v][e] = sigmoid(g[v][e]);
+    auto act = [&](int v, int e) __attribute__((always_inline)) { return GATE ? sg[v][e] * (silu ? g[v][e] : 1.f) : 1.f; };
+    auto z = [&](int v, int e) __attribute__((always_inline)) { return y[v][e] * r[v] * wy[v][e] * act(v, e); };
     if (a.dn) {
-      const float p = 1.f / sqrtf(row_sum<BLOCK>(hh, lanes, scratch) / (float)a.D + a.eps);
-      const float m = row_sum<BLOCK>(ax, lanes, scratch) * p / (float)a.D;
+      float hh = 0.f, ax = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = fmaf(rs[v][e], z[v][e], h[v][e]) * p;
+          d[v][e] = fmaf(rs[v][e], z(v, e), h[v][e]);
+          hh = fmaf(d[v][e], d[v][e], hh);
+          ax = fmaf(dn[v][e] * wn[v][e], d[v][e], ax);
+        }
+      hh = sum(hh);
+      ax = sum(ax);
+      const float p = 1.f / sqrtf(hh / (float)a.D + a.eps);
+      const float m = ax * p / (float)a.D;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = d[v][e] * p;
           d[v][e] = fmaf(p, fmaf(-x, m, dn[v][e] * wn[v][e]), dho[v][e]);
           dw[2][v][e] = fmaf(dn[v][e], x, dw[2][v][e]);
         }
@@ -291,26 +325,26 @@ __global__ __launch_bounds__(NORM_NT) void k_norm_bwd(NormArgs a) {
       dot[v] = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        dw[1][v][e] = fmaf(d[v][e], z[v][e], dw[1][v][e]);
-        const float ez = d[v][e] * rs[v][e], yr = y[v][e] * r[v];
-        if (a.gate_kind) {
-          const float gg = g[v][e], sg = sigmoid(gg);
-          const float slope = a.gate_kind == TTT_GATE_SILU ? fmaf(gg * sg, 1.f - sg, sg) : sg * (1.f - sg);
-          dg[e] = ez * yr * wy[v][e] * slope;
+        const float yr = y[v][e] * r[v], u = yr * wy[v][e], ac = act(v, e);
+        dw[1][v][e] = fmaf(d[v][e], u * ac, dw[1][v][e]);
+        const float ez = d[v][e] * rs[v][e];
+        if (GATE) {   // s (1 - s), and for silu s + g s (1 - s)
+          const float s = sg[v][e];
+          dg[e] = ez * u * (silu ? fmaf(ac, 1.f - s, s) : s * (1.f - s));
         }
-        const float f = ez * act[v][e];
+        const float f = ez * ac;
         dw[0][v][e] = fmaf(f, yr, dw[0][v][e]);
         d[v][e] = f * wy[v][e];
         dot[v] = fmaf(d[v][e], yr, dot[v]);
       }
-      if (a.dg && in && has[v]) store8(static_cast<T*>(a.dg) + t * a.lddg + col[v], dg);
+      if (GATE && a.dg && in && has[v]) store8(static_cast<T*>(a.dg) + t * a.lddg + col[v], dg);
     }
     if (a.norm_y) {
       if (a.gw == a.D) {
         float s = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) s += dot[v];
-        s = row_sum<BLOCK>(s, lanes, scratch) / (float)a.D;
+        s = sum(s) / (float)a.D;
 #pragma unroll
         for (int v = 0; v < NV; ++v) dot[v] = s;
       } else {
@@ -382,13 +416,13 @@ int norm_vectors(int D) {
 }
 int64_t norm_rows(int D) { return D > NORM_WAVE_D ? 1 : NORM_NT / norm_lanes(D); }
 
-template <typename T, bool BWD>
-hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
+template <typename T, bool BWD, bool GATE>
+hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
   const int64_t rows = norm_rows(a.D);
   const dim3 grid(BWD ? (unsigned)a.wgs : (unsigned)((a.tokens + rows - 1) / rows)), block(NORM_NT);
-#define NORM_CASE(B, N)                                                             \
-  if constexpr (BWD) hipLaunchKernelGGL((k_norm_bwd<T, B, N>), grid, block, 0, st, a); \
-  else hipLaunchKernelGGL((k_norm<T, B, N>), grid, block, 0, st, a);                 \
+#define NORM_CASE(B, N)                                                                      \
+  if constexpr (BWD) hipLaunchKernelGGL((k_norm_bwd<T, B, N, GATE>), grid, block, 0, st, a); \
+  else hipLaunchKernelGGL((k_norm<T, B, N, GATE>), grid, block, 0, st, a);                   \
   break;
   switch (norm_vectors(a.D) + (a.D > NORM_WAVE_D ? 4 : 0)) {
     case 1: NORM_CASE(false, 1)
@@ -402,6 +436,11 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
   }
 #undef NORM_CASE
   return hipGetLastError();
+}
+
+template <typename T, bool BWD>
+hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
+  return a.gate_kind ? launch_rows<T, BWD, true>(a, st) : launch_rows<T, BWD, false>(a, st);
 }
 
 }  // namespace
