@@ -7,11 +7,11 @@
 //   ds = sum d z,  e = d s,  dg = e u act'(g),  f = e act(g),  dw_y = sum f y r,
 //   dy = r (f w_y - y r mean_g(f w_y y r)).
 //
-// Every tensor is read or written once: the memory bounds it.  A row belongs to some lanes of a wave
-// (up to 2048 elements) or to a workgroup, 8 elements of a lane side by side, so that a group (a
-// power of two of at most 512 elements) lies in neighbouring lanes of one wave; nothing is kept
-// between the forward and the backward, which reads its 16 or 32 bits of h and y again instead of
-// saved statistics.
+// Every tensor is read or written once: the memory bounds it.  A lane holds 8 neighbouring elements of
+// a row, the row some lanes of a wave or up to 16 whole waves, so that a group (a power of two of at
+// most 512 elements) lies in neighbouring lanes of one wave, and few registers keep many waves, and
+// with them many bytes, under way (16 or 32 elements a lane: one wave to a SIMD).  Nothing is kept
+// between the forward and the backward, which reads h and y again instead of saved statistics.
 #include "ttt_device.hpp"
 #include "ttt_mixer_internal.h"
 
@@ -19,7 +19,6 @@ namespace ttt {
 namespace {
 
 constexpr int NORM_NT = 256;
-constexpr int NORM_WGS = 1024;         // workgroups of a backward launch, at most
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -104,262 +103,209 @@ __device__ __forceinline__ float lanes_sum(float v, int n) {
   return v;
 }
 
-// Sums over a row.  Of a workgroup's row each call takes the other half of `scratch` in turn, so that one
+// Sums over a row.  Of a row of W waves each call takes the other half of `scratch` in turn, so that one
 // barrier keeps its readers from the next call's writers.
-template <bool BLOCK>
+template <int W>
 struct RowSum {
-  float (*scratch)[4];
+  float (*scratch)[16];
   int lanes, turn = 0;
   __device__ __forceinline__ float operator()(float v) {
-    v = lanes_sum(v, BLOCK ? 64 : lanes);
-    if constexpr (BLOCK) {
+    if constexpr (W == 1) {
+      return lanes_sum(v, lanes);
+    } else {
+      v = lanes_sum(v, 64);
       float* s = scratch[turn];
       turn ^= 1;
-      if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) s[wave] = v;
       lds_barrier();
-      v = s[0] + s[1] + s[2] + s[3];
+      return total(s + wave / W * W);
     }
-    return v;
+  }
+  // two at once
+  __device__ __forceinline__ void operator()(float& u, float& v) {
+    if constexpr (W == 1) {
+      u = lanes_sum(u, lanes);
+      v = lanes_sum(v, lanes);
+    } else {
+      u = lanes_sum(u, 64);
+      v = lanes_sum(v, 64);
+      float* s = scratch[turn];
+      turn ^= 1;
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+        s[wave] = u;
+        s[32 + wave] = v;   // of the pair of halves that lies 32 floats on
+      }
+      lds_barrier();
+      u = total(s + wave / W * W);
+      v = total(s + 32 + wave / W * W);
+    }
+  }
+  static __device__ __forceinline__ float total(const float* s) {
+    float x = s[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) x += s[i];
+    return x;
   }
 };
 
-// 1 / root mean square of each vector's group (or of the row).
-template <bool BLOCK, int NV>
-__device__ __forceinline__ void inv_rms(const float (&ss)[NV], float (&r)[NV], const NormArgs& a, RowSum<BLOCK>& sum) {
-  if (a.gw == a.D) {
-    float s = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) s += ss[v];
-    s = 1.f / sqrtf(sum(s) / (float)a.D + a.eps);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) r[v] = s;
-  } else {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) r[v] = 1.f / sqrtf(lanes_sum(ss[v], a.gw >> 3) / (float)a.gw + a.eps);
-  }
+template <int W>
+constexpr int norm_threads = W > 4 ? 64 * W : NORM_NT;
+
+// 1 / root mean square of the lane's group (or of the row).
+template <int W>
+__device__ __forceinline__ float inv_rms(float ss, const NormArgs& a, RowSum<W>& sum) {
+  return 1.f / sqrtf((a.gw == a.D ? sum(ss) : lanes_sum(ss, a.gw >> 3)) / (float)a.gw + a.eps);
 }
 
-// GATE: whether there is a gate; its kind is one select an element.
-template <typename T, bool BLOCK, int NV, bool GATE>
-__global__ __launch_bounds__(NORM_NT) void k_norm(NormArgs a) {
-  __shared__ float scratch[2][4];
-  const int lanes = BLOCK ? NORM_NT : norm_lanes(a.D);
-  RowSum<BLOCK> sum{scratch, lanes};
-  const int lane = (int)threadIdx.x % lanes;
-  const int64_t t = BLOCK ? blockIdx.x : (int64_t)blockIdx.x * (NORM_NT / lanes) + threadIdx.x / lanes;
-  const bool in = t < a.tokens;       // the sums need a wave's lanes together
+// W: waves of a row; GATE: whether there is a gate (its kind is one select an element).
+template <typename T, int W, bool GATE>
+__global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
+  __shared__ float scratch[4][16];
+  const int lanes = W == 1 ? norm_lanes(a.D) : 64 * W;
+  RowSum<W> sum{scratch, lanes};
+  const int64_t t = (int64_t)blockIdx.x * (norm_threads<W> / lanes) + threadIdx.x / lanes;
+  const int col = (int)threadIdx.x % lanes * 8;
+  const bool on = t < a.tokens && col < a.D;       // the sums need all lanes
   const bool silu = a.gate_kind == TTT_GATE_SILU;
-  Raw8<T> y[NV], h[NV], g[NV];
-  int col[NV];
-  bool on[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    col[v] = (v * lanes + lane) * 8;
-    on[v] = in && col[v] < a.D;
-    y[v].fill(0.f);
-    h[v].fill(0.f);
-    g[v].fill(0.f);
-    if (on[v]) {
-      y[v].load(static_cast<const T*>(a.y) + t * a.ldy + col[v]);
-      if (a.h) h[v].load(static_cast<const T*>(a.h) + t * a.ldh + col[v]);
-      if (GATE) g[v].load(static_cast<const T*>(a.gate) + t * a.ldg + col[v]);
-    }
+  Raw8<T> y, h, g, w, s;
+  y.fill(0.f);
+  h.fill(0.f);
+  g.fill(0.f);
+  w.fill(1.f);
+  s.fill(1.f);
+  if (on) {
+    y.load(static_cast<const T*>(a.y) + t * a.ldy + col);
+    if (a.h) h.load(static_cast<const T*>(a.h) + t * a.ldh + col);
+    if (GATE) g.load(static_cast<const T*>(a.gate) + t * a.ldg + col);
+    if (a.wy) w.load(static_cast<const T*>(a.wy) + col);
+    if (a.rs) s.load(static_cast<const T*>(a.rs) + col);
   }
-  float r[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) r[v] = 1.f;
+  float r = 1.f;
   if (a.norm_y) {
-    float ss[NV];
+    float ss = 0.f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      ss[v] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss[v] = fmaf(y[v][e], y[v][e], ss[v]);
-    }
-    inv_rms<BLOCK, NV>(ss, r, a, sum);
+    for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+    r = inv_rms<W>(ss, a, sum);
   }
-  float x[NV][8], hh = 0.f;
+  float x[8], hh = 0.f;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    Raw8<T> w, s;
-    w.fill(1.f);
-    s.fill(1.f);
-    if (a.wy && on[v]) w.load(static_cast<const T*>(a.wy) + col[v]);
-    if (a.rs && on[v]) s.load(static_cast<const T*>(a.rs) + col[v]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float z = y[v][e] * r[v] * w[e];
-      if (GATE) z *= sigmoid(g[v][e]) * (silu ? g[v][e] : 1.f);
-      x[v][e] = fmaf(s[e], z, h[v][e]);
-      hh = fmaf(x[v][e], x[v][e], hh);
-    }
+  for (int e = 0; e < 8; ++e) {
+    float z = y[e] * r * w[e];
+    if (GATE) z *= sigmoid(g[e]) * (silu ? g[e] : 1.f);
+    x[e] = fmaf(s[e], z, h[e]);
+    hh = fmaf(x[e], x[e], hh);
   }
-  if (a.ho)
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (on[v]) store8(static_cast<T*>(a.ho) + t * a.ldho + col[v], x[v]);
+  if (a.ho && on) store8(static_cast<T*>(a.ho) + t * a.ldho + col, x);
   if (a.n) {
     const float p = 1.f / sqrtf(sum(hh) / (float)a.D + a.eps);
+    if (on) {
+      w.fill(1.f);
+      if (a.wn) w.load(static_cast<const T*>(a.wn) + col);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if (on[v]) {
-        Raw8<T> w;
-        w.fill(1.f);
-        if (a.wn) w.load(static_cast<const T*>(a.wn) + col[v]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * p * w[e];
-        store8(static_cast<T*>(a.n) + t * a.ldn + col[v], x[v]);
-      }
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * p * w[e];
+      store8(static_cast<T*>(a.n) + t * a.ldn + col, x);
+    }
   }
 }
 
 // Backward: the workgroups walk over the rows, so that the partial sums of the scales' gradients are
 // few; a second launch adds them up in order.
-template <typename T, bool BLOCK, int NV, bool GATE>
-__global__ __launch_bounds__(NORM_NT) void k_norm_bwd(NormArgs a) {
-  __shared__ float scratch[2][4];
-  __shared__ __attribute__((aligned(16))) float red[NORM_NT * 8];
-  const int lanes = BLOCK ? NORM_NT : norm_lanes(a.D);
-  RowSum<BLOCK> sum{scratch, lanes};
-  const int lane = (int)threadIdx.x % lanes, rows = NORM_NT / lanes;
-  const bool silu = a.gate_kind == TTT_GATE_SILU;
-  int col[NV];
-  bool has[NV];
-  Raw8<T> wy[NV], rs[NV], wn[NV];
-  float dw[3][NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    col[v] = (v * lanes + lane) * 8;
-    has[v] = col[v] < a.D;
-    wy[v].fill(1.f);
-    rs[v].fill(1.f);
-    wn[v].fill(1.f);
-    if (has[v]) {
-      if (a.wy) wy[v].load(static_cast<const T*>(a.wy) + col[v]);
-      if (a.rs) rs[v].load(static_cast<const T*>(a.rs) + col[v]);
-      if (a.wn) wn[v].load(static_cast<const T*>(a.wn) + col[v]);
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dw[i][v][e] = 0.f;
+template <typename T, int W, bool GATE>
+__global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
+  constexpr int NT = norm_threads<W>;
+  __shared__ float scratch[4][16];
+  __shared__ __attribute__((aligned(16))) float red[W > 2 ? 1 : NT * 8];
+  const int lanes = W == 1 ? norm_lanes(a.D) : 64 * W, rows = NT / lanes;
+  RowSum<W> sum{scratch, lanes};
+  const int col = (int)threadIdx.x % lanes * 8;
+  const bool has = col < a.D, silu = a.gate_kind == TTT_GATE_SILU;
+  Raw8<T> wy, rs, wn;
+  float dw[3][8];
+  wy.fill(1.f);
+  rs.fill(1.f);
+  wn.fill(1.f);
+  if (has) {
+    if (a.wy) wy.load(static_cast<const T*>(a.wy) + col);
+    if (a.rs) rs.load(static_cast<const T*>(a.rs) + col);
+    if (a.wn) wn.load(static_cast<const T*>(a.wn) + col);
   }
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
   // every lane of a workgroup runs the same rounds: sums need them together
   for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.tokens; t0 += (int64_t)gridDim.x * rows) {
     const int64_t t = t0 + (int)threadIdx.x / lanes;
-    const bool in = t < a.tokens;
-    Raw8<T> y[NV], h[NV], g[NV], dho[NV], dn[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      y[v].fill(0.f);
-      h[v].fill(0.f);
-      g[v].fill(0.f);
-      dho[v].fill(0.f);
-      dn[v].fill(0.f);
-      if (in && has[v]) {
-        y[v].load(static_cast<const T*>(a.y) + t * a.ldy + col[v]);
-        if (a.h) h[v].load(static_cast<const T*>(a.h) + t * a.ldh + col[v]);
-        if (GATE) g[v].load(static_cast<const T*>(a.gate) + t * a.ldg + col[v]);
-        if (a.dho) dho[v].load(static_cast<const T*>(a.dho) + t * a.lddho + col[v]);
-        if (a.dn) dn[v].load(static_cast<const T*>(a.dn) + t * a.lddn + col[v]);
-      }
+    const bool on = has && t < a.tokens;
+    Raw8<T> y, h, g, dho, dn;
+    y.fill(0.f);
+    h.fill(0.f);
+    g.fill(0.f);
+    dho.fill(0.f);
+    dn.fill(0.f);
+    if (on) {
+      y.load(static_cast<const T*>(a.y) + t * a.ldy + col);
+      if (a.h) h.load(static_cast<const T*>(a.h) + t * a.ldh + col);
+      if (GATE) g.load(static_cast<const T*>(a.gate) + t * a.ldg + col);
+      if (a.dho) dho.load(static_cast<const T*>(a.dho) + t * a.lddho + col);
+      if (a.dn) dn.load(static_cast<const T*>(a.dn) + t * a.lddn + col);
     }
-    float r[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) r[v] = 1.f;
+    float r = 1.f;
     if (a.norm_y) {
-      float ss[NV];
+      float ss = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        ss[v] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss[v] = fmaf(y[v][e], y[v][e], ss[v]);
-      }
-      inv_rms<BLOCK, NV>(ss, r, a, sum);
+      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+      r = inv_rms<W>(ss, a, sum);
     }
     // the gate's sigmoid, and d, the gradient of h'
-    float sg[NV][8], d[NV][8];
+    float sg[8], d[8];
     if (GATE)
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sg[v][e] = sigmoid(g[v][e]);
-    auto act = [&](int v, int e) __attribute__((always_inline)) { return GATE ? sg[v][e] * (silu ? g[v][e] : 1.f) : 1.f; };
-    auto z = [&](int v, int e) __attribute__((always_inline)) { return y[v][e] * r[v] * wy[v][e] * act(v, e); };
+      for (int e = 0; e < 8; ++e) sg[e] = sigmoid(g[e]);
+    auto act = [&](int e) __attribute__((always_inline)) { return GATE ? sg[e] * (silu ? g[e] : 1.f) : 1.f; };
     if (a.dn) {
       float hh = 0.f, ax = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[v][e] = fmaf(rs[v][e], z(v, e), h[v][e]);
-          hh = fmaf(d[v][e], d[v][e], hh);
-          ax = fmaf(dn[v][e] * wn[v][e], d[v][e], ax);
-        }
-      hh = sum(hh);
-      ax = sum(ax);
+      for (int e = 0; e < 8; ++e) {
+        d[e] = fmaf(rs[e], y[e] * r * wy[e] * act(e), h[e]);
+        hh = fmaf(d[e], d[e], hh);
+        ax = fmaf(dn[e] * wn[e], d[e], ax);
+      }
+      sum(hh, ax);
       const float p = 1.f / sqrtf(hh / (float)a.D + a.eps);
       const float m = ax * p / (float)a.D;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = d[v][e] * p;
-          d[v][e] = fmaf(p, fmaf(-x, m, dn[v][e] * wn[v][e]), dho[v][e]);
-          dw[2][v][e] = fmaf(dn[v][e], x, dw[2][v][e]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float x = d[e] * p;
+        d[e] = fmaf(p, fmaf(-x, m, dn[e] * wn[e]), dho[e]);
+        dw[2][e] = fmaf(dn[e], x, dw[2][e]);
+      }
     } else {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[v][e] = dho[v][e];
+      for (int e = 0; e < 8; ++e) d[e] = dho[e];
     }
-    if (a.dh)
+    if (a.dh && on) store8(static_cast<T*>(a.dh) + t * a.lddh + col, d);
+    float dg[8], dot = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (in && has[v]) store8(static_cast<T*>(a.dh) + t * a.lddh + col[v], d[v]);
-    float dot[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      float dg[8];
-      dot[v] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float yr = y[v][e] * r[v], u = yr * wy[v][e], ac = act(v, e);
-        dw[1][v][e] = fmaf(d[v][e], u * ac, dw[1][v][e]);
-        const float ez = d[v][e] * rs[v][e];
-        if (GATE) {   // s (1 - s), and for silu s + g s (1 - s)
-          const float s = sg[v][e];
-          dg[e] = ez * u * (silu ? fmaf(ac, 1.f - s, s) : s * (1.f - s));
-        }
-        const float f = ez * ac;
-        dw[0][v][e] = fmaf(f, yr, dw[0][v][e]);
-        d[v][e] = f * wy[v][e];
-        dot[v] = fmaf(d[v][e], yr, dot[v]);
-      }
-      if (GATE && a.dg && in && has[v]) store8(static_cast<T*>(a.dg) + t * a.lddg + col[v], dg);
+    for (int e = 0; e < 8; ++e) {
+      const float yr = y[e] * r, u = yr * wy[e], ac = act(e);
+      dw[1][e] = fmaf(d[e], u * ac, dw[1][e]);
+      const float ez = d[e] * rs[e];
+      if (GATE) dg[e] = ez * u * (silu ? fmaf(ac, 1.f - sg[e], sg[e]) : sg[e] * (1.f - sg[e]));
+      const float f = ez * ac;
+      dw[0][e] = fmaf(f, yr, dw[0][e]);
+      d[e] = f * wy[e];
+      dot = fmaf(d[e], yr, dot);
     }
+    if (GATE && a.dg && on) store8(static_cast<T*>(a.dg) + t * a.lddg + col, dg);
     if (a.norm_y) {
-      if (a.gw == a.D) {
-        float s = 0.f;
+      dot = (a.gw == a.D ? sum(dot) : lanes_sum(dot, a.gw >> 3)) / (float)a.gw;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) s += dot[v];
-        s = sum(s) / (float)a.D;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) dot[v] = s;
-      } else {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) dot[v] = lanes_sum(dot[v], a.gw >> 3) / (float)a.gw;
-      }
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[v][e] = r[v] * fmaf(-y[v][e] * r[v], dot[v], d[v][e]);
+      for (int e = 0; e < 8; ++e) d[e] = r * fmaf(-y[e] * r, dot, d[e]);
     }
-    if (a.dy)
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (in && has[v]) store8(static_cast<T*>(a.dy) + t * a.lddy + col[v], d[v]);
+    if (a.dy && on) store8(static_cast<T*>(a.dy) + t * a.lddy + col, d);
   }
   if (!a.part) return;
   // the workgroup's rows together, in 64 bits and one order
@@ -367,21 +313,18 @@ __global__ __launch_bounds__(NORM_NT) void k_norm_bwd(NormArgs a) {
   for (int i = 0; i < 3; ++i) {
     if (!(i == 0 ? a.dwy : i == 1 ? a.drs : a.dwn)) continue;
     float* part = a.part + ((int64_t)i * a.wgs + blockIdx.x) * a.D;
+    if constexpr (W > 2) {
+      if (has) store8(part + col, dw[i]);
+    } else {
+      __syncthreads();
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if constexpr (BLOCK) {
-        if (has[v]) store8(part + col[v], dw[i][v]);
-      } else {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) red[e * NORM_NT + threadIdx.x] = dw[i][v][e];
-        __syncthreads();
-        for (int c = threadIdx.x; c < lanes * 8; c += NORM_NT) {
-          const int e = c / lanes, l = c - e * lanes, at = (v * lanes + l) * 8 + e;
-          double s = 0.0;
-          for (int k = 0; k < rows; ++k) s += (double)red[e * NORM_NT + k * lanes + l];
-          if (at < a.D) part[at] = (float)s;
-        }
+      for (int e = 0; e < 8; ++e) red[e * NT + threadIdx.x] = dw[i][e];
+      __syncthreads();
+      for (int c = threadIdx.x; c < lanes * 8; c += NT) {
+        const int l = c >> 3, e = c & 7;
+        double s = 0.0;
+        for (int k = 0; k < rows; ++k) s += (double)red[e * NT + k * lanes + l];
+        if (c < a.D) part[c] = (float)s;
       }
     }
   }
@@ -408,34 +351,35 @@ __global__ __launch_bounds__(1024) void k_norm_dw(NormArgs a) {
   if (threadIdx.x < 16 && c < a.D) out[c] = (float)acc[threadIdx.x];
 }
 
-// Whether a row belongs to a workgroup, and 16- or 32-byte runs of a lane.
-constexpr int NORM_WAVE_D = 2048;
-int norm_vectors(int D) {
-  const int n = D > NORM_WAVE_D ? NORM_NT : norm_lanes(D);
-  return (D + 8 * n - 1) / (8 * n);
+// Waves of a row, rows of a workgroup.
+int norm_waves(int D) {
+  int w = 1;
+  while (w * 512 < D) w *= 2;
+  return w;
 }
-int64_t norm_rows(int D) { return D > NORM_WAVE_D ? 1 : NORM_NT / norm_lanes(D); }
+int64_t norm_rows(int D) {
+  const int w = norm_waves(D);
+  return w > 4 ? 1 : NORM_NT / (w > 1 ? 64 * w : norm_lanes(D));
+}
+
+template <typename T, bool BWD, bool GATE, int W>
+hipError_t launch_w(const NormArgs& a, hipStream_t st) {
+  const int64_t rows = norm_rows(a.D);
+  const dim3 block(norm_threads<W>);
+  if constexpr (BWD) hipLaunchKernelGGL((k_norm_bwd<T, W, GATE>), dim3(a.wgs), block, 0, st, a);
+  else hipLaunchKernelGGL((k_norm<T, W, GATE>), dim3((unsigned)((a.tokens + rows - 1) / rows)), block, 0, st, a);
+  return hipGetLastError();
+}
 
 template <typename T, bool BWD, bool GATE>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
-  const int64_t rows = norm_rows(a.D);
-  const dim3 grid(BWD ? (unsigned)a.wgs : (unsigned)((a.tokens + rows - 1) / rows)), block(NORM_NT);
-#define NORM_CASE(B, N)                                                                      \
-  if constexpr (BWD) hipLaunchKernelGGL((k_norm_bwd<T, B, N, GATE>), grid, block, 0, st, a); \
-  else hipLaunchKernelGGL((k_norm<T, B, N, GATE>), grid, block, 0, st, a);                   \
-  break;
-  switch (norm_vectors(a.D) + (a.D > NORM_WAVE_D ? 4 : 0)) {
-    case 1: NORM_CASE(false, 1)
-    case 2: NORM_CASE(false, 2)
-    case 3: NORM_CASE(false, 3)
-    case 4: NORM_CASE(false, 4)
-    case 6: NORM_CASE(true, 2)
-    case 7: NORM_CASE(true, 3)
-    case 8: NORM_CASE(true, 4)
-    default: return hipErrorInvalidValue;
+  switch (norm_waves(a.D)) {
+    case 1: return launch_w<T, BWD, GATE, 1>(a, st);
+    case 2: return launch_w<T, BWD, GATE, 2>(a, st);
+    case 4: return launch_w<T, BWD, GATE, 4>(a, st);
+    case 8: return launch_w<T, BWD, GATE, 8>(a, st);
+    default: return launch_w<T, BWD, GATE, 16>(a, st);
   }
-#undef NORM_CASE
-  return hipGetLastError();
 }
 
 template <typename T, bool BWD>
@@ -447,7 +391,8 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
 
 int32_t residual_norm_wgs(int32_t D, int64_t tokens) {
   const int64_t rows = norm_rows(D), n = (tokens + rows - 1) / rows;
-  return (int32_t)(n < NORM_WGS ? n : NORM_WGS);
+  const int w = norm_waves(D), most = w > 8 ? 256 : w > 4 ? 384 : 768;   // as many as run at once
+  return (int32_t)(n < most ? n : most);
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, int bf16, hipStream_t st) {
