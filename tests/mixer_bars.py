@@ -3,7 +3,7 @@ the oracle and see them exceed the bars.
 
 U = 2^-24 and R = 2^-8 are the half steps of fp32 and bf16 relative to the value.
 
-Linear attention, for one head, in chunks of C = 32 tokens from the sequence's first (backward in
+Linear attention, for one head, in chunks of C = 64 tokens from the sequence's first (backward in
 time: last) token.  Every sum is bounded by that of its terms' absolute values, A.  A state takes
 per chunk a product with a power (2 U), at most 3 C additions of products of bf16 numbers (the decayed
 value in three parts: 3 C U), the decayed value's own roundings (power, scale, product: 4 U), and one
@@ -27,7 +27,7 @@ import numpy as np
 
 U = 2.0 ** -24
 R = 2.0 ** -8
-C = 32
+C = 64
 
 
 def layer(q, k, v, decay, x0, scale_p, scale_s, scale_w, forward):

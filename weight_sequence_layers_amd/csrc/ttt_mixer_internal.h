@@ -15,7 +15,7 @@ __device__ __forceinline__ __attribute__((address_space(1))) T* as_global(T* p) 
 }
 
 // ------------------------------------------------------------------------ linear attention
-constexpr int LIN_C = 32;          // tokens of a chunk
+constexpr int LIN_C = 64;          // tokens of a chunk
 constexpr int LIN_MAX_ROLES = 3;
 
 // One recurrence over the sequences, S <- decay S + k v^T read by q: the layer itself, or one of its

@@ -28,20 +28,21 @@ __device__ __forceinline__ int lin_swz(int r) {
 template <int P, int NW>
 struct LinLoad {
   static constexpr int ROWS = 1024 / P;                     // rows of one wave's load
-  static constexpr int N = LIN_C / ROWS;                    // loads of a tile
-  static constexpr int PER = (N + NW - 1) / NW;
-  int32_t off[PER];
+  static constexpr int N = LIN_C / ROWS / NW;               // loads of a wave
+  static constexpr int VAR = NW * ROWS < 16 ? 16 / (NW * ROWS) : 1;   // the swizzle repeats after 16 rows
+  int32_t off[VAR], step;
   uint32_t ld2;
-  int wave;
+  int slice;
   __device__ __forceinline__ void init(int64_t ld, int rev) {
-    const int lane = threadIdx.x & 63;
-    wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     ld2 = (uint32_t)(ld * 2);
+    slice = wave * 1024;
+    const int32_t row = rev ? -(int32_t)ld2 : (int32_t)ld2;
+    step = NW * ROWS * VAR * row;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int r = (wave + i * NW) * ROWS + lane / (P / 16), c = (lane % (P / 16)) ^ lin_swz<P>(r);
-      const int32_t at = r * (int32_t)ld2;
-      off[i] = (rev ? -at : at) + c * 16;
+    for (int i = 0; i < VAR; ++i) {
+      const int r = (wave + i * NW) * ROWS + lane / (P / 16);
+      off[i] = r * row + ((lane % (P / 16)) ^ lin_swz<P>(r)) * 16;
     }
   }
   // The n rows at p, in their order or (rev) from the last to the first; the others read as 0:
@@ -50,11 +51,10 @@ struct LinLoad {
     const uint32_t last = (uint32_t)(n - 1) * ld2;
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)(last + P), 0x00020000);
-    const uint32_t top = rev ? last : 0;
+    const int32_t top = rev ? (int32_t)last : 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (N % NW == 0 || wave + i * NW < N)   // wave-uniform
-        dma16(rs, (lds_void_t*)(tile + (wave + i * NW) * 1024), (uint32_t)off[i] + top);
+    for (int i = 0; i < N; ++i)
+      dma16(rs, (lds_void_t*)(tile + slice + i * NW * 1024), (uint32_t)(off[i % VAR] + (i / VAR) * step + top));
   }
 };
 
@@ -71,16 +71,18 @@ struct LinAt {
   }
 };
 
-// Row lane % 32, elements base + 4 (lane / 32) + (0..3) and + 8: the order in which a lane holds the
-// rows of an accumulator.  base a multiple of 16.
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Row base_row + lane % 32, elements base + 4 (lane / 32) + (0..3) and + 8: the order in which a lane
+// holds the rows of an accumulator.  base_row a multiple of 32, base of 16.
 template <int P>
-__device__ __forceinline__ bf16x8 lin_row(const char* tile, const LinAt<P>& at, int base) {
+__device__ __forceinline__ bf16x8 lin_row(const char* tile, const LinAt<P>& at, int base_row, int base) {
   s16x4 x[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) x[i] = *reinterpret_cast<const s16x4*>(tile + (at.row ^ (base * 2) ^ (i << 4)));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  const s16x8 v = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8, v);
+  for (int i = 0; i < 2; ++i)
+    x[i] = *reinterpret_cast<const s16x4*>(tile + base_row * P + (at.row ^ (base * 2) ^ (i << 4)));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 // Element base + lane % 32 of rows row + 4 (lane / 32) + (0..3) and + 8.  base a multiple of 32, row
 // of 16.
@@ -92,27 +94,38 @@ __device__ __forceinline__ bf16x8 lin_col(const char* tile, const LinAt<P>& at, 
     const char* p = tile + (row + 8 * i) * P + (at.col ^ (base << 1) ^ (i << 5));
     x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
   }
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  const s16x8 v = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8, v);
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 __device__ __forceinline__ f32x16 lin_mma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// Two numbers rounded to bf16, and their values.
+__device__ __forceinline__ uint32_t lin_pack(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+__device__ __forceinline__ float lin_first(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
+__device__ __forceinline__ float lin_second(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
+
 // x as N bf16 numbers whose sum it is, to 8 N bits.
 template <int N>
 __device__ __forceinline__ void lin_split(const float (&x)[8], bf16x8 (&p)[N]) {
+  u32x4 u[N];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float r = x[e];
+  for (int e = 0; e < 4; ++e) {
+    float a = x[2 * e], b = x[2 * e + 1];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      p[i][e] = static_cast<__bf16>(r);
-      r -= static_cast<float>(p[i][e]);
+      u[i][e] = lin_pack(a, b);
+      a -= lin_first(u[i][e]);
+      b -= lin_second(u[i][e]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = __builtin_bit_cast(bf16x8, u[i]);
 }
 
 // a^n, in 64 bits: a table made of rounded products would drift over long sequences
@@ -125,205 +138,342 @@ __device__ __forceinline__ float lin_power(float a, int n) {
   return (float)p;
 }
 
-// A workgroup walks one segment of one sequence, head and role; its NW waves hold 32 columns of the
-// state each, all DA rows of it, as accumulators.  The output is computed transposed (a lane is a
-// token), so that the accumulators of the state and of the scores are the operands of the products
-// that follow as they lie, in the order of an accumulator's rows; q and k are read from LDS in
-// that order.  Every wave computes the chunk's 32 x 32 scores itself: an eighth more products, and no
-// exchange between waves.
-// OUT false: only the segment's own sum, from zeros.
-template <int DA, int NW, bool OUT>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 1 : 2)))
-void k_linear(LinArgs a) {
-  constexpr int PA = DA * 2, PV = NW * 64;                    // bytes of a tile's row
-  constexpr int KO = OUT ? LIN_C * PA : 0, VO = KO + LIN_C * PA, STAGE = VO + LIN_C * PV;
-  constexpr int RT = DA / 32;
-  __shared__ __attribute__((aligned(1024))) char st0[STAGE];
-  __shared__ __attribute__((aligned(1024))) char st1[STAGE];
-  __shared__ float pw[LIN_C + 1];
-  auto uniform = [](int x) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(x); };
-  int id = xcd_block(blockIdx.x, a.total);
-  const int slice = uniform(id % a.slices);
-  id = uniform(id / a.slices);
-  const int ri = uniform(id % a.roles);
-  id = uniform(id / a.roles);
-  const int h = uniform(id % a.heads);
-  id = uniform(id / a.heads);
-  const int nseg = OUT ? a.nseg : a.nseg - 1;
-  const int seg = uniform(id % nseg), b = uniform(id / nseg);
-  const LinRole& r = a.role[ri];
-  const int rev = r.rev;
+// Waits until at most n of the wave's memory operations are under way (loads end in the order of
+// their issue), then for the workgroup: what the waves had loaded is there, what they had read is free.
+template <int N>
+__device__ __forceinline__ void lin_wait() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+  lds_barrier();
+}
+
+// A workgroup's place in a launch: role, sequence, head, segment and columns.
+struct LinPlace {
+  int slice;       // (in the order in which they are taken from the workgroup's number)
+  const LinRole& r;
+  int h, seg, b, len, t0, cnt, chunks;
   int64_t row0;
-  int len;
-  lin_span(a.starts, b, a.tokens, a.T, row0, len);
-  const int t0 = seg * a.L;                                  // first token, in the role's time
-  if (OUT ? seg > 0 && t0 >= len : t0 + a.L >= len) return;
-  const int cnt = min(a.L, len - t0), chunks = (cnt + LIN_C - 1) / LIN_C;
+  bool none;       // nothing to do
+  static __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+  static __device__ __forceinline__ int take(int& id, int n) {
+    const int q = uniform(id / n), x = uniform(id - q * n);
+    id = q;
+    return x;
+  }
+  __device__ __forceinline__ LinPlace(const LinArgs& a, int nseg, int id, bool out)
+      : slice(take(id, a.slices)), r(a.role[take(id, a.roles)]), h(take(id, a.heads)), seg(take(id, nseg)), b(id) {
+    lin_span(a.starts, b, a.tokens, a.T, row0, len);
+    t0 = seg * a.L;                                          // first token, in the role's time
+    none = out ? seg > 0 && t0 >= len : t0 + a.L >= len;
+    cnt = min(a.L, len - t0);
+    chunks = (cnt + LIN_C - 1) / LIN_C;
+  }
+};
 
-  const int lane = threadIdx.x & 63, hl = lane >> 5, li = lane & 31;
-  const int wave = uniform((int)(threadIdx.x >> 6));
-  const float lam = a.decay[h];
-  if (threadIdx.x <= LIN_C) pw[threadIdx.x] = lin_power(lam, (int)threadIdx.x);
+// Powers of the decay, and the weights of a chunk's tokens in the state behind it: of 64 tokens, and of
+// the last chunk's.
+struct LinTables {
+  float pw[LIN_C + 4];
+  float wt[2][LIN_C];
+  __device__ __forceinline__ void init(float lam, const LinPlace& at) {
+    const int i = threadIdx.x, last = at.cnt - (at.chunks - 1) * LIN_C;
+    if (i <= LIN_C) pw[i] = lin_power(lam, i);
+    if (i < LIN_C) {
+      wt[0][i] = lin_power(lam, LIN_C - 1 - i) * at.r.scale_w;
+      wt[1][i] = lin_power(lam, max(last - 1 - i, 0)) * at.r.scale_w;   // rows behind the last are 0
+    }
+  }
+};
 
-  const int col0 = slice * 32 * NW;                          // the workgroup's first column
-  const u16* qb = r.q + (int64_t)h * DA;
-  const u16* kb = r.k + (int64_t)h * DA;
-  const u16* vb = r.v + (int64_t)h * a.DB + col0;
-  LinLoad<PA, NW> lq, lk;
-  LinLoad<PV, NW> lv;
-  if (OUT) lq.init(r.ldq, rev);
-  lk.init(r.ldk, rev);
-  lv.init(r.ldv, rev);
-  auto issue = [&](char* st, int c) __attribute__((always_inline)) {
-    const int n = min(LIN_C, cnt - c * LIN_C), t = t0 + c * LIN_C;
-    const int64_t row = row0 + (rev ? len - t - n : t);
-    if (OUT) lq.issue(st, qb + row * r.ldq, n, rev);
-    lk.issue(st + KO, kb + row * r.ldk, n, rev);
-    lv.issue(st + VO, vb + row * r.ldv, n, rev);
-  };
-  if (chunks) issue(st0, 0);
-
-  // the state: element v of tile rt is row 32 rt + 8 (v / 4) + 4 hl + v % 4, column li of the wave's
-  const int64_t elems = (int64_t)DA * a.DB;
-  const int colw = col0 + 32 * wave + li;
-  const int64_t entry = lin_slot(a.slot, b, a.slots);
+// The state of a wave: element v of tile rt is row 32 rt + 8 (v / 4) + 4 hl + v % 4, column li of its 32.
+template <int RT>
+struct LinState {
   f32x16 s[RT];
-  const float* init = nullptr;
-  if (OUT) {
-    if (r.ws) init = r.ws + (((int64_t)b * a.heads + h) * a.nseg + seg) * elems;
-    else if (r.init && entry >= 0) init = r.init + (entry * a.heads + h) * elems;
-  }
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) s[rt] = f32x16{};
-  if (init) {
+  // s <- f s + k^T (w v) over a chunk; vf: the wave's columns of v
+  template <int PA>
+  __device__ __forceinline__ void add(const char* k, const LinAt<PA>& at, const bf16x8 (&vf)[LIN_C / 16], const float* wt,
+                                      float f, int hl) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int row = 32 * rt + 8 * g + 4 * hl;
-        if (r.trans) {
-          const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(init + (int64_t)colw * DA + row));
+      for (int v = 0; v < 16; ++v) s[rt][v] *= f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[rt][4 * g + e] = x[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[rt][4 * g + e] = *as_global(init + (int64_t)(row + e) * a.DB + colw);
-        }
-      }
-  }
-  LinAt<PA> at;
-  LinAt<PV> av;
-  at.init();
-  av.init();
-  __syncthreads();
-  // element v of the scores: key 8 (v / 4) + 4 hl + v % 4 of the chunk, query li
-  float dm[16];
-  if (OUT)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int j = 8 * (v >> 2) + 4 * hl + (v & 3);
-      dm[v] = li >= j ? pw[li >= j ? li - j : 0] * r.scale_p : 0.f;
-    }
-
-  auto step = [&](const char* cur, char* nxt, int c) __attribute__((always_inline)) {
-    const int n = min(LIN_C, cnt - c * LIN_C);
-    if (c + 1 < chunks) issue(nxt, c + 1);
-    // backward in time the state before the first token (the gradient of the last state) is that
-    // of the first token itself: one power less
-    const int e0 = rev && t0 + c == 0 ? 0 : 1;
-    bf16x8 vf[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) vf[x] = lin_col<PV>(cur + VO, av, 32 * wave, 16 * x);
-    if constexpr (OUT) {
-      f32x16 p = f32x16{}, o = f32x16{}, o1 = f32x16{};
-#pragma unroll
-      for (int x = 0; x < 2 * RT; ++x) {
-        const bf16x8 qf = lin_row<PA>(cur, at, 16 * x);
-        p = lin_mma(lin_row<PA>(cur + KO, at, 16 * x), qf, p);
-        float sv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sv[e] = s[x >> 1][8 * (x & 1) + e];
-        bf16x8 sp[2];
-        lin_split(sv, sp);
-        o = lin_mma(sp[0], qf, o);
-        o1 = lin_mma(sp[1], qf, o1);
-      }
-      const float f = pw[li + e0] * r.scale_s;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) o[v] = (o[v] + o1[v]) * f;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float pv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pv[e] = p[8 * x + e] * dm[8 * x + e];
-        bf16x8 pp[2];
-        lin_split(pv, pp);
-        o = lin_mma(vf[x], pp[0], o);
-        o = lin_mma(vf[x], pp[1], o);
-      }
-      if (li < n) {
-        const int t = t0 + c * LIN_C + li;
-        u16* row = r.out + (row0 + (rev ? len - 1 - t : t)) * r.ldo + (int64_t)h * a.DB + col0 + 32 * wave + 4 * hl;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-          *as_global(reinterpret_cast<u32x2*>(row + 8 * g)) =
-              u32x2{f2bf(o[4 * g]) | ((uint32_t)f2bf(o[4 * g + 1]) << 16),
-                    f2bf(o[4 * g + 2]) | ((uint32_t)f2bf(o[4 * g + 3]) << 16)};
-        }
-      }
-    }
-    const float sd = pw[n - 1 + e0];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) s[rt][v] *= sd;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < LIN_C / 16; ++x) {
       float w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = 16 * x + 8 * (e >> 2) + 4 * hl + (e & 3);   // rows behind the last token are 0
-        w[e] = static_cast<float>(vf[x][e]) * (pw[max(n - 1 - j, 0)] * r.scale_w);
+      for (int g = 0; g < 2; ++g) {
+        const f32x4 t = *reinterpret_cast<const f32x4*>(wt + 16 * x + 8 * g + 4 * hl);
+        const u32x4 u = __builtin_bit_cast(u32x4, vf[x]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          w[4 * g + 2 * e] = lin_first(u[2 * g + e]) * t[2 * e];
+          w[4 * g + 2 * e + 1] = lin_second(u[2 * g + e]) * t[2 * e + 1];
+        }
       }
       bf16x8 wp[3];
       lin_split(w, wp);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const bf16x8 kf = lin_col<PA>(cur + KO, at, 32 * rt, 16 * x);
+        const bf16x8 kf = lin_col<PA>(k, at, 32 * rt, 16 * x);
 #pragma unroll
         for (int i = 0; i < 3; ++i) s[rt] = lin_mma(kf, wp[i], s[rt]);
       }
     }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-  };
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  int c = 0;
-  for (; c + 1 < chunks; c += 2) {
-    step(st0, st1, c);
-    step(st1, st0, c + 1);
   }
-  if (c < chunks) step(st0, st1, c);
-
-  float* fin = nullptr;
-  float f = 1.f;
-  if constexpr (OUT) {
-    if (r.fin && entry >= 0 && t0 + a.L >= len) fin = r.fin + (entry * a.heads + h) * elems;
-    if (rev && len > 0) f = lam;   // behind the last step back lies the state before the first token
-  } else {
-    fin = r.ws + (((int64_t)b * a.heads + h) * a.nseg + seg) * elems;
-  }
-  if (fin) {
+  __device__ __forceinline__ void store(float* p, int ld, int hl, float f) const {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int row = 32 * rt + 8 * (v >> 2) + 4 * hl + (v & 3);
-        *as_global(fin + (int64_t)row * a.DB + colw) = s[rt][v] * f;
+      for (int v = 0; v < 16; ++v)
+        *as_global(p + (int64_t)(32 * rt + 8 * (v >> 2) + 4 * hl + (v & 3)) * ld) = s[rt][v] * f;
+  }
+};
+
+// A workgroup walks one segment of one sequence, head and role, 64 tokens at a time; its NW waves hold 32
+// columns of the state each, all DA rows of it, as accumulators.  The output is computed transposed
+// (a lane is a token), so that the accumulators of the state and of the scores are the operands of the
+// products that follow as they lie, in the order of an accumulator's rows; q and k are read from LDS
+// in that order.  Every wave computes the chunk's scores itself (three tiles of 32 x 32: a fifth of its
+// products), which saves an exchange between the waves.
+//
+// Four areas of LDS take turns: while q, k and v of a chunk lie in three, the next chunk's q comes into
+// the fourth; once q has been read its k comes into q's, and once all has been read its v into k's: each
+// load has half a chunk's work or more to arrive.
+template <int DA, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 1 : 2)))
+void k_linear(LinArgs a) {
+  constexpr int PA = DA * 2, PV = NW * 64;                    // bytes of a tile's row
+  constexpr int AREA = LIN_C * (PA > PV ? PA : PV), RT = DA / 32;
+  __shared__ __attribute__((aligned(1024))) char a0[AREA];
+  __shared__ __attribute__((aligned(1024))) char a1[AREA];
+  __shared__ __attribute__((aligned(1024))) char a2[AREA];
+  __shared__ __attribute__((aligned(1024))) char a3[AREA];
+  __shared__ __attribute__((aligned(16))) LinTables tb;
+  const LinPlace at(a, a.nseg, xcd_block(blockIdx.x, a.total), true);
+  if (at.none) return;
+  const LinRole& r = at.r;
+  const int rev = r.rev, h = at.h, b = at.b, len = at.len, t0 = at.t0, cnt = at.cnt, chunks = at.chunks;
+  const int lane = threadIdx.x & 63, hl = lane >> 5, li = lane & 31;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const float lam = a.decay[h];
+
+  const int col0 = at.slice * 32 * NW;                       // the workgroup's first column
+  const u16* qb = r.q + (int64_t)h * DA;
+  const u16* kb = r.k + (int64_t)h * DA;
+  const u16* vb = r.v + (int64_t)h * a.DB + col0;
+  LinLoad<PA, NW> lq, lk;
+  LinLoad<PV, NW> lv;
+  lq.init(r.ldq, rev);
+  lk.init(r.ldk, rev);
+  lv.init(r.ldv, rev);
+  auto size = [&](int c) __attribute__((always_inline)) { return min(LIN_C, cnt - c * LIN_C); };
+  auto row = [&](int c) __attribute__((always_inline)) {     // of chunk c's lowest token
+    const int t = t0 + c * LIN_C;
+    return at.row0 + (rev ? len - t - size(c) : t);
+  };
+  if (chunks) {
+    lq.issue(a0, qb + row(0) * r.ldq, size(0), rev);
+    lk.issue(a1, kb + row(0) * r.ldk, size(0), rev);
+    lv.issue(a2, vb + row(0) * r.ldv, size(0), rev);
+  }
+  tb.init(lam, at);
+
+  const int64_t elems = (int64_t)DA * a.DB;
+  const int colw = col0 + 32 * wave + li;
+  const int64_t entry = lin_slot(a.slot, b, a.slots);
+  LinState<RT> S;
+  const float* init = nullptr;
+  if (r.ws) init = r.ws + (((int64_t)b * a.heads + h) * a.nseg + at.seg) * elems;
+  else if (r.init && entry >= 0) init = r.init + (entry * a.heads + h) * elems;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) S.s[rt] = f32x16{};
+  if (init) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int i = 32 * rt + 8 * g + 4 * hl;
+        if (r.trans) {
+          const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(init + (int64_t)colw * DA + i));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S.s[rt][4 * g + e] = x[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S.s[rt][4 * g + e] = *as_global(init + (int64_t)(i + e) * a.DB + colw);
+        }
       }
   }
+  LinAt<PA> ta;
+  LinAt<PV> tv;
+  ta.init();
+  tv.init();
+  lin_wait<0>();
+  // element v of a tile of scores: key 8 (v / 4) + 4 hl + v % 4, query li
+  float dm[16];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int j = 8 * (v >> 2) + 4 * hl + (v & 3);
+    dm[v] = li >= j ? tb.pw[li >= j ? li - j : 0] * r.scale_p : 0.f;
+  }
+  const float f21 = tb.pw[li + 1] * (r.scale_p / r.scale_w);   // with wt's second half: a^(32 + li - j)
+
+  uint32_t ow[2][8];
+  auto step = [&](char* qa, char* ka, char* va, char* spare, int c) __attribute__((always_inline)) {
+    const int n = size(c);
+    const bool more = c + 1 < chunks;
+    if (more) lq.issue(spare, qb + row(c + 1) * r.ldq, size(c + 1), rev);
+    // backward in time the state before the first token (the gradient of the last state) is that
+    // of the first token itself: one power less
+    const int e0 = rev && t0 + c == 0 ? 0 : 1;
+    f32x16 p11 = f32x16{}, p21 = f32x16{}, p22 = f32x16{}, o1 = f32x16{}, o2 = f32x16{};
+#pragma unroll
+    for (int x = 0; x < 2 * RT; ++x) {
+      const bf16x8 q1 = lin_row<PA>(qa, ta, 0, 16 * x), q2 = lin_row<PA>(qa, ta, 32, 16 * x);
+      const bf16x8 k1 = lin_row<PA>(ka, ta, 0, 16 * x), k2 = lin_row<PA>(ka, ta, 32, 16 * x);
+      p11 = lin_mma(k1, q1, p11);
+      p21 = lin_mma(k1, q2, p21);
+      p22 = lin_mma(k2, q2, p22);
+      float sv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sv[e] = S.s[x >> 1][8 * (x & 1) + e];
+      bf16x8 sp[2];
+      lin_split(sv, sp);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o1 = lin_mma(sp[i], q1, o1);
+        o2 = lin_mma(sp[i], q2, o2);
+      }
+      if (DA == 256) __builtin_amdgcn_sched_barrier(0);   // all fragments read ahead would not fit
+    }
+    if (more) lin_wait<LinLoad<PA, NW>::N>();   // v is there, q is free
+    else lin_wait<0>();
+    if (more) lk.issue(qa, kb + row(c + 1) * r.ldk, size(c + 1), rev);
+    bf16x8 vf[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) vf[x] = lin_col<PV>(va, tv, 32 * wave, 16 * x);
+    const float f1 = tb.pw[li + e0] * r.scale_s, f2 = tb.pw[32 + li + e0] * r.scale_s;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      o1[v] *= f1;
+      o2[v] *= f2;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float pv[3][8];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const f32x4 t = *reinterpret_cast<const f32x4*>(&tb.wt[0][32 + 16 * x + 8 * g + 4 * hl]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int v = 8 * x + 4 * g + e;
+          pv[0][4 * g + e] = p11[v] * dm[v];
+          pv[1][4 * g + e] = p21[v] * (f21 * t[e]);
+          pv[2][4 * g + e] = p22[v] * dm[v];
+        }
+      }
+      bf16x8 pp[3][2];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) lin_split(pv[i], pp[i]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o1 = lin_mma(vf[x], pp[0][i], o1);
+        o2 = lin_mma(vf[x], pp[1][i], o2);
+        o2 = lin_mma(vf[2 + x], pp[2][i], o2);
+      }
+    }
+    // the halves of the wave swapped in pairs: 8 neighbouring elements of a row in a lane
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; g += 2)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const f32x16& o = i ? o2 : o1;
+          const auto w = __builtin_amdgcn_permlane32_swap(lin_pack(o[4 * g + 2 * e], o[4 * g + 2 * e + 1]),
+                                                          lin_pack(o[4 * g + 4 + 2 * e], o[4 * g + 5 + 2 * e]), false, false);
+          ow[i][2 * g + e] = w[0];
+          ow[i][2 * g + 2 + e] = w[1];
+        }
+    S.template add<PA>(ka, ta, vf, tb.wt[more ? 0 : 1], tb.pw[n - 1 + e0], hl);
+    lin_wait<0>();   // the next chunk's q and k are there, k and v are free
+    if (more) lv.issue(ka, vb + row(c + 1) * r.ldv, size(c + 1), rev);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (32 * i + li < n) {
+        const int t = t0 + c * LIN_C + 32 * i + li;
+        u16* y = r.out + (at.row0 + (rev ? len - 1 - t : t)) * r.ldo + (int64_t)h * a.DB + col0 + 32 * wave + 8 * hl;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          *as_global(reinterpret_cast<u32x4*>(y + 16 * g)) =
+              u32x4{ow[i][4 * g], ow[i][4 * g + 1], ow[i][4 * g + 2], ow[i][4 * g + 3]};
+      }
+  };
+  int c = 0;
+  for (; c + 4 <= chunks; c += 4) {
+    step(a0, a1, a2, a3, c);
+    step(a3, a0, a1, a2, c + 1);
+    step(a2, a3, a0, a1, c + 2);
+    step(a1, a2, a3, a0, c + 3);
+  }
+  if (c < chunks) step(a0, a1, a2, a3, c);
+  if (c + 1 < chunks) step(a3, a0, a1, a2, c + 1);
+  if (c + 2 < chunks) step(a2, a3, a0, a1, c + 2);
+
+  if (r.fin && entry >= 0 && t0 + a.L >= len)   // behind the last step back lies the state before the first token
+    S.store(r.fin + (entry * a.heads + h) * elems + colw, a.DB, hl, rev && len > 0 ? lam : 1.f);
+}
+
+// Each segment's own sum, from zeros, of all but the last.
+template <int DA, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 1 : 2)))
+void k_linear_states(LinArgs a) {
+  constexpr int PA = DA * 2, PV = NW * 64, VO = LIN_C * PA, RT = DA / 32;
+  __shared__ __attribute__((aligned(1024))) char st0[LIN_C * (PA + PV)];
+  __shared__ __attribute__((aligned(1024))) char st1[LIN_C * (PA + PV)];
+  __shared__ __attribute__((aligned(16))) LinTables tb;
+  const LinPlace at(a, a.nseg - 1, xcd_block(blockIdx.x, a.total), false);
+  if (at.none) return;
+  const LinRole& r = at.r;
+  const int rev = r.rev, lane = threadIdx.x & 63, hl = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int col0 = at.slice * 32 * NW;
+  const u16* kb = r.k + (int64_t)at.h * DA;
+  const u16* vb = r.v + (int64_t)at.h * a.DB + col0;
+  LinLoad<PA, NW> lk;
+  LinLoad<PV, NW> lv;
+  lk.init(r.ldk, rev);
+  lv.init(r.ldv, rev);
+  auto issue = [&](char* st, int c) __attribute__((always_inline)) {   // every chunk is whole
+    const int t = at.t0 + c * LIN_C;
+    const int64_t row = at.row0 + (rev ? at.len - t - LIN_C : t);
+    lk.issue(st, kb + row * r.ldk, LIN_C, rev);
+    lv.issue(st + VO, vb + row * r.ldv, LIN_C, rev);
+  };
+  issue(st0, 0);
+  tb.init(a.decay[at.h], at);
+  LinState<RT> S;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) S.s[rt] = f32x16{};
+  LinAt<PA> ta;
+  LinAt<PV> tv;
+  ta.init();
+  tv.init();
+  lin_wait<0>();
+  auto step = [&](const char* cur, char* nxt, int c) __attribute__((always_inline)) {
+    if (c + 1 < at.chunks) issue(nxt, c + 1);
+    bf16x8 vf[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) vf[x] = lin_col<PV>(cur + VO, tv, 32 * wave, 16 * x);
+    S.template add<PA>(cur, ta, vf, tb.wt[0], tb.pw[LIN_C], hl);
+    lin_wait<0>();
+  };
+  int c = 0;
+  for (; c + 1 < at.chunks; c += 2) {
+    step(st0, st1, c);
+    step(st1, st0, c + 1);
+  }
+  if (c < at.chunks) step(st0, st1, c);
+  S.store(r.ws + (((int64_t)at.b * a.heads + at.h) * a.nseg + at.seg) * DA * a.DB + col0 + 32 * wave + (lane & 31), a.DB,
+          hl, 1.f);
 }
 
 // From the segments' own sums to the states before each: a thread takes four elements of a state
@@ -361,28 +511,30 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinArgs a, int DA) {
   }
 }
 
-template <int DA, bool OUT>
-hipError_t launch_nw(const LinArgs& a, int NW, hipStream_t st) {
-  if (NW == 2) hipLaunchKernelGGL((k_linear<DA, 2, OUT>), dim3(a.total), dim3(128), 0, st, a);
-  else hipLaunchKernelGGL((k_linear<DA, 4, OUT>), dim3(a.total), dim3(256), 0, st, a);
+template <int DA>
+hipError_t launch_nw(const LinArgs& a, int NW, bool out, hipStream_t st) {
+  const dim3 grid(a.total), block(64 * NW);
+  if (out && NW == 2) hipLaunchKernelGGL((k_linear<DA, 2>), grid, block, 0, st, a);
+  else if (out) hipLaunchKernelGGL((k_linear<DA, 4>), grid, block, 0, st, a);
+  else if (NW == 2) hipLaunchKernelGGL((k_linear_states<DA, 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_linear_states<DA, 4>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
-template <bool OUT>
-hipError_t launch_da(const LinArgs& a, int DA, int NW, hipStream_t st) {
+hipError_t launch_da(const LinArgs& a, int DA, int NW, bool out, hipStream_t st) {
   if (a.total == 0) return hipSuccess;
-  return DA == 64 ? launch_nw<64, OUT>(a, NW, st)
-         : DA == 128 ? launch_nw<128, OUT>(a, NW, st) : launch_nw<256, OUT>(a, NW, st);
+  return DA == 64 ? launch_nw<64>(a, NW, out, st)
+         : DA == 128 ? launch_nw<128>(a, NW, out, st) : launch_nw<256>(a, NW, out, st);
 }
 
 }  // namespace
 
 hipError_t launch_linear_walk(const LinArgs& a, int DA, int NW, hipStream_t st) {
-  return launch_da<true>(a, DA, NW, st);
+  return launch_da(a, DA, NW, true, st);
 }
 
 hipError_t launch_linear_states(const LinArgs& a, int DA, int NW, hipStream_t st) {
-  return launch_da<false>(a, DA, NW, st);
+  return launch_da(a, DA, NW, false, st);
 }
 
 hipError_t launch_linear_scan(const LinArgs& a, int DA, hipStream_t st) {
