@@ -9,7 +9,8 @@ per chunk a product with a power (2 U), at most 3 C additions of products of bf1
 value in three parts: 3 C U), the decayed value's own roundings (power, scale, product: 4 U), and one
 join of a segment's sum with the state before it (2 U):
   E' = a^n E + (3 n + 8) U A'.
-An output takes the state in two bf16 parts (each leaves at most 2^-8 of what it is given: 2^-16) in a
+Where only outputs follow from it the decayed value enters in two parts, which leave 2^-16 of it: F, as E
+and 2^-16 (A' - a^n A) a chunk.  An output takes the state in two bf16 parts (each leaves at most 2^-8 of what it is given: 2^-16) in a
 sum of 2 D products, the power and scale (3 U); and the chunk's own scores, sums of D products (D U),
 with the mask's factor (3 U), in two bf16 parts (2^-16) in a sum of 2 C products.  It is rounded to bf16
 at the end.
@@ -36,7 +37,7 @@ def layer(q, k, v, decay, x0, scale_p, scale_s, scale_w, forward):
     operands are in reversed order, x0 is what the first of them meets and the state is given as the
     next would meet it."""
     K, V = k.shape[1], v.shape[1]
-    S, A, E = np.array(x0, np.float64), np.abs(x0), np.zeros((K, V))
+    S, A, E, F = np.array(x0, np.float64), np.abs(x0), np.zeros((K, V)), np.zeros((K, V))
     out, bar = np.zeros((len(q), V)), np.zeros((len(q), V))
     for t0 in range(0, len(q), C):
         n = min(C, len(q) - t0)
@@ -46,13 +47,15 @@ def layer(q, k, v, decay, x0, scale_p, scale_s, scale_w, forward):
         near = np.where(i[:, None] >= i, np.power(decay, np.maximum(i[:, None] - i, 0)), 0.0) * scale_p
         past = np.power(decay, i + e0)[:, None] * scale_s
         out[t0:t0 + n] = past * (qq @ S) + (near * (qq @ kk.T)) @ vv
-        bar[t0:t0 + n] = (past * (np.abs(qq) @ (E + (2.0 ** -16 + (2 * K + 8) * U) * A)) +
+        bar[t0:t0 + n] = (past * (np.abs(qq) @ (F + (2.0 ** -16 + (2 * K + 8) * U) * A)) +
                           (2.0 ** -16 + (K + 2 * C + 8) * U) * ((near * (np.abs(qq) @ np.abs(kk).T)) @ np.abs(vv)))
         w = np.power(decay, n - 1 - i)[:, None] * scale_w
         f = decay ** (n - 1 + e0)
         S = f * S + kk.T @ (w * vv)
-        A = f * A + np.abs(kk).T @ (w * np.abs(vv))
+        new = np.abs(kk).T @ (w * np.abs(vv))
+        A = f * A + new
         E = f * E + (3 * n + 8) * U * A
+        F = f * F + (3 * n + 8) * U * A + 2.0 ** -16 * new
     if not forward and len(q):
         S, A, E = decay * S, decay * A, decay * E + U * decay * A
     return (out, bar + R * np.abs(out) + 1e-30), (S, E + U * np.abs(S) + 1e-30)

@@ -222,9 +222,7 @@ def test_linear_attention_slots():
     assert torch.equal(pool[others], sin[others])
     last = c.call(None, sout, slot)              # from zeros
     c.check(last, sout, None, entry)
-    nothing = c.call(sin, None, slot)
-    torch.cuda.synchronize()
-    assert torch.equal(nothing, out)
+    c.check(c.call(sin, None, slot), None, sin, entry)    # no state asked for
 
 
 @pytest.mark.parametrize("T,K,V", [(700, 128, 128), (2500, 64, 64)])

@@ -367,6 +367,7 @@ ttt_status ttt_linear_attention_backward(const ttt_linear_attention_config* cfg,
     a.role[0].scale_w = 1.f;
     a.role[1] = role(nullptr, 0, q, ld_q, dout, ld_dout, nullptr, 0);
     a.role[1].init = dstate_out;
+    a.role[1].fin = dstate_in;
     a.role[1].ws = wp;
     a.role[1].rev = 1;
     a.role[1].scale_w = c;

@@ -58,15 +58,19 @@ struct LinLoad {
   }
 };
 
-// Offsets of a lane's fragments in a tile.
-template <int P>
+// Offsets of a lane's fragments in a tile.  PERM: along the columns the second and third four of every
+// 16 elements change places.  An accumulator's element v is row 8 (v / 4) + 4 (lane / 32) + v % 4 of its
+// tile; rows taken in that order make a lane's eight of 16 neighbours, 8 (lane / 32) .. + 7, which is how
+// an operand along the rows is read in one piece.
+template <int P, bool PERM>
 struct LinAt {
-  int row;   // along the rows: elements 4 (lane / 32) .. + 3 of row lane % 32
+  int row;   // along the rows: elements 8 (lane / 32) .. + 7 of row lane % 32
   int col;   // along the columns: elements 16 (g & 1) + 4 (j & 3) .. + 3 of row 4 (g / 2) + j / 4
   __device__ __forceinline__ void init() {
     const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 4, j = lane & 15;
-    row = r * P + (lin_swz<P>(r) << 4) + 8 * (lane >> 5);
-    const int m = 16 * (g & 1) + 4 * (j & 3), rc = 4 * (g >> 1) + (j >> 2);
+    row = r * P + ((lin_swz<P>(r) ^ (lane >> 5)) << 4);
+    const int four = PERM ? ((j & 1) << 1) | ((j >> 1) & 1) : j & 3;
+    const int m = 16 * (g & 1) + 4 * four, rc = 4 * (g >> 1) + (j >> 2);
     col = rc * P + (((m >> 3) ^ lin_swz<P>(rc)) << 4) + (m & 7) * 2;
   }
 };
@@ -74,20 +78,15 @@ struct LinAt {
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Row base_row + lane % 32, elements base + 4 (lane / 32) + (0..3) and + 8: the order in which a lane
-// holds the rows of an accumulator.  base_row a multiple of 32, base of 16.
-template <int P>
-__device__ __forceinline__ bf16x8 lin_row(const char* tile, const LinAt<P>& at, int base_row, int base) {
-  s16x4 x[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    x[i] = *reinterpret_cast<const s16x4*>(tile + base_row * P + (at.row ^ (base * 2) ^ (i << 4)));
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+// Row base_row + lane % 32, elements base + 8 (lane / 32) .. + 7.  base_row a multiple of 32, base of 16.
+template <int P, bool PERM>
+__device__ __forceinline__ bf16x8 lin_row(const char* tile, const LinAt<P, PERM>& at, int base_row, int base) {
+  return *reinterpret_cast<const bf16x8*>(tile + base_row * P + (at.row ^ (base * 2)));
 }
-// Element base + lane % 32 of rows row + 4 (lane / 32) + (0..3) and + 8.  base a multiple of 32, row
-// of 16.
-template <int P>
-__device__ __forceinline__ bf16x8 lin_col(const char* tile, const LinAt<P>& at, int base, int row) {
+// Element base + lane % 32 (in the order of PERM) of rows row + 4 (lane / 32) + (0..3) and + 8.  base a
+// multiple of 32, row of 16.
+template <int P, bool PERM>
+__device__ __forceinline__ bf16x8 lin_col(const char* tile, const LinAt<P, PERM>& at, int base, int row) {
   s16x4 x[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -110,20 +109,18 @@ __device__ __forceinline__ uint32_t lin_pack(float a, float b) {
 __device__ __forceinline__ float lin_first(uint32_t u) { return __builtin_bit_cast(float, u << 16); }
 __device__ __forceinline__ float lin_second(uint32_t u) { return __builtin_bit_cast(float, u & 0xffff0000u); }
 
-// x as N bf16 numbers whose sum it is, to 8 N bits.
+// x as N bf16 numbers whose sum it is, to 8 N bits, and what is left of it.
 template <int N>
-__device__ __forceinline__ void lin_split(const float (&x)[8], bf16x8 (&p)[N]) {
+__device__ __forceinline__ void lin_split(float (&x)[8], bf16x8 (&p)[N]) {
   u32x4 u[N];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float a = x[2 * e], b = x[2 * e + 1];
+  for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      u[i][e] = lin_pack(a, b);
-      a -= lin_first(u[i][e]);
-      b -= lin_second(u[i][e]);
+      u[i][e] = lin_pack(x[2 * e], x[2 * e + 1]);
+      x[2 * e] -= lin_first(u[i][e]);
+      x[2 * e + 1] -= lin_second(u[i][e]);
     }
-  }
 #pragma unroll
   for (int i = 0; i < N; ++i) p[i] = __builtin_bit_cast(bf16x8, u[i]);
 }
@@ -184,14 +181,15 @@ struct LinTables {
   }
 };
 
-// The state of a wave: element v of tile rt is row 32 rt + 8 (v / 4) + 4 hl + v % 4, column li of its 32.
+// The state of a wave: element v of tile rt is row 32 rt + 16 (v / 8) + 8 hl + v % 8, column li of its 32.
 template <int RT>
 struct LinState {
   f32x16 s[RT];
-  // s <- f s + k^T (w v) over a chunk; vf: the wave's columns of v
+  // s <- f s + k^T (w v) over a chunk; vf: the wave's columns of v.  w v enters as two bf16 numbers, or
+  // as three.
   template <int PA>
-  __device__ __forceinline__ void add(const char* k, const LinAt<PA>& at, const bf16x8 (&vf)[LIN_C / 16], const float* wt,
-                                      float f, int hl) {
+  __device__ __forceinline__ void add(const char* k, const LinAt<PA, true>& at, const bf16x8 (&vf)[LIN_C / 16],
+                                      const float* wt, float f, int hl, bool three) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -209,13 +207,19 @@ struct LinState {
           w[4 * g + 2 * e + 1] = lin_second(u[2 * g + e]) * t[2 * e + 1];
         }
       }
-      bf16x8 wp[3];
+      bf16x8 wp[2], kf[RT];
       lin_split(w, wp);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const bf16x8 kf = lin_col<PA>(k, at, 32 * rt, 16 * x);
+      for (int rt = 0; rt < RT; ++rt) kf[rt] = lin_col(k, at, 32 * rt, 16 * x);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) s[rt] = lin_mma(kf, wp[i], s[rt]);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[rt] = lin_mma(kf[rt], wp[i], s[rt]);
+      if (three) {   // what is left of w, w now
+        bf16x8 rest[1];
+        lin_split(w, rest);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[rt] = lin_mma(kf[rt], rest[0], s[rt]);
       }
     }
   }
@@ -224,16 +228,16 @@ struct LinState {
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int v = 0; v < 16; ++v)
-        *as_global(p + (int64_t)(32 * rt + 8 * (v >> 2) + 4 * hl + (v & 3)) * ld) = s[rt][v] * f;
+        *as_global(p + (int64_t)(32 * rt + 16 * (v >> 3) + 8 * hl + (v & 7)) * ld) = s[rt][v] * f;
   }
 };
 
 // A workgroup walks one segment of one sequence, head and role, 64 tokens at a time; its NW waves hold 32
 // columns of the state each, all DA rows of it, as accumulators.  The output is computed transposed
 // (a lane is a token), so that the accumulators of the state and of the scores are the operands of the
-// products that follow as they lie, in the order of an accumulator's rows; q and k are read from LDS
-// in that order.  Every wave computes the chunk's scores itself (three tiles of 32 x 32: a fifth of its
-// products), which saves an exchange between the waves.
+// products that follow as they lie.  The scores' three tiles of 32 x 32 (two of the diagonal, one below) are a wave's
+// each, which leaves them, decayed and split, in LDS for the others: the barrier that they need is
+// there for v.
 //
 // Four areas of LDS take turns: while q, k and v of a chunk lie in three, the next chunk's q comes into
 // the fourth; once q has been read its k comes into q's, and once all has been read its v into k's: each
@@ -247,6 +251,7 @@ void k_linear(LinArgs a) {
   __shared__ __attribute__((aligned(1024))) char a1[AREA];
   __shared__ __attribute__((aligned(1024))) char a2[AREA];
   __shared__ __attribute__((aligned(1024))) char a3[AREA];
+  __shared__ __attribute__((aligned(1024))) bf16x8 scores[3][2][2][64];   // [tile][keys of 16][part][lane]
   __shared__ __attribute__((aligned(16))) LinTables tb;
   const LinPlace at(a, a.nseg, xcd_block(blockIdx.x, a.total), true);
   if (at.none) return;
@@ -281,6 +286,8 @@ void k_linear(LinArgs a) {
   const int colw = col0 + 32 * wave + li;
   const int64_t entry = lin_slot(a.slot, b, a.slots);
   LinState<RT> S;
+  float* fin = nullptr;
+  if (r.fin && entry >= 0 && t0 + a.L >= len) fin = r.fin + (entry * a.heads + h) * elems + colw;
   const float* init = nullptr;
   if (r.ws) init = r.ws + (((int64_t)b * a.heads + h) * a.nseg + at.seg) * elems;
   else if (r.init && entry >= 0) init = r.init + (entry * a.heads + h) * elems;
@@ -291,7 +298,7 @@ void k_linear(LinArgs a) {
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int i = 32 * rt + 8 * g + 4 * hl;
+        const int i = 32 * rt + 16 * (g >> 1) + 8 * hl + 4 * (g & 1);
         if (r.trans) {
           const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(init + (int64_t)colw * DA + i));
 #pragma unroll
@@ -302,8 +309,8 @@ void k_linear(LinArgs a) {
         }
       }
   }
-  LinAt<PA> ta;
-  LinAt<PV> tv;
+  LinAt<PA, true> ta;
+  LinAt<PV, false> tv;
   ta.init();
   tv.init();
   lin_wait<0>();
@@ -324,14 +331,33 @@ void k_linear(LinArgs a) {
     // backward in time the state before the first token (the gradient of the last state) is that
     // of the first token itself: one power less
     const int e0 = rev && t0 + c == 0 ? 0 : 1;
-    f32x16 p11 = f32x16{}, p21 = f32x16{}, p22 = f32x16{}, o1 = f32x16{}, o2 = f32x16{};
+    for (int tile = wave; tile < 3; tile += NW) {   // queries and keys: second and first half; both first; both second
+      const int qi = tile == 1 ? 0 : 32, ki = tile == 2 ? 32 : 0;
+      f32x16 p = f32x16{};
+#pragma unroll
+      for (int x = 0; x < 2 * RT; ++x) p = lin_mma(lin_row(ka, ta, ki, 16 * x), lin_row(qa, ta, qi, 16 * x), p);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float pv[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const f32x4 t = *reinterpret_cast<const f32x4*>(&tb.wt[0][32 + 16 * x + 8 * g + 4 * hl]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int v = 8 * x + 4 * g + e;
+            pv[4 * g + e] = p[v] * (tile ? dm[v] : f21 * t[e]);
+          }
+        }
+        bf16x8 pp[2];
+        lin_split(pv, pp);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) scores[tile][x][i][lane] = pp[i];
+      }
+    }
+    f32x16 o1 = f32x16{}, o2 = f32x16{};
 #pragma unroll
     for (int x = 0; x < 2 * RT; ++x) {
-      const bf16x8 q1 = lin_row<PA>(qa, ta, 0, 16 * x), q2 = lin_row<PA>(qa, ta, 32, 16 * x);
-      const bf16x8 k1 = lin_row<PA>(ka, ta, 0, 16 * x), k2 = lin_row<PA>(ka, ta, 32, 16 * x);
-      p11 = lin_mma(k1, q1, p11);
-      p21 = lin_mma(k1, q2, p21);
-      p22 = lin_mma(k2, q2, p22);
+      const bf16x8 q1 = lin_row(qa, ta, 0, 16 * x), q2 = lin_row(qa, ta, 32, 16 * x);
       float sv[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) sv[e] = S.s[x >> 1][8 * (x & 1) + e];
@@ -342,14 +368,13 @@ void k_linear(LinArgs a) {
         o1 = lin_mma(sp[i], q1, o1);
         o2 = lin_mma(sp[i], q2, o2);
       }
-      if (DA == 256) __builtin_amdgcn_sched_barrier(0);   // all fragments read ahead would not fit
     }
-    if (more) lin_wait<LinLoad<PA, NW>::N>();   // v is there, q is free
+    if (more) lin_wait<LinLoad<PA, NW>::N>();   // v and the scores are there, q is free
     else lin_wait<0>();
     if (more) lk.issue(qa, kb + row(c + 1) * r.ldk, size(c + 1), rev);
     bf16x8 vf[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) vf[x] = lin_col<PV>(va, tv, 32 * wave, 16 * x);
+    for (int x = 0; x < 4; ++x) vf[x] = lin_col(va, tv, 32 * wave, 16 * x);
     const float f1 = tb.pw[li + e0] * r.scale_s, f2 = tb.pw[32 + li + e0] * r.scale_s;
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
@@ -357,29 +382,13 @@ void k_linear(LinArgs a) {
       o2[v] *= f2;
     }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float pv[3][8];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const f32x4 t = *reinterpret_cast<const f32x4*>(&tb.wt[0][32 + 16 * x + 8 * g + 4 * hl]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int v = 8 * x + 4 * g + e;
-          pv[0][4 * g + e] = p11[v] * dm[v];
-          pv[1][4 * g + e] = p21[v] * (f21 * t[e]);
-          pv[2][4 * g + e] = p22[v] * dm[v];
-        }
-      }
-      bf16x8 pp[3][2];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) lin_split(pv[i], pp[i]);
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        o1 = lin_mma(vf[x], pp[0][i], o1);
-        o2 = lin_mma(vf[x], pp[1][i], o2);
-        o2 = lin_mma(vf[2 + x], pp[2][i], o2);
+        o1 = lin_mma(vf[x], scores[1][x][i][lane], o1);
+        o2 = lin_mma(vf[x], scores[0][x][i][lane], o2);
+        o2 = lin_mma(vf[2 + x], scores[2][x][i][lane], o2);
       }
-    }
     // the halves of the wave swapped in pairs: 8 neighbouring elements of a row in a lane
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -393,7 +402,7 @@ void k_linear(LinArgs a) {
           ow[i][2 * g + e] = w[0];
           ow[i][2 * g + 2 + e] = w[1];
         }
-    S.template add<PA>(ka, ta, vf, tb.wt[more ? 0 : 1], tb.pw[n - 1 + e0], hl);
+    S.template add<PA>(ka, ta, vf, tb.wt[more ? 0 : 1], tb.pw[n - 1 + e0], hl, fin != nullptr);
     lin_wait<0>();   // the next chunk's q and k are there, k and v are free
     if (more) lv.issue(ka, vb + row(c + 1) * r.ldv, size(c + 1), rev);
 #pragma unroll
@@ -408,18 +417,18 @@ void k_linear(LinArgs a) {
       }
   };
   int c = 0;
-  for (; c + 4 <= chunks; c += 4) {
-    step(a0, a1, a2, a3, c);
-    step(a3, a0, a1, a2, c + 1);
-    step(a2, a3, a0, a1, c + 2);
-    step(a1, a2, a3, a0, c + 3);
+  while (c < chunks) {
+    step(a0, a1, a2, a3, c++);
+    if (c == chunks) break;
+    step(a3, a0, a1, a2, c++);
+    if (c == chunks) break;
+    step(a2, a3, a0, a1, c++);
+    if (c == chunks) break;
+    step(a1, a2, a3, a0, c++);
   }
-  if (c < chunks) step(a0, a1, a2, a3, c);
-  if (c + 1 < chunks) step(a3, a0, a1, a2, c + 1);
-  if (c + 2 < chunks) step(a2, a3, a0, a1, c + 2);
 
-  if (r.fin && entry >= 0 && t0 + a.L >= len)   // behind the last step back lies the state before the first token
-    S.store(r.fin + (entry * a.heads + h) * elems + colw, a.DB, hl, rev && len > 0 ? lam : 1.f);
+  if (fin)   // behind the last step back lies the state before the first token
+    S.store(fin, a.DB, hl, rev && len > 0 ? lam : 1.f);
 }
 
 // Each segment's own sum, from zeros, of all but the last.
@@ -453,8 +462,8 @@ void k_linear_states(LinArgs a) {
   LinState<RT> S;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) S.s[rt] = f32x16{};
-  LinAt<PA> ta;
-  LinAt<PV> tv;
+  LinAt<PA, true> ta;
+  LinAt<PV, false> tv;
   ta.init();
   tv.init();
   lin_wait<0>();
@@ -462,8 +471,8 @@ void k_linear_states(LinArgs a) {
     if (c + 1 < at.chunks) issue(nxt, c + 1);
     bf16x8 vf[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) vf[x] = lin_col<PV>(cur + VO, tv, 32 * wave, 16 * x);
-    S.template add<PA>(cur, ta, vf, tb.wt[0], tb.pw[LIN_C], hl);
+    for (int x = 0; x < 4; ++x) vf[x] = lin_col(cur + VO, tv, 32 * wave, 16 * x);
+    S.template add<PA>(cur, ta, vf, tb.wt[0], tb.pw[LIN_C], hl, r.fin != nullptr);
     lin_wait<0>();
   };
   int c = 0;
