@@ -71,14 +71,15 @@ LinPlan linear_plan(int64_t wgs, int64_t seq_len, int64_t most) {
   return p;
 }
 
-int32_t linear_waves(int32_t DB) { return DB == 64 ? 2 : 4; }
+// waves of a workgroup, 16 columns each
+int32_t linear_waves(int32_t DB) { return DB == 64 ? 4 : 8; }
 
 int64_t state_bytes(const ttt_linear_attention_config* c, int64_t n) {
   return n * c->heads * c->dim_k * c->dim_v * (int64_t)sizeof(float);
 }
 
 LinPlan forward_plan(const ttt_linear_attention_config* c, int32_t batch, int64_t seq_len) {
-  return linear_plan((int64_t)batch * c->heads * (c->dim_v / (32 * linear_waves(c->dim_v))), seq_len, 2 * NUM_CU);
+  return linear_plan((int64_t)batch * c->heads * (c->dim_v / (16 * linear_waves(c->dim_v))), seq_len, 2 * NUM_CU);
 }
 LinPlan backward_plan(const ttt_linear_attention_config* c, int32_t batch, int64_t seq_len) {
   return linear_plan((int64_t)batch * c->heads * 3, seq_len, 3 * NUM_CU);
@@ -128,7 +129,7 @@ LinRole role(const void* q, int64_t ldq, const void* k, int64_t ldk, const void*
 int32_t linear_grid(LinArgs& a, int32_t DB, int32_t nseg) {
   const int32_t NW = linear_waves(DB);
   a.DB = DB;
-  a.slices = DB / (32 * NW);
+  a.slices = DB / (16 * NW);
   a.total = (int32_t)((int64_t)a.batch * a.heads * nseg * a.roles * a.slices);
   return NW;
 }

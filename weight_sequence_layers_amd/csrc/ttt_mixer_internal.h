@@ -66,7 +66,7 @@ __host__ __device__ inline int64_t lin_slot(const int32_t* slot, int32_t b, int3
   return i >= 0 && i < slots ? i : -1;
 }
 
-// dims: elements of a head of q and k (DA); NW: waves of a workgroup, 32 elements of v each.
+// dims: elements of a head of q and k (DA); NW: waves of a workgroup, 16 elements of v each.
 // states: only each segment's own sum, into ws, of all but the last; scan: ws from those to the
 // states before each segment.
 hipError_t launch_linear_walk(const LinArgs& a, int DA, int NW, hipStream_t st);

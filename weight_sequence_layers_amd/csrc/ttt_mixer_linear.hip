@@ -54,50 +54,47 @@ struct LinLoad {
     const int32_t top = rev ? (int32_t)last : 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      dma16(rs, (lds_void_t*)(tile + slice + i * NW * 1024), (uint32_t)(off[i % VAR] + (i / VAR) * step + top));
-  }
-};
-
-// Offsets of a lane's fragments in a tile.  PERM: along the columns the second and third four of every
-// 16 elements change places.  An accumulator's element v is row 8 (v / 4) + 4 (lane / 32) + v % 4 of its
-// tile; rows taken in that order make a lane's eight of 16 neighbours, 8 (lane / 32) .. + 7, which is how
-// an operand along the rows is read in one piece.
-template <int P, bool PERM>
-struct LinAt {
-  int row;   // along the rows: elements 8 (lane / 32) .. + 7 of row lane % 32
-  int col;   // along the columns: elements 16 (g & 1) + 4 (j & 3) .. + 3 of row 4 (g / 2) + j / 4
-  __device__ __forceinline__ void init() {
-    const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 4, j = lane & 15;
-    row = r * P + ((lin_swz<P>(r) ^ (lane >> 5)) << 4);
-    const int four = PERM ? ((j & 1) << 1) | ((j >> 1) & 1) : j & 3;
-    const int m = 16 * (g & 1) + 4 * four, rc = 4 * (g >> 1) + (j >> 2);
-    col = rc * P + (((m >> 3) ^ lin_swz<P>(rc)) << 4) + (m & 7) * 2;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(tile + slice + i * NW * 1024), 16,
+                                               (uint32_t)(off[i % VAR] + (i / VAR) * step + top), 0, 0, 0);
   }
 };
 
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// Row base_row + lane % 32, elements base + 8 (lane / 32) .. + 7.  base_row a multiple of 32, base of 16.
-template <int P, bool PERM>
-__device__ __forceinline__ bf16x8 lin_row(const char* tile, const LinAt<P, PERM>& at, int base_row, int base) {
-  return *reinterpret_cast<const bf16x8*>(tile + base_row * P + (at.row ^ (base * 2)));
+// The lanes in a 16 x 16 x 32 product, lane = 16 g + j: an operand's row (column) j, of the 32 summed
+// over the numbers 8 g .. 8 g + 7; the result's column j, rows 4 g .. 4 g + 3.  What is summed over may
+// come in any order that both operands have.  Two results over one another are an operand as they lie:
+// rows 4 g + e of the first and of the second are its 8 g + e and 8 g + 4 + e.
+//
+// Row j of 16, elements 8 g .. 8 g + 7 of 32 (at + 64 bytes times their number).
+template <int P>
+__device__ __forceinline__ int lin_row_at() {
+  const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+  return j * P + ((g ^ lin_swz<P>(j)) << 4);
 }
-// Element base + lane % 32 (in the order of PERM) of rows row + 4 (lane / 32) + (0..3) and + 8.  base a
-// multiple of 32, row of 16.
-template <int P, bool PERM>
-__device__ __forceinline__ bf16x8 lin_col(const char* tile, const LinAt<P, PERM>& at, int base, int row) {
+__device__ __forceinline__ bf16x8 lin_row(const char* tile, int at, int y) {
+  return *reinterpret_cast<const bf16x8*>(tile + (at ^ (y << 6)));
+}
+// Along the columns, 16 of them: rows 4 g + (0..3) and 16 + 4 g + (0..3).  Four columns that lie
+// together go to lanes that do; `chunk` and `byte` say where lane j & 3's four are.
+template <int P>
+__device__ __forceinline__ int lin_col_at(int chunk, int byte) {
+  const int lane = threadIdx.x & 63, r = 4 * (lane >> 4) + ((lane & 15) >> 2);
+  return r * P + ((chunk ^ lin_swz<P>(r)) << 4) + byte;
+}
+template <int P>
+__device__ __forceinline__ bf16x8 lin_col(const char* tile, int at) {
   s16x4 x[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const char* p = tile + (row + 8 * i) * P + (at.col ^ (base << 1) ^ (i << 5));
-    x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p));
-  }
+  for (int i = 0; i < 2; ++i)
+    x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(tile + 16 * i * P + at));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-__device__ __forceinline__ f32x16 lin_mma(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+__device__ __forceinline__ f32x4 lin_mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 // Two numbers rounded to bf16, and their values.
@@ -181,87 +178,102 @@ struct LinTables {
   }
 };
 
-// The state of a wave: element v of tile rt is row 32 rt + 16 (v / 8) + 8 hl + v % 8, column li of its 32.
-template <int RT>
+// The state of a wave, 16 columns: element e of tile 2 y + t is row 32 y + 8 g + 4 t + e, column j.
+template <int DA>
 struct LinState {
-  f32x16 s[RT];
-  // s <- f s + k^T (w v) over a chunk; vf: the wave's columns of v.  w v enters as two bf16 numbers, or
-  // as three.
-  template <int PA>
-  __device__ __forceinline__ void add(const char* k, const LinAt<PA, true>& at, const bf16x8 (&vf)[LIN_C / 16],
-                                      const float* wt, float f, int hl, bool three) {
+  static constexpr int P = DA * 2, N = DA / 16;
+  f32x4 s[N];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int i = 0; i < N; ++i) s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void decay(float f) {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) s[rt][v] *= f;
+    for (int i = 0; i < N; ++i) s[i] *= f;
+  }
+  // rows 32 y .. + 31 as an operand, in two bf16 parts
+  __device__ __forceinline__ void parts(int y, bf16x8 (&p)[2]) const {
+    float x[8];
 #pragma unroll
-    for (int x = 0; x < LIN_C / 16; ++x) {
-      float w[8];
+    for (int e = 0; e < 8; ++e) x[e] = s[2 * y + (e >> 2)][e & 3];
+    lin_split(x, p);
+  }
+  // 32 tokens of the wave's columns of v by their weights
+  static __device__ __forceinline__ void weigh(bf16x8 vf, const float* wt, int g, float (&w)[8]) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const f32x4 t = *reinterpret_cast<const f32x4*>(wt + 16 * x + 8 * g + 4 * hl);
-        const u32x4 u = __builtin_bit_cast(u32x4, vf[x]);
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 t = *reinterpret_cast<const f32x4*>(wt + 16 * i + 4 * g);
+      const u32x4 u = __builtin_bit_cast(u32x4, vf);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          w[4 * g + 2 * e] = lin_first(u[2 * g + e]) * t[2 * e];
-          w[4 * g + 2 * e + 1] = lin_second(u[2 * g + e]) * t[2 * e + 1];
-        }
-      }
-      bf16x8 wp[2], kf[RT];
-      lin_split(w, wp);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) kf[rt] = lin_col(k, at, 32 * rt, 16 * x);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt] = lin_mma(kf[rt], wp[i], s[rt]);
-      if (three) {   // what is left of w, w now
-        bf16x8 rest[1];
-        lin_split(w, rest);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt] = lin_mma(kf[rt], rest[0], s[rt]);
+      for (int e = 0; e < 2; ++e) {
+        w[4 * i + 2 * e] = lin_first(u[2 * i + e]) * t[2 * e];
+        w[4 * i + 2 * e + 1] = lin_second(u[2 * i + e]) * t[2 * e + 1];
       }
     }
   }
-  __device__ __forceinline__ void store(float* p, int ld, int hl, float f) const {
+  // s += k^T (w v) over a chunk; vf: the wave's columns of v.  w v enters as two bf16 numbers, or as
+  // three.  at: lane j & 3's columns of k are 8 (j & 3) .. + 3, of every 32.
+  __device__ __forceinline__ void add(const char* k, int at, const bf16x8 (&vf)[LIN_C / 32], const float* wt, int g,
+                                      bool three) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int z = 0; z < LIN_C / 32; ++z) {
+      float w[8];
+      weigh(vf[z], wt + 32 * z, g, w);
+      bf16x8 wp[2], rest[1];
+      lin_split(w, wp);
+      if (three) lin_split(w, rest);
 #pragma unroll
-      for (int v = 0; v < 16; ++v)
-        *as_global(p + (int64_t)(32 * rt + 16 * (v >> 3) + 8 * hl + (v & 7)) * ld) = s[rt][v] * f;
+      for (int i = 0; i < N; ++i) {
+        const bf16x8 kf = lin_col<P>(k + 32 * z * P, (at ^ ((i >> 1) << 6)) + 8 * (i & 1));
+        s[i] = lin_mma(kf, wp[0], s[i]);
+        s[i] = lin_mma(kf, wp[1], s[i]);
+        if (three) s[i] = lin_mma(kf, rest[0], s[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* p, int ld, int g, float f) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *as_global(p + (int64_t)(16 * (i & ~1) + 8 * g + 4 * (i & 1) + e) * ld) = s[i][e] * f;
   }
 };
 
-// A workgroup walks one segment of one sequence, head and role, 64 tokens at a time; its NW waves hold 32
+// A workgroup walks one segment of one sequence, head and role, 64 tokens at a time; its NW waves hold 16
 // columns of the state each, all DA rows of it, as accumulators.  The output is computed transposed
 // (a lane is a token), so that the accumulators of the state and of the scores are the operands of the
-// products that follow as they lie.  The scores' three tiles of 32 x 32 (two of the diagonal, one below) are a wave's
-// each, which leaves them, decayed and split, in LDS for the others: the barrier that they need is
-// there for v.
+// products that follow as they lie.  The scores' ten tiles of 16 x 16 are spread over the waves, which
+// leave them, decayed and split, in LDS for all: the barrier that they need is there for v.
+//
+// A wave's matrix and vector instructions do not run side by side, those of two waves do (4 products
+// and 24 multiplications: 120 ns of one wave, 70 a wave of two): many narrow waves, four to a SIMD, at
+// the price of reading q and k from LDS for each (columns of 32 a wave, two to a SIMD: 451 us for a
+// prompt of 131072 tokens of 8 heads of 128).
 //
 // Four areas of LDS take turns: while q, k and v of a chunk lie in three, the next chunk's q comes into
-// the fourth; once q has been read its k comes into q's, and once all has been read its v into k's: each
-// load has half a chunk's work or more to arrive.
+// the fourth; once q has been read its k comes into q's, and once all has been read its v into k's.
 template <int DA, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 1 : 2)))
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 2 : 4)))
 void k_linear(LinArgs a) {
-  constexpr int PA = DA * 2, PV = NW * 64;                    // bytes of a tile's row
-  constexpr int AREA = LIN_C * (PA > PV ? PA : PV), RT = DA / 32;
+  constexpr int PA = DA * 2, PV = NW * 32;                    // bytes of a tile's row
+  constexpr int AREA = LIN_C * (PA > PV ? PA : PV), Y = DA / 32;
   __shared__ __attribute__((aligned(1024))) char a0[AREA];
   __shared__ __attribute__((aligned(1024))) char a1[AREA];
   __shared__ __attribute__((aligned(1024))) char a2[AREA];
   __shared__ __attribute__((aligned(1024))) char a3[AREA];
-  __shared__ __attribute__((aligned(1024))) bf16x8 scores[3][2][2][64];   // [tile][keys of 16][part][lane]
+  // [queries of 16 with keys of 32: 0 0, 1 0, 2 0, 2 1, 3 0, 3 1][part][lane][keys of 16]
+  __shared__ __attribute__((aligned(1024))) u32x2 scores[6][2][64][2];
   __shared__ __attribute__((aligned(16))) LinTables tb;
   const LinPlace at(a, a.nseg, xcd_block(blockIdx.x, a.total), true);
   if (at.none) return;
   const LinRole& r = at.r;
   const int rev = r.rev, h = at.h, b = at.b, len = at.len, t0 = at.t0, cnt = at.cnt, chunks = at.chunks;
-  const int lane = threadIdx.x & 63, hl = lane >> 5, li = lane & 31;
+  const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const float lam = a.decay[h];
 
-  const int col0 = at.slice * 32 * NW;                       // the workgroup's first column
+  const int col0 = at.slice * 16 * NW;                       // the workgroup's first column
   const u16* qb = r.q + (int64_t)h * DA;
   const u16* kb = r.k + (int64_t)h * DA;
   const u16* vb = r.v + (int64_t)h * a.DB + col0;
@@ -275,146 +287,122 @@ void k_linear(LinArgs a) {
     const int t = t0 + c * LIN_C;
     return at.row0 + (rev ? len - t - size(c) : t);
   };
+  auto load_q = [&](char* p, int c) __attribute__((always_inline)) { lq.issue(p, qb + row(c) * r.ldq, size(c), rev); };
+  auto load_k = [&](char* p, int c) __attribute__((always_inline)) { lk.issue(p, kb + row(c) * r.ldk, size(c), rev); };
+  auto load_v = [&](char* p, int c) __attribute__((always_inline)) { lv.issue(p, vb + row(c) * r.ldv, size(c), rev); };
   if (chunks) {
-    lq.issue(a0, qb + row(0) * r.ldq, size(0), rev);
-    lk.issue(a1, kb + row(0) * r.ldk, size(0), rev);
-    lv.issue(a2, vb + row(0) * r.ldv, size(0), rev);
+    load_q(a0, 0);
+    load_k(a1, 0);
+    load_v(a2, 0);
   }
   tb.init(lam, at);
+  if (wave < 2) scores[0][wave][lane][1] = scores[3][wave][lane][1] = u32x2{0, 0};   // keys behind all of the queries
 
   const int64_t elems = (int64_t)DA * a.DB;
-  const int colw = col0 + 32 * wave + li;
+  const int colw = col0 + 16 * wave + j;
   const int64_t entry = lin_slot(a.slot, b, a.slots);
-  LinState<RT> S;
+  LinState<DA> S;
   float* fin = nullptr;
   if (r.fin && entry >= 0 && t0 + a.L >= len) fin = r.fin + (entry * a.heads + h) * elems + colw;
   const float* init = nullptr;
   if (r.ws) init = r.ws + (((int64_t)b * a.heads + h) * a.nseg + at.seg) * elems;
   else if (r.init && entry >= 0) init = r.init + (entry * a.heads + h) * elems;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) S.s[rt] = f32x16{};
+  S.clear();
   if (init) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int i = 0; i < DA / 16; ++i) {
+      const int x = 16 * (i & ~1) + 8 * g + 4 * (i & 1);
+      if (r.trans) {
+        S.s[i] = *as_global(reinterpret_cast<const f32x4*>(init + (int64_t)colw * DA + x));
+      } else {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int i = 32 * rt + 16 * (g >> 1) + 8 * hl + 4 * (g & 1);
-        if (r.trans) {
-          const f32x4 x = *as_global(reinterpret_cast<const f32x4*>(init + (int64_t)colw * DA + i));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S.s[rt][4 * g + e] = x[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S.s[rt][4 * g + e] = *as_global(init + (int64_t)(i + e) * a.DB + colw);
-        }
+        for (int e = 0; e < 4; ++e) S.s[i][e] = *as_global(init + (int64_t)(x + e) * a.DB + colw);
       }
+    }
   }
-  LinAt<PA, true> ta;
-  LinAt<PV, false> tv;
-  ta.init();
-  tv.init();
+  const int ra = lin_row_at<PA>();
+  const int ka_at = lin_col_at<PA>(j & 3, 0), va_at = lin_col_at<PV>(2 * wave + ((j & 3) >> 1), 8 * (j & 1));
   lin_wait<0>();
-  // element v of a tile of scores: key 8 (v / 4) + 4 hl + v % 4, query li
-  float dm[16];
-#pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    const int j = 8 * (v >> 2) + 4 * hl + (v & 3);
-    dm[v] = li >= j ? tb.pw[li >= j ? li - j : 0] * r.scale_p : 0.f;
-  }
-  const float f21 = tb.pw[li + 1] * (r.scale_p / r.scale_w);   // with wt's second half: a^(32 + li - j)
 
-  uint32_t ow[2][8];
+  u32x4 ow[2];   // the last chunk's output: 8 elements from 8 (g / 2) of token 16 (2 i + g % 2) + j
   auto step = [&](char* qa, char* ka, char* va, char* spare, int c) __attribute__((always_inline)) {
     const int n = size(c);
     const bool more = c + 1 < chunks;
-    if (more) lq.issue(spare, qb + row(c + 1) * r.ldq, size(c + 1), rev);
+    if (more) load_q(spare, c + 1);
     // backward in time the state before the first token (the gradient of the last state) is that
     // of the first token itself: one power less
     const int e0 = rev && t0 + c == 0 ? 0 : 1;
-    for (int tile = wave; tile < 3; tile += NW) {   // queries and keys: second and first half; both first; both second
-      const int qi = tile == 1 ? 0 : 32, ki = tile == 2 ? 32 : 0;
-      f32x16 p = f32x16{};
+    for (int tile = wave; tile < 10; tile += NW) {
+      const int qi = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, ki = tile - qi * (qi + 1) / 2;
+      f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int x = 0; x < 2 * RT; ++x) p = lin_mma(lin_row(ka, ta, ki, 16 * x), lin_row(qa, ta, qi, 16 * x), p);
+      for (int y = 0; y < Y; ++y)
+        p = lin_mma(lin_row(ka + 16 * ki * PA, ra, y), lin_row(qa + 16 * qi * PA, ra, y), p);
+      float pv[4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float pv[8];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const f32x4 t = *reinterpret_cast<const f32x4*>(&tb.wt[0][32 + 16 * x + 8 * g + 4 * hl]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int v = 8 * x + 4 * g + e;
-            pv[4 * g + e] = p[v] * (tile ? dm[v] : f21 * t[e]);
-          }
-        }
-        bf16x8 pp[2];
-        lin_split(pv, pp);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) scores[tile][x][i][lane] = pp[i];
+      for (int e = 0; e < 4; ++e) {   // query j of 16, key 4 g + e
+        const int d = 16 * (qi - ki) + j - 4 * g - e;
+        pv[e] = d >= 0 ? p[e] * (tb.pw[d >= 0 ? d : 0] * r.scale_p) : 0.f;
       }
+      u32x2 hi = u32x2{lin_pack(pv[0], pv[1]), lin_pack(pv[2], pv[3])};
+      const u32x2 lo = u32x2{lin_pack(pv[0] - lin_first(hi[0]), pv[1] - lin_second(hi[0])),
+                             lin_pack(pv[2] - lin_first(hi[1]), pv[3] - lin_second(hi[1]))};
+      const int at = qi < 2 ? qi : 2 * qi - 2 + (ki >> 1);
+      scores[at][0][lane][ki & 1] = hi;
+      scores[at][1][lane][ki & 1] = lo;
     }
-    f32x16 o1 = f32x16{}, o2 = f32x16{};
+    f32x4 o[4];
 #pragma unroll
-    for (int x = 0; x < 2 * RT; ++x) {
-      const bf16x8 q1 = lin_row(qa, ta, 0, 16 * x), q2 = lin_row(qa, ta, 32, 16 * x);
-      float sv[8];
+    for (int i = 0; i < 4; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sv[e] = S.s[x >> 1][8 * (x & 1) + e];
+    for (int y = 0; y < Y; ++y) {
       bf16x8 sp[2];
-      lin_split(sv, sp);
+      S.parts(y, sp);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        o1 = lin_mma(sp[i], q1, o1);
-        o2 = lin_mma(sp[i], q2, o2);
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8 qf = lin_row(qa + 16 * i * PA, ra, y);
+        o[i] = lin_mma(sp[0], qf, o[i]);
+        o[i] = lin_mma(sp[1], qf, o[i]);
       }
     }
     if (more) lin_wait<LinLoad<PA, NW>::N>();   // v and the scores are there, q is free
     else lin_wait<0>();
-    if (more) lk.issue(qa, kb + row(c + 1) * r.ldk, size(c + 1), rev);
-    bf16x8 vf[4];
+    if (more) load_k(qa, c + 1);
+    bf16x8 vf[2];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) vf[x] = lin_col(va, tv, 32 * wave, 16 * x);
-    const float f1 = tb.pw[li + e0] * r.scale_s, f2 = tb.pw[32 + li + e0] * r.scale_s;
+    for (int z = 0; z < 2; ++z) vf[z] = lin_col<PV>(va + 32 * z * PV, va_at);
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      o1[v] *= f1;
-      o2[v] *= f2;
-    }
+    for (int i = 0; i < 4; ++i) o[i] *= tb.pw[16 * i + j + e0] * r.scale_s;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        o1 = lin_mma(vf[x], scores[1][x][i][lane], o1);
-        o2 = lin_mma(vf[x], scores[0][x][i][lane], o2);
-        o2 = lin_mma(vf[2 + x], scores[2][x][i][lane], o2);
-      }
-    // the halves of the wave swapped in pairs: 8 neighbouring elements of a row in a lane
+      for (int z = 0; z <= i / 2; ++z)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          o[i] = lin_mma(vf[z], *reinterpret_cast<const bf16x8*>(scores[i < 2 ? i : 2 * i - 2 + z][x][lane]), o[i]);
+    S.decay(tb.pw[n - 1 + e0]);
+    S.add(ka, ka_at, vf, tb.wt[more ? 0 : 1], g, fin != nullptr);
+    // rows of 16 lanes swapped in pairs: 8 neighbouring elements of a token in a lane
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; g += 2)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const f32x16& o = i ? o2 : o1;
-          const auto w = __builtin_amdgcn_permlane32_swap(lin_pack(o[4 * g + 2 * e], o[4 * g + 2 * e + 1]),
-                                                          lin_pack(o[4 * g + 4 + 2 * e], o[4 * g + 5 + 2 * e]), false, false);
-          ow[i][2 * g + e] = w[0];
-          ow[i][2 * g + 2 + e] = w[1];
-        }
-    S.template add<PA>(ka, ta, vf, tb.wt[more ? 0 : 1], tb.pw[n - 1 + e0], hl, fin != nullptr);
+      for (int e = 0; e < 2; ++e) {
+        const auto w = __builtin_amdgcn_permlane16_swap(lin_pack(o[2 * i][2 * e], o[2 * i][2 * e + 1]),
+                                                        lin_pack(o[2 * i + 1][2 * e], o[2 * i + 1][2 * e + 1]), false, false);
+        ow[i][e] = w[0];
+        ow[i][2 + e] = w[1];
+      }
     lin_wait<0>();   // the next chunk's q and k are there, k and v are free
-    if (more) lv.issue(ka, vb + row(c + 1) * r.ldv, size(c + 1), rev);
+    if (more) load_v(ka, c + 1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (32 * i + li < n) {
-        const int t = t0 + c * LIN_C + 32 * i + li;
-        u16* y = r.out + (at.row0 + (rev ? len - 1 - t : t)) * r.ldo + (int64_t)h * a.DB + col0 + 32 * wave + 8 * hl;
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          *as_global(reinterpret_cast<u32x4*>(y + 16 * g)) =
-              u32x4{ow[i][4 * g], ow[i][4 * g + 1], ow[i][4 * g + 2], ow[i][4 * g + 3]};
+    for (int i = 0; i < 2; ++i) {
+      const int x = 16 * (2 * i + (g & 1)) + j;
+      if (x < n) {
+        const int t = t0 + c * LIN_C + x;
+        u16* y = r.out + (at.row0 + (rev ? len - 1 - t : t)) * r.ldo + (int64_t)h * a.DB + col0 + 16 * wave + 8 * (g >> 1);
+        *as_global(reinterpret_cast<u32x4*>(y)) = ow[i];
       }
+    }
   };
   int c = 0;
   while (c < chunks) {
@@ -426,63 +414,58 @@ void k_linear(LinArgs a) {
     if (c == chunks) break;
     step(a1, a2, a3, a0, c++);
   }
-
   if (fin)   // behind the last step back lies the state before the first token
-    S.store(fin, a.DB, hl, rev && len > 0 ? lam : 1.f);
+    S.store(fin, a.DB, g, rev && len > 0 ? lam : 1.f);
 }
 
 // Each segment's own sum, from zeros, of all but the last.
 template <int DA, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 1 : 2)))
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 2 : 4)))
 void k_linear_states(LinArgs a) {
-  constexpr int PA = DA * 2, PV = NW * 64, VO = LIN_C * PA, RT = DA / 32;
+  constexpr int PA = DA * 2, PV = NW * 32, VO = LIN_C * PA;
   __shared__ __attribute__((aligned(1024))) char st0[LIN_C * (PA + PV)];
   __shared__ __attribute__((aligned(1024))) char st1[LIN_C * (PA + PV)];
   __shared__ __attribute__((aligned(16))) LinTables tb;
   const LinPlace at(a, a.nseg - 1, xcd_block(blockIdx.x, a.total), false);
   if (at.none) return;
   const LinRole& r = at.r;
-  const int rev = r.rev, lane = threadIdx.x & 63, hl = lane >> 5;
+  const int rev = r.rev, lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int col0 = at.slice * 32 * NW;
+  const int col0 = at.slice * 16 * NW;
   const u16* kb = r.k + (int64_t)at.h * DA;
   const u16* vb = r.v + (int64_t)at.h * a.DB + col0;
   LinLoad<PA, NW> lk;
   LinLoad<PV, NW> lv;
   lk.init(r.ldk, rev);
   lv.init(r.ldv, rev);
-  auto issue = [&](char* st, int c) __attribute__((always_inline)) {   // every chunk is whole
+  auto load = [&](char* st, int c) __attribute__((always_inline)) {   // every chunk is whole
     const int t = at.t0 + c * LIN_C;
     const int64_t row = at.row0 + (rev ? at.len - t - LIN_C : t);
     lk.issue(st, kb + row * r.ldk, LIN_C, rev);
     lv.issue(st + VO, vb + row * r.ldv, LIN_C, rev);
   };
-  issue(st0, 0);
+  load(st0, 0);
   tb.init(a.decay[at.h], at);
-  LinState<RT> S;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) S.s[rt] = f32x16{};
-  LinAt<PA, true> ta;
-  LinAt<PV, false> tv;
-  ta.init();
-  tv.init();
-  lin_wait<0>();
-  auto step = [&](const char* cur, char* nxt, int c) __attribute__((always_inline)) {
-    if (c + 1 < at.chunks) issue(nxt, c + 1);
-    bf16x8 vf[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) vf[x] = lin_col(cur + VO, tv, 32 * wave, 16 * x);
-    S.template add<PA>(cur, ta, vf, tb.wt[0], tb.pw[LIN_C], hl, r.fin != nullptr);
-    lin_wait<0>();
-  };
+  LinState<DA> S;
+  S.clear();
+  const int ka_at = lin_col_at<PA>(j & 3, 0), va_at = lin_col_at<PV>(2 * wave + ((j & 3) >> 1), 8 * (j & 1));
   int c = 0;
-  for (; c + 1 < at.chunks; c += 2) {
-    step(st0, st1, c);
-    step(st1, st0, c + 1);
+  auto step = [&](const char* cur, char* free) __attribute__((always_inline)) {
+    lin_wait<0>();
+    if (c + 1 < at.chunks) load(free, c + 1);
+    bf16x8 vf[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) vf[z] = lin_col<PV>(cur + VO + 32 * z * PV, va_at);
+    S.decay(tb.pw[LIN_C]);
+    S.add(cur, ka_at, vf, tb.wt[0], g, r.fin != nullptr);
+    ++c;
+  };
+  while (c < at.chunks) {
+    step(st0, st1);
+    if (c == at.chunks) break;
+    step(st1, st0);
   }
-  if (c < at.chunks) step(st0, st1, c);
-  S.store(r.ws + (((int64_t)at.b * a.heads + at.h) * a.nseg + at.seg) * DA * a.DB + col0 + 32 * wave + (lane & 31), a.DB,
-          hl, 1.f);
+  S.store(r.ws + (((int64_t)at.b * a.heads + at.h) * a.nseg + at.seg) * DA * a.DB + col0 + 16 * wave + j, a.DB, g, 1.f);
 }
 
 // From the segments' own sums to the states before each: a thread takes four elements of a state
@@ -523,10 +506,10 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinArgs a, int DA) {
 template <int DA>
 hipError_t launch_nw(const LinArgs& a, int NW, bool out, hipStream_t st) {
   const dim3 grid(a.total), block(64 * NW);
-  if (out && NW == 2) hipLaunchKernelGGL((k_linear<DA, 2>), grid, block, 0, st, a);
-  else if (out) hipLaunchKernelGGL((k_linear<DA, 4>), grid, block, 0, st, a);
-  else if (NW == 2) hipLaunchKernelGGL((k_linear_states<DA, 2>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_linear_states<DA, 4>), grid, block, 0, st, a);
+  if (out && NW == 4) hipLaunchKernelGGL((k_linear<DA, 4>), grid, block, 0, st, a);
+  else if (out) hipLaunchKernelGGL((k_linear<DA, 8>), grid, block, 0, st, a);
+  else if (NW == 4) hipLaunchKernelGGL((k_linear_states<DA, 4>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_linear_states<DA, 8>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
