@@ -43,6 +43,7 @@ struct LinArgs {
   int32_t DB;                               // elements of a head of v
   int32_t nseg, L;                          // segments of a sequence at most, tokens of one
   int32_t slices, total;
+  int32_t nt;                               // 1: rows are read past the last-level cache
 };
 
 // A sequence's first row and its length.

@@ -47,15 +47,21 @@ struct LinLoad {
   }
   // The n rows at p, in their order or (rev) from the last to the first; the others read as 0:
   // their offsets lie behind the n rows, or wrap to 2^31 and more.
-  __device__ __forceinline__ void issue(char* tile, const u16* p, int n, int rev) const {
+  __device__ __forceinline__ void issue(char* tile, const u16* p, int n, int rev, int nt) const {
     const uint32_t last = (uint32_t)(n - 1) * ld2;
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)(last + P), 0x00020000);
     const int32_t top = rev ? (int32_t)last : 0;
+    if (nt) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(tile + slice + i * NW * 1024), 16,
-                                               (uint32_t)(off[i % VAR] + (i / VAR) * step + top), 0, 0, 0);
+      for (int i = 0; i < N; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(tile + slice + i * NW * 1024), 16,
+                                                 (uint32_t)(off[i % VAR] + (i / VAR) * step + top), 0, 0, 2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        dma16(rs, (lds_void_t*)(tile + slice + i * NW * 1024), (uint32_t)(off[i % VAR] + (i / VAR) * step + top));
+    }
   }
 };
 
@@ -287,9 +293,9 @@ void k_linear(LinArgs a) {
     const int t = t0 + c * LIN_C;
     return at.row0 + (rev ? len - t - size(c) : t);
   };
-  auto load_q = [&](char* p, int c) __attribute__((always_inline)) { lq.issue(p, qb + row(c) * r.ldq, size(c), rev); };
-  auto load_k = [&](char* p, int c) __attribute__((always_inline)) { lk.issue(p, kb + row(c) * r.ldk, size(c), rev); };
-  auto load_v = [&](char* p, int c) __attribute__((always_inline)) { lv.issue(p, vb + row(c) * r.ldv, size(c), rev); };
+  auto load_q = [&](char* p, int c) __attribute__((always_inline)) { lq.issue(p, qb + row(c) * r.ldq, size(c), rev, a.nt); };
+  auto load_k = [&](char* p, int c) __attribute__((always_inline)) { lk.issue(p, kb + row(c) * r.ldk, size(c), rev, a.nt); };
+  auto load_v = [&](char* p, int c) __attribute__((always_inline)) { lv.issue(p, vb + row(c) * r.ldv, size(c), rev, a.nt); };
   if (chunks) {
     load_q(a0, 0);
     load_k(a1, 0);
@@ -441,8 +447,8 @@ void k_linear_states(LinArgs a) {
   auto load = [&](char* st, int c) __attribute__((always_inline)) {   // every chunk is whole
     const int t = at.t0 + c * LIN_C;
     const int64_t row = at.row0 + (rev ? at.len - t - LIN_C : t);
-    lk.issue(st, kb + row * r.ldk, LIN_C, rev);
-    lv.issue(st + VO, vb + row * r.ldv, LIN_C, rev);
+    lk.issue(st, kb + row * r.ldk, LIN_C, rev, a.nt);
+    lv.issue(st + VO, vb + row * r.ldv, LIN_C, rev, a.nt);
   };
   load(st0, 0);
   tb.init(a.decay[at.h], at);
