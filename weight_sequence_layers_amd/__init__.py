@@ -781,15 +781,12 @@ def ttt_window_attention_backward(q, k, v, ld: int, out, ld_out: int, lse, dout,
 def make_linear_attention_config(*, heads: int, dim_k: int, dim_v: Optional[int] = None,
                                  scale: float = 0.0) -> ttt_linear_attention_config:
     """ttt_linear_attention_config; dim_v None: dim_k; scale 0: 1 / sqrt(dim_k)."""
-    dim_v = dim_k if dim_v is None else dim_v
-    _int32(int(heads) | int(dim_k) | int(dim_v))
-    _scale(scale)
-    return ttt_linear_attention_config(int(heads), int(dim_k), int(dim_v), float(scale))
-
-
-def _scale(scale: float) -> None:
+    heads, dim_k, scale = int(heads), int(dim_k), float(scale)
+    dim_v = dim_k if dim_v is None else int(dim_v)
+    _int32(heads | dim_k | dim_v)
     if scale and -2.0 ** -150 <= scale <= 2.0 ** -150:
         raise TTTError(4, f"scale {scale} is 0 in 32 bits, which selects another")
+    return ttt_linear_attention_config(heads, dim_k, dim_v, scale)
 
 
 def ttt_validate_linear_attention_config(cfg: ttt_linear_attention_config) -> None:
@@ -800,19 +797,25 @@ def _pool(t, name: str, cfg, dev: int, torch):
     """Pointer and number of entries of a pool of states [slots, heads, dim_k, dim_v] (None: none)."""
     if t is None:
         return None, 0
-    shape = t.shape
-    if len(shape) != 4 or tuple(shape[1:]) != (cfg.heads, cfg.dim_k, cfg.dim_v):
-        raise TTTError(2, f"{name} is {list(shape)}, [slots, {cfg.heads}, {cfg.dim_k}, {cfg.dim_v}] is read")
-    _int32(shape[0])
-    return _arg(t, name, torch.float32, 0, dev), shape[0]
+    if t.dim() == 4:
+        n, h, k, v = t.shape
+        if h == cfg.heads and k == cfg.dim_k and v == cfg.dim_v:
+            _int32(n)
+            if t.dtype is torch.float32 and t.get_device() == dev and t.is_contiguous():
+                return t.data_ptr(), n
+            return _arg(t, name, torch.float32, 0, dev), n
+    raise TTTError(2, f"{name} is {list(t.shape)}, [slots, {cfg.heads}, {cfg.dim_k}, {cfg.dim_v}] is read")
 
 
 def _pools(state_in, state_out, cfg, dev: int, torch):
     """Pointers of the two pools and their number of entries."""
-    (pi, ni), (po, no) = _pool(state_in, "state_in", cfg, dev, torch), _pool(state_out, "state_out", cfg, dev, torch)
+    pi, ni = _pool(state_in, "state_in", cfg, dev, torch)
+    if state_out is state_in:
+        return pi, pi, ni
+    po, no = _pool(state_out, "state_out", cfg, dev, torch)
     if state_in is not None and state_out is not None and ni != no:
         raise TTTError(2, f"state_in of {ni} entries, state_out of {no}")
-    return pi, po, max(ni, no)
+    return pi, po, ni or no
 
 
 def ttt_linear_attention_work(cfg: ttt_linear_attention_config, batch: int, seq_len: int) -> int:
