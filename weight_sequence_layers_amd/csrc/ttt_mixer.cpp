@@ -64,13 +64,13 @@ ttt_status check_rows(const int32_t* starts, int64_t tokens, int32_t batch, int6
 //   - half as many again for sequences of unequal lengths, whose segments go by the longest: 24 prompts
 //     up to 4096 tokens of 12 heads of 64 take 187 us in 2 segments, 151 in 3, 141 in 4, 150 in 6;
 //   - down to one chunk each (3 x 777 tokens of 2 heads, a training step: 104 us whole, 58 in segments of
-//     129, 51 in segments of 65), but none for sequences of LIN_WHOLE tokens or fewer, for which
-//     launches cost more (3 prompts up to 130 tokens: 17 us whole, 25 in two).
+//     129, 51 in segments of 65), but none for sequences of LIN_WHOLE tokens or fewer, for which the
+//     launches cost more (a prompt of 8 heads: 192 tokens 17 us whole, 21 cut; 256 21 and 21; 384 28 and 22).
 struct LinPlan {
   int32_t nseg, L;
 };
 
-constexpr int64_t NUM_CU = 256, LIN_WHOLE = 512;
+constexpr int64_t NUM_CU = 256, LIN_WHOLE = 256;
 
 LinPlan linear_plan(int64_t wgs, int64_t seq_len, int64_t slots) {
   const int64_t n = wgs && seq_len > LIN_WHOLE ? std::max<int64_t>(1, std::min(slots / wgs, seq_len / LIN_C)) : 1;

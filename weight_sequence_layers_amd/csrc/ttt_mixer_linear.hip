@@ -24,30 +24,49 @@ __device__ __forceinline__ int lin_swz(int r) {
   return P == 128 ? (((r >> 1) & 1) << 2) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
 }
 
-// Loads of a tile of LIN_C rows of P bytes, straight into LDS, by NW waves.
+// A value of every lane, held in scalar registers: the launch's arguments are read once, not at every use.
+template <typename T>
+__device__ __forceinline__ T lin_scalar(T x) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 8, "one or two registers");
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)u), hi = __builtin_amdgcn_readfirstlane((int)(u >> 32));
+    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+  }
+}
+
+// Loads of the chunks of one operand in turn, tiles of LIN_C rows of P bytes, straight into LDS, by NW
+// waves.
 template <int P, int NW>
 struct LinLoad {
   static constexpr int ROWS = 1024 / P;                     // rows of one wave's load
   static constexpr int N = LIN_C / ROWS / NW;               // loads of a wave
   static constexpr int VAR = NW * ROWS < 16 ? 16 / (NW * ROWS) : 1;   // the swizzle repeats after 16 rows
+  const char* p;         // the next chunk's lowest token
   int32_t off[VAR], step;
   uint32_t ld2;
-  int slice;
-  __device__ __forceinline__ void init(int64_t ld, int rev) {
+  int slice, rev, nt;
+  // base: the head's columns of row 0; row: the lowest token of the first chunk
+  __device__ __forceinline__ void init(const u16* base, int64_t ld, int64_t row, int rev_, int nt_) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    ld2 = (uint32_t)(ld * 2);
+    p = lin_scalar(reinterpret_cast<const char*>(base + row * ld));
+    ld2 = lin_scalar((uint32_t)(ld * 2));
+    rev = rev_;
+    nt = nt_;
     slice = wave * 1024;
-    const int32_t row = rev ? -(int32_t)ld2 : (int32_t)ld2;
-    step = NW * ROWS * VAR * row;
+    const int32_t line = rev ? -(int32_t)ld2 : (int32_t)ld2;
+    step = NW * ROWS * VAR * line;
 #pragma unroll
     for (int i = 0; i < VAR; ++i) {
       const int r = (wave + i * NW) * ROWS + lane / (P / 16);
-      off[i] = r * row + ((lane % (P / 16)) ^ lin_swz<P>(r)) * 16;
+      off[i] = r * line + ((lane % (P / 16)) ^ lin_swz<P>(r)) * 16;
     }
   }
-  // The n rows at p, in their order or (rev) from the last to the first; the others read as 0:
-  // their offsets lie behind the n rows, or wrap to 2^31 and more.
-  __device__ __forceinline__ void issue(char* tile, const u16* p, int n, int rev, int nt) const {
+  // The chunk's n rows, in their order or (rev) from the last to the first; the others read as 0: their
+  // offsets lie behind the n rows, or wrap to 2^31 and more.  next: rows of the chunk behind it.
+  __device__ __forceinline__ void issue(char* tile, int n, int next) {
     const uint32_t last = (uint32_t)(n - 1) * ld2;
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)(last + P), 0x00020000);
@@ -62,6 +81,7 @@ struct LinLoad {
       for (int i = 0; i < N; ++i)
         dma16(rs, (lds_void_t*)(tile + slice + i * NW * 1024), (uint32_t)(off[i % VAR] + (i / VAR) * step + top));
     }
+    p += rev ? -(int64_t)next * ld2 : (int64_t)LIN_C * ld2;
   }
 };
 
@@ -228,12 +248,19 @@ struct LinState {
       bf16x8 wp[2], rest[1];
       lin_split(w, wp);
       if (three) lin_split(w, rest);
+      // four tiles in turn: a product that goes on with the last one's result waits for it
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const bf16x8 kf = lin_col<P>(k + 32 * z * P, (at ^ ((i >> 1) << 6)) + 8 * (i & 1));
-        s[i] = lin_mma(kf, wp[0], s[i]);
-        s[i] = lin_mma(kf, wp[1], s[i]);
-        if (three) s[i] = lin_mma(kf, rest[0], s[i]);
+      for (int i = 0; i < N; i += 4) {
+        bf16x8 kf[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) kf[t] = lin_col<P>(k + 32 * z * P, (at ^ (((i + t) >> 1) << 6)) + 8 * (t & 1));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[i + t] = lin_mma(kf[t], wp[0], s[i + t]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s[i + t] = lin_mma(kf[t], wp[1], s[i + t]);
+        if (three)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) s[i + t] = lin_mma(kf[t], rest[0], s[i + t]);
       }
     }
   }
@@ -258,7 +285,9 @@ struct LinState {
 // prompt of 131072 tokens of 8 heads of 128).
 //
 // Four areas of LDS take turns: while q, k and v of a chunk lie in three, the next chunk's q comes into
-// the fourth; once q has been read its k comes into q's, and once all has been read its v into k's.
+// the fourth; once q has been read its k comes into q's, and once all has been read its v into k's.  Three
+// stages of whole chunks, two of them under way, gain nothing even where a workgroup has a CU to itself
+// (one prompt of 512 tokens of 8 heads: 34.7 us, 36.0 so): a chunk's chain of products is what takes the time.
 template <int DA, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(DA == 256 ? 2 : 4)))
 void k_linear(LinArgs a) {
@@ -274,28 +303,27 @@ void k_linear(LinArgs a) {
   const LinPlace at(a, a.nseg, xcd_block(blockIdx.x, a.total), true);
   if (at.none) return;
   const LinRole& r = at.r;
-  const int rev = r.rev, h = at.h, b = at.b, len = at.len, t0 = at.t0, cnt = at.cnt, chunks = at.chunks;
+  const int rev = lin_scalar(r.rev), h = at.h, b = at.b;
+  const int len = lin_scalar(at.len), t0 = at.t0, cnt = lin_scalar(at.cnt), chunks = lin_scalar(at.chunks);
+  const float scale_p = lin_scalar(r.scale_p), scale_s = lin_scalar(r.scale_s);
   const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const float lam = a.decay[h];
 
   const int col0 = at.slice * 16 * NW;                       // the workgroup's first column
-  const u16* qb = r.q + (int64_t)h * DA;
-  const u16* kb = r.k + (int64_t)h * DA;
-  const u16* vb = r.v + (int64_t)h * a.DB + col0;
+  auto size = [&](int c) __attribute__((always_inline)) { return max(0, min(LIN_C, cnt - c * LIN_C)); };
   LinLoad<PA, NW> lq, lk;
   LinLoad<PV, NW> lv;
-  lq.init(r.ldq, rev);
-  lk.init(r.ldk, rev);
-  lv.init(r.ldv, rev);
-  auto size = [&](int c) __attribute__((always_inline)) { return min(LIN_C, cnt - c * LIN_C); };
-  auto row = [&](int c) __attribute__((always_inline)) {     // of chunk c's lowest token
-    const int t = t0 + c * LIN_C;
-    return at.row0 + (rev ? len - t - size(c) : t);
-  };
-  auto load_q = [&](char* p, int c) __attribute__((always_inline)) { lq.issue(p, qb + row(c) * r.ldq, size(c), rev, a.nt); };
-  auto load_k = [&](char* p, int c) __attribute__((always_inline)) { lk.issue(p, kb + row(c) * r.ldk, size(c), rev, a.nt); };
-  auto load_v = [&](char* p, int c) __attribute__((always_inline)) { lv.issue(p, vb + row(c) * r.ldv, size(c), rev, a.nt); };
+  {
+    const int64_t first = at.row0 + (rev ? len - t0 - size(0) : t0);
+    const int nt = lin_scalar(a.nt);
+    lq.init(r.q + (int64_t)h * DA, r.ldq, first, rev, nt);
+    lk.init(r.k + (int64_t)h * DA, r.ldk, first, rev, nt);
+    lv.init(r.v + (int64_t)h * a.DB + col0, r.ldv, first, rev, nt);
+  }
+  auto load_q = [&](char* p, int c) __attribute__((always_inline)) { lq.issue(p, size(c), size(c + 1)); };
+  auto load_k = [&](char* p, int c) __attribute__((always_inline)) { lk.issue(p, size(c), size(c + 1)); };
+  auto load_v = [&](char* p, int c) __attribute__((always_inline)) { lv.issue(p, size(c), size(c + 1)); };
   if (chunks) {
     load_q(a0, 0);
     load_k(a1, 0);
@@ -330,7 +358,17 @@ void k_linear(LinArgs a) {
   const int ka_at = lin_col_at<PA>(j & 3, 0), va_at = lin_col_at<PV>(2 * wave + ((j & 3) >> 1), 8 * (j & 1));
   lin_wait<0>();
 
-  u32x4 ow[2];   // the last chunk's output: 8 elements from 8 (g / 2) of token 16 (2 i + g % 2) + j
+  u32x4 ow[2];   // a chunk's output: 8 elements from 8 (g / 2) of token 16 (2 i + g % 2) + j
+  // the workgroup's columns of the next chunk's first token, and the lane's place from there
+  char* op = lin_scalar(reinterpret_cast<char*>(r.out + (at.row0 + (rev ? len - 1 - t0 : t0)) * r.ldo + (int64_t)h * a.DB + col0));
+  const int32_t ldo2 = lin_scalar((int32_t)(rev ? -r.ldo : r.ldo) * 2);
+  const int32_t ox = 16 * (g & 1) + j, oc = 32 * wave + 16 * (g >> 1);
+  auto store = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (32 * i + ox < size(c)) *as_global(reinterpret_cast<u32x4*>(op + (int64_t)((32 * i + ox) * ldo2 + oc))) = ow[i];
+    op += (int64_t)LIN_C * ldo2;
+  };
   auto step = [&](char* qa, char* ka, char* va, char* spare, int c) __attribute__((always_inline)) {
     const int n = size(c);
     const bool more = c + 1 < chunks;
@@ -348,7 +386,7 @@ void k_linear(LinArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {   // query j of 16, key 4 g + e
         const int d = 16 * (qi - ki) + j - 4 * g - e;
-        pv[e] = d >= 0 ? p[e] * (tb.pw[d >= 0 ? d : 0] * r.scale_p) : 0.f;
+        pv[e] = d >= 0 ? p[e] * (tb.pw[d >= 0 ? d : 0] * scale_p) : 0.f;
       }
       u32x2 hi = u32x2{lin_pack(pv[0], pv[1]), lin_pack(pv[2], pv[3])};
       const u32x2 lo = u32x2{lin_pack(pv[0] - lin_first(hi[0]), pv[1] - lin_second(hi[0])),
@@ -364,12 +402,13 @@ void k_linear(LinArgs a) {
     for (int y = 0; y < Y; ++y) {
       bf16x8 sp[2];
       S.parts(y, sp);
+      bf16x8 qf[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8 qf = lin_row(qa + 16 * i * PA, ra, y);
-        o[i] = lin_mma(sp[0], qf, o[i]);
-        o[i] = lin_mma(sp[1], qf, o[i]);
-      }
+      for (int i = 0; i < 4; ++i) qf[i] = lin_row(qa + 16 * i * PA, ra, y);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = lin_mma(sp[x], qf[i], o[i]);
     }
     if (more) lin_wait<LinLoad<PA, NW>::N>();   // v and the scores are there, q is free
     else lin_wait<0>();
@@ -378,13 +417,13 @@ void k_linear(LinArgs a) {
 #pragma unroll
     for (int z = 0; z < 2; ++z) vf[z] = lin_col<PV>(va + 32 * z * PV, va_at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= tb.pw[16 * i + j + e0] * r.scale_s;
+    for (int i = 0; i < 4; ++i) o[i] *= tb.pw[16 * i + j + e0] * scale_s;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int z = 0; z < 2; ++z)
 #pragma unroll
-      for (int z = 0; z <= i / 2; ++z)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int i = 2 * z; i < 4; ++i)
           o[i] = lin_mma(vf[z], *reinterpret_cast<const bf16x8*>(scores[i < 2 ? i : 2 * i - 2 + z][x][lane]), o[i]);
     S.decay(tb.pw[n - 1 + e0]);
     S.add(ka, ka_at, vf, tb.wt[more ? 0 : 1], g, fin != nullptr);
@@ -400,15 +439,7 @@ void k_linear(LinArgs a) {
       }
     lin_wait<0>();   // the next chunk's q and k are there, k and v are free
     if (more) load_v(ka, c + 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int x = 16 * (2 * i + (g & 1)) + j;
-      if (x < n) {
-        const int t = t0 + c * LIN_C + x;
-        u16* y = r.out + (at.row0 + (rev ? len - 1 - t : t)) * r.ldo + (int64_t)h * a.DB + col0 + 16 * wave + 8 * (g >> 1);
-        *as_global(reinterpret_cast<u32x4*>(y)) = ow[i];
-      }
-    }
+    store(c);
   };
   int c = 0;
   while (c < chunks) {
@@ -435,22 +466,24 @@ void k_linear_states(LinArgs a) {
   const LinPlace at(a, a.nseg - 1, xcd_block(blockIdx.x, a.total), false);
   if (at.none) return;
   const LinRole& r = at.r;
-  const int rev = r.rev, lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+  const int rev = lin_scalar(r.rev), lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int col0 = at.slice * 16 * NW;
-  const u16* kb = r.k + (int64_t)at.h * DA;
-  const u16* vb = r.v + (int64_t)at.h * a.DB + col0;
+  const int chunks = lin_scalar(at.chunks);
+  const bool three = lin_scalar(r.fin) != nullptr;
   LinLoad<PA, NW> lk;
   LinLoad<PV, NW> lv;
-  lk.init(r.ldk, rev);
-  lv.init(r.ldv, rev);
-  auto load = [&](char* st, int c) __attribute__((always_inline)) {   // every chunk is whole
-    const int t = at.t0 + c * LIN_C;
-    const int64_t row = at.row0 + (rev ? at.len - t - LIN_C : t);
-    lk.issue(st, kb + row * r.ldk, LIN_C, rev, a.nt);
-    lv.issue(st + VO, vb + row * r.ldv, LIN_C, rev, a.nt);
+  {
+    const int64_t first = at.row0 + (rev ? at.len - at.t0 - LIN_C : at.t0);   // every chunk is whole
+    const int nt = lin_scalar(a.nt);
+    lk.init(r.k + (int64_t)at.h * DA, r.ldk, first, rev, nt);
+    lv.init(r.v + (int64_t)at.h * a.DB + col0, r.ldv, first, rev, nt);
+  }
+  auto load = [&](char* st) __attribute__((always_inline)) {
+    lk.issue(st, LIN_C, LIN_C);
+    lv.issue(st + VO, LIN_C, LIN_C);
   };
-  load(st0, 0);
+  load(st0);
   tb.init(a.decay[at.h], at);
   LinState<DA> S;
   S.clear();
@@ -458,17 +491,17 @@ void k_linear_states(LinArgs a) {
   int c = 0;
   auto step = [&](const char* cur, char* free) __attribute__((always_inline)) {
     lin_wait<0>();
-    if (c + 1 < at.chunks) load(free, c + 1);
+    if (c + 1 < chunks) load(free);
     bf16x8 vf[2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) vf[z] = lin_col<PV>(cur + VO + 32 * z * PV, va_at);
     S.decay(tb.pw[LIN_C]);
-    S.add(cur, ka_at, vf, tb.wt[0], g, r.fin != nullptr);
+    S.add(cur, ka_at, vf, tb.wt[0], g, three);
     ++c;
   };
-  while (c < at.chunks) {
+  while (c < chunks) {
     step(st0, st1);
-    if (c == at.chunks) break;
+    if (c == chunks) break;
     step(st1, st0);
   }
   S.store(r.ws + (((int64_t)at.b * a.heads + at.h) * a.nseg + at.seg) * DA * a.DB + col0 + 16 * wave + j, a.DB, g, 1.f);
