@@ -17,8 +17,10 @@ namespace ttt {
 namespace {
 
 // A tile keeps the 16-byte chunk c of row r at chunk c ^ lin_swz(r) of the row (P bytes): 16
-// consecutive rows at one chunk, and 32 elements of 4 consecutive rows, lie on distinct banks,
-// whether it is read along its rows or along its columns.
+// consecutive rows at one chunk lie on distinct banks (read along the rows), and so do 4 neighbouring
+// chunks of 4 consecutive rows (along the columns, where a product reads the first or the second halves
+// of chunks only: two fifths of the LDS's busy cycles are conflicts; halves in turn by lane, without
+// conflicts, made k_linear_states no faster).
 template <int P>
 __device__ __forceinline__ int lin_swz(int r) {
   return P == 128 ? (((r >> 1) & 1) << 2) | ((r >> 2) & 3) : ((r & 3) << 2) | ((r >> 2) & 3);
@@ -204,7 +206,9 @@ struct LinTables {
   }
 };
 
-// The state of a wave, 16 columns: element e of tile 2 y + t is row 32 y + 8 g + 4 t + e, column j.
+// The state of a wave, 16 columns: element e of tile 2 y + t is row 32 y + 8 g + 4 t + e, column j.  fp32 in
+// accumulators over a whole segment, as an operand two bf16 parts, so that out's error stays its own
+// rounding.
 template <int DA>
 struct LinState {
   static constexpr int P = DA * 2, N = DA / 16;
@@ -281,8 +285,13 @@ struct LinState {
 //
 // A wave's matrix and vector instructions do not run side by side, those of two waves do (4 products
 // and 24 multiplications: 120 ns of one wave, 70 a wave of two): many narrow waves, four to a SIMD, at
-// the price of reading q and k from LDS for each (columns of 32 a wave, two to a SIMD: 451 us for a
-// prompt of 131072 tokens of 8 heads of 128).
+// the price of reading q and k from LDS for each.  Columns of 32 a wave, two to a SIMD, were as fast on
+// long sequences (131072 tokens of 8 heads of 128: 403 us, 417 so) and slower on the others (24 ragged
+// prompts 198 -> 182, a training step of 3 x 777 tokens 79 -> 75).  What bounds the long ones: loads and
+// stores alone take 223 us of this kernel there, its work without loads 238, both 310; the matrix cores
+// are busy 31 % of the cycles, the vector units 42, the LDS 44, at 1.6 to 1.9 GHz: four waves of a SIMD
+// that each wait for their own chain of products, and power; neither another order of the instructions
+// nor a deeper ring of loads nor fewer LDS conflicts changed the time.
 //
 // Four areas of LDS take turns: while q, k and v of a chunk lie in three, the next chunk's q comes into
 // the fourth; once q has been read its k comes into q's, and once all has been read its v into k's.  Three
