@@ -636,6 +636,22 @@ def test_residual_norm_far_rows():
     assert all(torch.equal(a, b) for a, b in zip(near, far))
 
 
+def test_residual_norm_of_more_rows_than_a_launch():
+    """2^20 workgroups of one row each, and five more, in place."""
+    D, T = 1032, (1 << 20) + 5
+    c = Norm(T=61, D=D, kind="silu", pad=0)
+    near = c.call()
+    x = [t.repeat(T // 61 + 1, 1)[:T].contiguous() for t in (c.y, c.h, c.gate)]   # 2.2 GB each
+    y, h, gate = x
+    W.ttt_residual_norm(c.cfg, h, D, y, D, gate, D, c.wy, c.rs, c.wn, h, D, y, D, T)
+    torch.cuda.synchronize()
+    for got, ref in zip((h, y), near):
+        for a in (0, (1 << 20) // 61 * 61 - 61):      # the first rows, and those around the launch's end
+            assert torch.equal(got[a:a + 61], ref[:61])
+        for r in range((1 << 20) - 3, T):
+            assert torch.equal(got[r], ref[r % 61])
+
+
 def test_residual_norm_backward_captured():
     c = Norm(T=3001, D=256, groups=4, kind="silu")
     work = torch.empty(W.ttt_residual_norm_backward_work(c.cfg, c.T), dtype=torch.uint8, device=DEV)

@@ -283,6 +283,40 @@ int main() {
   return 0;
 }
 ''')
+    _run_host(src, tmp_path)
+
+
+def test_norm_launches_of_many_rows(tmp_path):
+    """A launch has fewer than 2^32 threads, and the launches that follow one another have the rows in turn."""
+    src = tmp_path / "index.cpp"
+    src.write_text(r'''
+#include <hip/hip_runtime.h>
+#include <cstdio>
+#include <cstdlib>
+#include "ttt_mixer_internal.h"
+using namespace ttt;
+#define CHECK(x) do { if (!(x)) { printf("line %d\n", __LINE__); exit(1); } } while (0)
+int main() {
+  CHECK(NORM_LAUNCH * 1024 < (int64_t)1 << 32);
+  NormArgs a = {};
+  a.y = (const void*)4096; a.ldy = 1 << 20;
+  a.n = (void*)8192; a.ldn = 8;
+  a.tokens = (1 << 25) - 3;
+  int64_t rows = 0;
+  for (int64_t first = 0; first < a.tokens; first += 1 << 20) {
+    const NormArgs p = norm_part(a, first, 1 << 20, 2);
+    CHECK(!p.h && !p.gate && !p.ho && p.tokens > 0 && p.tokens <= 1 << 20);
+    CHECK((int64_t)p.y == 4096 + (first << 21) && (int64_t)p.n == 8192 + first * 16 && p.ldy == a.ldy);
+    rows += p.tokens;
+  }
+  CHECK(rows == a.tokens);
+  return 0;
+}
+''')
+    _run_host(src, tmp_path)
+
+
+def _run_host(src, tmp_path):
     exe = tmp_path / "index"
     r = subprocess.run([B.HIPCC, "--offload-arch=gfx950", "-std=c++17", "-w", "-x", "hip", str(src), "-I" + os.path.join(ROOT, "include"),
                         "-I" + B.CSRC, "-o", str(exe)], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)

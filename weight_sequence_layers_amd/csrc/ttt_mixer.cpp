@@ -164,7 +164,6 @@ ttt_status check_norm(const ttt_residual_norm_config* c) {
 }
 
 ttt_status check_norm_tokens(int64_t tokens) {
-  // at most 2^23 workgroups of 256 threads where a row is a workgroup's, counted in 32 bits
   if (tokens < 0 || tokens > ((int64_t)1 << 25))
     return failf(TTT_E_SHAPE, "tokens %lld: in [0, 2^25]", (long long)tokens);
   return TTT_OK;

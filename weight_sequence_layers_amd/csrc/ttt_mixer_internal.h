@@ -104,6 +104,24 @@ struct NormArgs {
   float *dwy, *drs, *dwn;
 };
 
+// Workgroups of a launch at most: a launch's threads, up to 1024 of each, are counted in 32 bits.
+constexpr int64_t NORM_LAUNCH = (int64_t)1 << 20;
+
+// The forward call's rows from `first` on, at most n, of elements of `size` bytes.
+inline NormArgs norm_part(const NormArgs& a, int64_t first, int64_t n, int size) {
+  NormArgs p = a;
+  const auto from = [&](auto*& x, int64_t ld) {
+    if (x) x = (char*)x + first * ld * size;
+  };
+  from(p.h, a.ldh);
+  from(p.y, a.ldy);
+  from(p.gate, a.ldg);
+  from(p.ho, a.ldho);
+  from(p.n, a.ldn);
+  p.tokens = a.tokens - first < n ? a.tokens - first : n;
+  return p;
+}
+
 hipError_t launch_residual_norm(const NormArgs& a, int bf16, hipStream_t st);
 hipError_t launch_residual_norm_backward(const NormArgs& a, int bf16, hipStream_t st);
 int32_t residual_norm_wgs(int32_t D, int64_t tokens);   // workgroups of a backward launch

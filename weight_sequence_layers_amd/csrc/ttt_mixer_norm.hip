@@ -370,10 +370,16 @@ int64_t norm_rows(int D) {
 
 template <typename T, bool BWD, bool GATE, int W>
 hipError_t launch_w(const NormArgs& a, hipStream_t st) {
-  const int64_t rows = norm_rows(a.D);
   const dim3 block(norm_threads<W>);
-  if constexpr (BWD) hipLaunchKernelGGL((k_norm_bwd<T, W, GATE>), dim3(a.wgs), block, 0, st, a);
-  else hipLaunchKernelGGL((k_norm<T, W, GATE>), dim3((unsigned)((a.tokens + rows - 1) / rows)), block, 0, st, a);
+  if constexpr (BWD) {
+    hipLaunchKernelGGL((k_norm_bwd<T, W, GATE>), dim3(a.wgs), block, 0, st, a);
+  } else {
+    const int64_t rows = norm_rows(a.D), most = NORM_LAUNCH * rows;
+    for (int64_t first = 0; first < a.tokens; first += most) {
+      const NormArgs p = norm_part(a, first, most, sizeof(T));
+      hipLaunchKernelGGL((k_norm<T, W, GATE>), dim3((unsigned)((p.tokens + rows - 1) / rows)), block, 0, st, p);
+    }
+  }
   return hipGetLastError();
 }
 
