@@ -34,8 +34,8 @@ extern "C" {
  *   S_t = decay[h] S_{t-1} + k_t v_t^T,      out_t = scale S_t^T q_t
  * that is out_t = scale (decay^(t+1) S_in^T q_t + sum_{j <= t} decay^(t-j) (q_t . k_j) v_j).
  * decay is a constant of the head (no gradient): fp32 [heads] on the device, in [0, 1]; 1 is
- * linear attention without decay, 0 leaves each token its own value only.  Another finite
- * value is taken by the formula.
+ * linear attention without decay, 0 leaves each token its own value only.  Another value is
+ * taken by the formula where its powers up to seq_len are finite in fp32.
  * Limits: heads in [1, 4096]; dim_k and dim_v 64, 128 or 256, each; scale finite and > 0, or 0,
  * which selects 1 / sqrt(dim_k).
  */

@@ -435,6 +435,41 @@ def test_linear_attention_without_sequences_or_tokens():
     assert bool((out == 7).all()) and torch.equal(sout, sin) and torch.equal(dsin, sin)
 
 
+def test_linear_attention_of_the_largest_batch():
+    """65535 sequences of one token, 2^20 sequences and heads together: out = scale (q . k) v; the weight in
+    fp32 (64 roundings of 2^-24 of the products' sizes) and as two bf16 numbers (2^-16), out rounded."""
+    B, heads, D = 65535, 16, 64
+    cfg = W.make_linear_attention_config(heads=heads, dim_k=D)
+    q, k, v = (torch.randn(B, heads * D, generator=gen(i), device=DEV).to(BF) for i in range(3))
+    out, decay = torch.empty_like(q), torch.ones(heads, device=DEV)
+    W.ttt_linear_attention(cfg, q, heads * D, k, heads * D, v, heads * D, decay, None, None, None, None, out, heads * D, B,
+                           B, 1, None)
+    torch.cuda.synchronize()
+    q, k, v, o = (t.view(B, heads, D).double() for t in (q, k, v, out))
+    p, size = (q * k).sum(-1, keepdim=True) / 8, (q * k).abs().sum(-1, keepdim=True) / 8
+    assert bool(((o - p * v).abs() <= 2.0 ** -8 * (p * v).abs() + 2.0 ** -15 * size * v.abs()).all())
+
+
+@pytest.mark.parametrize("lens", [[90, 64], [600]])
+def test_linear_attention_of_decays_outside_the_unit_interval(lens):
+    """Negative ones and ones past 1 are taken by the formula: (-a)^n = (-1)^n a^n, so that the results are
+    those of a with every other key and query and the first state turned, within their bars."""
+    c = Linear(lens=lens, heads=3, K=64, V=64, decay=[-0.9, 1.004, -1.0])
+    sin, sout = c.states(), c.states()
+    out = c.call(sin, sout)
+    torch.cuda.synchronize()
+    for i, n in enumerate(lens):
+        for h, a in enumerate([-0.9, 1.004, -1.0]):
+            q, k, v = c.qkv(i, h)
+            sign, last = 1.0, 1.0
+            if a < 0:      # S_t of -a is (-1)^(t + 1) times that of a
+                sign, last = -1.0, 1.0 if n % 2 else -1.0
+                turn = np.where(np.arange(n) % 2, -1.0, 1.0)[:, None]
+                q, k = q * turn, k * turn
+            (o, bar), (S, sbar) = bars.forward(q, k, v, abs(c.lam(h)), sign * np64(sin[i, h]), c.scale)
+            assert worst(c.part(out, i, h, 64), o, bar) <= 1 and worst(np64(sout[i, h]), last * S, sbar) <= 1
+
+
 def test_linear_attention_gradients_against_differences():
     """The kernel's own forward, differenced along one direction of v and of the initial state, in which the
     output is linear: the outputs' roundings, R / sqrt(3) of each, are all that is left."""
