@@ -94,8 +94,9 @@ ttt_status ttt_linear_attention(const ttt_linear_attention_config* cfg, const vo
  * buffer's rows) and, where given, dstate_in, that of the initial states (fp32, as dstate_out).
  * With P_t = decay P_{t+1} + scale q_t dout_t^T (P_T the gradient of the final state over decay):
  *   dq_t = scale S_t dout_t,  dk_t = P_t v_t,  dv_t = P_t^T k_t,  dstate_in = decay P_0.
- * Precision, order, starts and limits as above.  The gradients and work may not overlap the inputs or each
- * other.  Rows that belong to no sequence are left as they are.
+ * Precision, order, starts and limits as above; all values must be finite, one that is not reaches up
+ * to 63 tokens back, and backward in time (dk, dv) as many on.  The gradients and work may not overlap the
+ * inputs or each other.  Rows that belong to no sequence are left as they are.
  */
 ttt_status ttt_linear_attention_backward_work(const ttt_linear_attention_config* cfg,
                                               int32_t batch, int64_t seq_len, int64_t* bytes);
