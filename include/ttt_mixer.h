@@ -120,7 +120,11 @@ ttt_status ttt_linear_attention_step(const ttt_linear_attention_config* cfg, con
                                      float* state_out, const int32_t* slot, int32_t slots,
                                      void* out, int64_t ld_out, int32_t seqs, void* stream);
 
-/* The gate of a sub-layer's output: none, sigmoid(g), or silu(g) = g sigmoid(g). */
+/*
+ * The gate of a sub-layer's output: none, sigmoid(g), or silu(g) = g sigmoid(g).  Any g may be given, the
+ * lowest number of the type as a mask among them; at infinity they are their limits: sigmoid 0 and 1, silu
+ * 0 at minus infinity.
+ */
 typedef enum { TTT_GATE_NONE = 0, TTT_GATE_SIGMOID = 1, TTT_GATE_SILU = 2 } ttt_gate;
 
 /*

@@ -14,7 +14,7 @@
 // between the forward and the backward, which reads h and y again instead of saved statistics.
 //
 // Measured: 64320 rows of 768 in fp32 (two read, two written, 791 MB) 150 us, 5.3 TB/s; backward with a
-// gate of 32768 rows of 1024 in bf16 (537 MB) 116 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
+// gate of 32768 rows of 1024 in bf16 (537 MB) 118 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
 // TB/s, 5 us of each the weights' second launch; a copy of 4 GB reaches 5.0.  Without a gate bf16 rows
 // run at 6.2 to 6.7; backwards of rows past 2048 elements at 2.7 to 3.9, their barriers (one workgroup of
 // 8 or 16 waves to a row, one to a CU) no longer hidden.
@@ -64,18 +64,24 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
   *as_global(reinterpret_cast<f32x4*>(p + 4)) = f32x4{x[4], x[5], x[6], x[7]};
 }
 
-// 1 / (1 + exp(-g)) within about two half steps of fp32: the exponent keeps what its product rounds
-// off, the reciprocal takes a Newton step; beyond 2^126 it stays there (the sigmoid below 2^-126).
+// 1 / (1 + exp(-g)) within about ten half steps of fp32, for every g.  With e = exp(-|g|), which is at most 1, it is
+// 1 / (1 + e) or e / (1 + e): nothing overflows or cancels.  e is the square of exp(-|g| / 2), so that it may be
+// below fp32's normal numbers, which the exponential itself cannot give; the exponent keeps what its product
+// rounds off, |g| held to 110 (e is 0 from 104 on), and the reciprocal takes a Newton step.  NaN stays NaN.
+constexpr float GATE_FAR = 110.f;
 __device__ __forceinline__ float sigmoid(float g) {
-  constexpr float L = -1.44269504088896341f, LL = -1.925963033500e-8f;
-  float t = g * L;
-  const float low = fmaf(g, L, -t) + g * LL;
-  t = t > 126.f ? 126.f : t;
-  const float x = __builtin_amdgcn_exp2f(t);
-  const float d = 1.f + fmaf(x, low * 0.693147181f, x);
-  const float r = __builtin_amdgcn_rcpf(d);
-  return fmaf(r, fmaf(-d, r, 1.f), r);
+  constexpr float L = -0.72134752044448170f, LL = -9.6298149556e-9f;   // -log2(e) / 2, and what its rounding leaves
+  const float a = fabsf(g) > GATE_FAR ? GATE_FAR : fabsf(g);
+  const float t = a * L, low = fmaf(a, L, -t) + a * LL;
+  float x = __builtin_amdgcn_exp2f(t);
+  x = fmaf(x, low * 0.693147181f, x);
+  const float e = x * x, d = 1.f + e;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = fmaf(r, fmaf(-d, r, 1.f), r);
+  return g >= 0.f ? r : e * r;
 }
+// The factor that silu has and the sigmoid has not: g, held where the sigmoid is 0 so that their product is.
+__device__ __forceinline__ float silu_factor(float g) { return fmaxf(g, -GATE_FAR); }
 
 // Lanes of a row: a power of two of a wave's, or the workgroup.
 __host__ __device__ inline int norm_lanes(int D) {
@@ -199,7 +205,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float z = y[e] * r * w[e];
-    if (GATE) z *= sigmoid(g[e]) * (silu ? g[e] : 1.f);
+    if (GATE) z *= sigmoid(g[e]) * (silu ? silu_factor(g[e]) : 1.f);
     x[e] = fmaf(s[e], z, h[e]);
     hh = fmaf(x[e], x[e], hh);
   }
@@ -270,7 +276,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
     if (GATE)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sg[e] = sigmoid(g[e]);
-    auto act = [&](int e) __attribute__((always_inline)) { return GATE ? sg[e] * (silu ? g[e] : 1.f) : 1.f; };
+    auto act = [&](int e) __attribute__((always_inline)) { return GATE ? sg[e] * (silu ? silu_factor(g[e]) : 1.f) : 1.f; };
     if (a.dn) {
       float hh = 0.f, ax = 0.f;
 #pragma unroll
