@@ -62,6 +62,28 @@ def test_the_gates_value_of_every_number(kind, act):
     assert np.max(e) <= 1, (g[np.argmax(e)], got[np.argmax(e)], ref[np.argmax(e)])
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "silu"])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_the_gates_slope_of_every_number(kind, act):
+    """dgate of y = dh_out = 1.  s and 1 - s within 10 U each: s (1 - s) 21 U, and s + g s (1 - s) 22 U of the
+    sum of its terms' sizes; the output's rounding on top, and half of the least numbers as in the value's test."""
+    g = every_gate(act).view(-1, 64)
+    say(f"gate slopes {kind} {act} {len(g)}")
+    cfg = W.make_residual_norm_config(dim=64, gate=kind, act=act)
+    out, one = torch.empty_like(g), torch.ones_like(g)
+    W.ttt_residual_norm_backward(cfg, None, 0, one, 64, g, 64, None, None, None, one, 64, None, 0, None, 0, None, 0, out, 64,
+                                 None, None, None, None, len(g))
+    torch.cuda.synchronize()
+    g, got = np64(g), np64(out)
+    nan = np.isnan(g)
+    assert np.array_equal(np.isnan(got), nan)
+    g, got = g[~nan], got[~nan]
+    ref, (s, o) = stable(g, kind)[1], parts(g)
+    size = s * o if kind == "sigmoid" else s * (1 + np.clip(np.abs(g), 0, 1000) * o)
+    e = np.abs(got - ref) / (H[out.dtype] * np.abs(ref) + 22 * U * size + LEAST[out.dtype] + 220 * 2.0 ** -150)
+    assert np.max(e) <= 1, (g[np.argmax(e)], got[np.argmax(e)], ref[np.argmax(e)])
+
+
 # one gate a row, beside ordinary ones
 SMALL = [-80.0, -87.3, -88.0, -100.0, -104.0, -150.0, -1e4, -4.72e7, -1e8, -1e9, -1e10, -1e12, -1e30, -3e38, "min", "-inf"]
 LARGE = [20.0, 88.0, 150.0, 1e4, 1e8, 1e12, 1e30, 2.4e38, 3e38, "max", "inf"]

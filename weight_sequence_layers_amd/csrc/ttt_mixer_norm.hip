@@ -14,7 +14,7 @@
 // between the forward and the backward, which reads h and y again instead of saved statistics.
 //
 // Measured: 64320 rows of 768 in fp32 (two read, two written, 791 MB) 150 us, 5.3 TB/s; backward with a
-// gate of 32768 rows of 1024 in bf16 (537 MB) 118 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
+// gate of 32768 rows of 1024 in bf16 (537 MB) 117 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
 // TB/s, 5 us of each the weights' second launch; a copy of 4 GB reaches 5.0.  Without a gate bf16 rows
 // run at 6.2 to 6.7; backwards of rows past 2048 elements at 2.7 to 3.9, their barriers (one workgroup of
 // 8 or 16 waves to a row, one to a CU) no longer hidden.
@@ -54,9 +54,12 @@ struct Raw8<float> {
   __device__ __forceinline__ float operator[](int i) const { return w[i >> 2][i & 3]; }
 };
 __device__ __forceinline__ void store8(u16* p, const float* x) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   u32x4 w;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = f2bf(x[2 * i]) | ((uint32_t)f2bf(x[2 * i + 1]) << 16);
+  for (int i = 0; i < 4; ++i)   // two at once, rounded to the nearest even one
+    w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x[2 * i], x[2 * i + 1]}), bf16x2));
   *as_global(reinterpret_cast<u32x4*>(p)) = w;
 }
 __device__ __forceinline__ void store8(float* p, const float* x) {
@@ -64,12 +67,13 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
   *as_global(reinterpret_cast<f32x4*>(p + 4)) = f32x4{x[4], x[5], x[6], x[7]};
 }
 
-// 1 / (1 + exp(-g)) within about ten half steps of fp32, for every g.  With e = exp(-|g|), which is at most 1, it is
-// 1 / (1 + e) or e / (1 + e): nothing overflows or cancels.  e is the square of exp(-|g| / 2), so that it may be
-// below fp32's normal numbers, which the exponential itself cannot give; the exponent keeps what its product
-// rounds off, |g| held to 110 (e is 0 from 104 on), and the reciprocal takes a Newton step.  NaN stays NaN.
+// The smaller of 1 / (1 + exp(-g)) and what that leaves of 1, with g's sign, within about ten half steps of fp32,
+// for every g.  With e = exp(-|g|), which is at most 1, it is e / (1 + e): nothing overflows or cancels, nor does 1 less it.  e
+// is the square of exp(-|g| / 2), so that it may be below fp32's normal numbers, which the exponential itself
+// cannot give; the exponent keeps what its product rounds off, |g| held to 110 (e is 0 from 104 on), and the
+// reciprocal takes a Newton step.  NaN stays NaN.
 constexpr float GATE_FAR = 110.f;
-__device__ __forceinline__ float sigmoid(float g) {
+__device__ __forceinline__ float sigmoid_tail(float g) {
   constexpr float L = -0.72134752044448170f, LL = -9.6298149556e-9f;   // -log2(e) / 2, and what its rounding leaves
   const float a = fabsf(g) > GATE_FAR ? GATE_FAR : fabsf(g);
   const float t = a * L, low = fmaf(a, L, -t) + a * LL;
@@ -78,10 +82,22 @@ __device__ __forceinline__ float sigmoid(float g) {
   const float e = x * x, d = 1.f + e;
   float r = __builtin_amdgcn_rcpf(d);
   r = fmaf(r, fmaf(-d, r, 1.f), r);
-  return g >= 0.f ? r : e * r;
+  return copysignf(e * r, g);
 }
-// The factor that silu has and the sigmoid has not: g, held where the sigmoid is 0 so that their product is.
-__device__ __forceinline__ float silu_factor(float g) { return fmaxf(g, -GATE_FAR); }
+// The gate's value from the tail q: the sigmoid, or for silu g times it, g held where it is 0 so that their
+// product is; and its slope, s (1 - s) or s + g s (1 - s), g held on both sides.
+__device__ __forceinline__ float from_tail(float q) {   // by the sign's bit: q may be -0
+  return __builtin_bit_cast(int32_t, q) < 0 ? -q : 1.f - q;
+}
+template <int GATE>
+__device__ __forceinline__ float gate_value(float g, float q) {
+  return GATE == TTT_GATE_SILU ? from_tail(q) * __builtin_amdgcn_fmed3f(g, -GATE_FAR, INFINITY) : from_tail(q);
+}
+template <int GATE>
+__device__ __forceinline__ float gate_slope(float g, float q) {
+  const float m = fabsf(q) * (1.f - fabsf(q));
+  return GATE == TTT_GATE_SILU ? fmaf(__builtin_amdgcn_fmed3f(g, -GATE_FAR, GATE_FAR), m, from_tail(q)) : m;
+}
 
 // Lanes of a row: a power of two of a wave's, or the workgroup.
 __host__ __device__ inline int norm_lanes(int D) {
@@ -171,8 +187,8 @@ __device__ __forceinline__ float inv_rms(float ss, const NormArgs& a, RowSum<W>&
   return 1.f / sqrtf((a.gw == a.D ? sum(ss) : lanes_sum(ss, a.gw >> 3)) / (float)a.gw + a.eps);
 }
 
-// W: waves of a row; GATE: whether there is a gate (its kind is one select an element).
-template <typename T, int W, bool GATE>
+// W: waves of a row; GATE: the gate's kind (as a select of each element: 120 us instead of 118.7 for that backward).
+template <typename T, int W, int GATE>
 __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
   __shared__ float scratch[4][16];
   const int lanes = W == 1 ? norm_lanes(a.D) : 64 * W;
@@ -180,7 +196,6 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
   const int64_t t = (int64_t)blockIdx.x * (norm_threads<W> / lanes) + threadIdx.x / lanes;
   const int col = (int)threadIdx.x % lanes * 8;
   const bool on = t < a.tokens && col < a.D;       // the sums need all lanes
-  const bool silu = a.gate_kind == TTT_GATE_SILU;
   Raw8<T> y, h, g, w, s;
   y.fill(0.f);
   h.fill(0.f);
@@ -205,7 +220,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float z = y[e] * r * w[e];
-    if (GATE) z *= sigmoid(g[e]) * (silu ? silu_factor(g[e]) : 1.f);
+    if (GATE) z *= gate_value<GATE>(g[e], sigmoid_tail(g[e]));
     x[e] = fmaf(s[e], z, h[e]);
     hh = fmaf(x[e], x[e], hh);
   }
@@ -224,7 +239,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
 
 // Backward: the workgroups walk over the rows, so that the partial sums of the scales' gradients are
 // few; a second launch adds them up in order.
-template <typename T, int W, bool GATE>
+template <typename T, int W, int GATE>
 __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
   constexpr int NT = norm_threads<W>;
   __shared__ float scratch[4][16];
@@ -232,7 +247,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
   const int lanes = W == 1 ? norm_lanes(a.D) : 64 * W, rows = NT / lanes;
   RowSum<W> sum{scratch, lanes};
   const int col = (int)threadIdx.x % lanes * 8;
-  const bool has = col < a.D, silu = a.gate_kind == TTT_GATE_SILU;
+  const bool has = col < a.D;
   Raw8<T> wy, rs, wn;
   float dw[3][8];
   wy.fill(1.f);
@@ -271,12 +286,12 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
       for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
       r = inv_rms<W>(ss, a, sum);
     }
-    // the gate's sigmoid, and d, the gradient of h'
-    float sg[8], d[8];
+    // the gate's tail, and d, the gradient of h'
+    float q[8], d[8];
     if (GATE)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sg[e] = sigmoid(g[e]);
-    auto act = [&](int e) __attribute__((always_inline)) { return GATE ? sg[e] * (silu ? silu_factor(g[e]) : 1.f) : 1.f; };
+      for (int e = 0; e < 8; ++e) q[e] = sigmoid_tail(g[e]);
+    auto act = [&](int e) __attribute__((always_inline)) { return GATE ? gate_value<GATE>(g[e], q[e]) : 1.f; };
     if (a.dn) {
       float hh = 0.f, ax = 0.f;
 #pragma unroll
@@ -302,10 +317,11 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
     float dg[8], dot = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+      if (GATE) asm("" : "+v"(q[e]));   // the gate's values again from the tail: kept, they took 16 more registers
       const float yr = y[e] * r, u = yr * wy[e], ac = act(e);
       dw[1][e] = fmaf(d[e], u * ac, dw[1][e]);
       const float ez = d[e] * rs[e];
-      if (GATE) dg[e] = ez * u * (silu ? fmaf(ac, 1.f - sg[e], sg[e]) : sg[e] * (1.f - sg[e]));
+      if (GATE) dg[e] = ez * u * gate_slope<GATE>(g[e], q[e]);
       const float f = ez * ac;
       dw[0][e] = fmaf(f, yr, dw[0][e]);
       d[e] = f * wy[e];
@@ -374,7 +390,7 @@ int64_t norm_rows(int D) {
   return w > 4 ? 1 : NORM_NT / (w > 1 ? 64 * w : norm_lanes(D));
 }
 
-template <typename T, bool BWD, bool GATE, int W>
+template <typename T, bool BWD, int GATE, int W>
 hipError_t launch_w(const NormArgs& a, hipStream_t st) {
   const dim3 block(norm_threads<W>);
   if constexpr (BWD) {
@@ -389,7 +405,7 @@ hipError_t launch_w(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, bool BWD, bool GATE>
+template <typename T, bool BWD, int GATE>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
   switch (norm_waves(a.D)) {
     case 1: return launch_w<T, BWD, GATE, 1>(a, st);
@@ -402,7 +418,9 @@ hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
 
 template <typename T, bool BWD>
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
-  return a.gate_kind ? launch_rows<T, BWD, true>(a, st) : launch_rows<T, BWD, false>(a, st);
+  return a.gate_kind == TTT_GATE_NONE      ? launch_rows<T, BWD, TTT_GATE_NONE>(a, st)
+         : a.gate_kind == TTT_GATE_SIGMOID ? launch_rows<T, BWD, TTT_GATE_SIGMOID>(a, st)
+                                           : launch_rows<T, BWD, TTT_GATE_SILU>(a, st);
 }
 
 }  // namespace
