@@ -6,6 +6,7 @@ import weight_sequence_layers_amd as W
 from test_gpu_mixer import BF, DEV, Norm, gen, say
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
 
 # 768 workgroups of 256 / lanes rows up to rows of 2048 elements, 384 and 256 of one row beyond; the last round not
 # full, with 1 to 3 sums over each row
@@ -49,3 +50,47 @@ def test_residual_norm_backward_adds_up_every_row(T, D, act):
                                  None, None, sums[2], work, T)
     torch.cuda.synchronize()
     assert all(torch.equal(s.double(), want) for s in sums)
+
+
+@pytest.mark.parametrize("T,D", [(768 * 1024 + 5, 1032), (384 * 1024 + 5, 2056)])
+def test_residual_norm_backward_of_equal_rows(T, D):
+    """Equal terms, which a long sum in 32 bits rounds to one side at every addition: 1 + 2^-15 - 2^-20 added to a sum
+    between 512 and 1024, whose numbers are 2^-14 apart, adds 1.  The sums are chains of at most 64 additions (64 U),
+    what joins them (U) and one rounding at the end."""
+    say(f"equal rows T={T} D={D}")
+    c = 1 + 2.0 ** -15 - 2.0 ** -20
+    y, d, one = (torch.full(s, x, device=DEV) for s, x in (((T, D), 1.0), ((T, D), c), ((D,), 1.0)))
+    cfg = W.make_residual_norm_config(dim=D, act="f32")
+    work = torch.empty(W.ttt_residual_norm_backward_work(cfg, T), dtype=torch.uint8, device=DEV)
+    got = torch.empty(D, device=DEV)
+    dy = torch.empty(T, D, device=DEV)
+    W.ttt_residual_norm_backward(cfg, None, 0, y, D, None, 0, None, one, None, d, D, None, 0, None, 0, dy, D, None, 0, None,
+                                 got, None, work, T)
+    torch.cuda.synchronize()
+    e = float(((got.double() - T * c) / (T * c)).abs().max())
+    assert e <= 66 * U, e
+
+
+def test_residual_norm_backward_of_several_launches_captured():
+    """Rows past 64 to a workgroup go into launches of their own: replayed with other rows beside the same eager call on
+    another stream; work between the calls holds anything."""
+    c = Norm(T=256 * 64 * 2 + 9, D=4104, kind="silu", pad=0)
+    n = W.ttt_residual_norm_backward_work(c.cfg, c.T)
+    outs, eager = [c.new(0), c.new(0), c.new(0), c.sums()], [c.new(0), c.new(0), c.new(0), c.sums()]
+    work, other = (torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(2))
+    c.back(*outs, work=work)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        c.back(*outs, work=work)
+    for i in range(3):
+        c.y.copy_(torch.randn(c.y.shape, generator=gen(10 + i), device=DEV))
+        for t in (*outs[:3], *outs[3], *eager[:3], *eager[3]):
+            t.fill_(7.0)
+        work.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            c.back(*eager, work=other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*outs[:3], *outs[3]), (*eager[:3], *eager[3])))

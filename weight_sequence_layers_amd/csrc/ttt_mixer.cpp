@@ -188,8 +188,13 @@ bool partly(const Rows& o, std::initializer_list<Rows> ins) {
   return false;
 }
 
-int64_t norm_work_bytes(const ttt_residual_norm_config* c, int64_t tokens) {
+// The workgroups' partial sums, and behind them, where there are several launches, their sums so far.
+int64_t norm_part_bytes(const ttt_residual_norm_config* c, int64_t tokens) {
   return (int64_t)3 * residual_norm_wgs(c->dim, tokens) * c->dim * (int64_t)sizeof(float);
+}
+int64_t norm_work_bytes(const ttt_residual_norm_config* c, int64_t tokens) {
+  return norm_part_bytes(c, tokens) +
+         (tokens > residual_norm_chunk(c->dim) ? (int64_t)3 * c->dim * (int64_t)sizeof(double) : 0);
 }
 
 struct NormInputs {
@@ -578,7 +583,7 @@ ttt_status ttt_residual_norm_backward(const ttt_residual_norm_config* cfg, const
   a.drs = dres_scale;
   a.dwn = dn_weight;
   a.part = want ? static_cast<float*>(work) : nullptr;
-  a.wgs = residual_norm_wgs(cfg->dim, tokens);
+  if (want && tokens) a.sofar = reinterpret_cast<double*>(static_cast<char*>(work) + norm_part_bytes(cfg, tokens));
   BLK_HIP(launch_residual_norm_backward(a, cfg->act == TTT_BF16, static_cast<hipStream_t>(stream)));
   return TTT_OK;
 }

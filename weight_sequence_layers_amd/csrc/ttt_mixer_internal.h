@@ -100,14 +100,15 @@ struct NormArgs {
   int32_t norm_y, gate_kind;
   float eps;
   float* part;                   // backward: [3][wgs][D] partial sums, or null
-  int32_t wgs;
+  double* sofar;                 // [3][D] their sums over the rows of earlier launches
+  int32_t wgs, begun, more;      // begun, more: there are launches before, behind
   float *dwy, *drs, *dwn;
 };
 
 // Workgroups of a launch at most: a launch's threads, up to 1024 of each, are counted in 32 bits.
 constexpr int64_t NORM_LAUNCH = (int64_t)1 << 20;
 
-// The forward call's rows from `first` on, at most n, of elements of `size` bytes.
+// A call's rows from `first` on, at most n, of elements of `size` bytes.
 inline NormArgs norm_part(const NormArgs& a, int64_t first, int64_t n, int size) {
   NormArgs p = a;
   const auto from = [&](auto*& x, int64_t ld) {
@@ -118,12 +119,18 @@ inline NormArgs norm_part(const NormArgs& a, int64_t first, int64_t n, int size)
   from(p.gate, a.ldg);
   from(p.ho, a.ldho);
   from(p.n, a.ldn);
+  from(p.dho, a.lddho);
+  from(p.dn, a.lddn);
+  from(p.dh, a.lddh);
+  from(p.dy, a.lddy);
+  from(p.dg, a.lddg);
   p.tokens = a.tokens - first < n ? a.tokens - first : n;
   return p;
 }
 
 hipError_t launch_residual_norm(const NormArgs& a, int bf16, hipStream_t st);
 hipError_t launch_residual_norm_backward(const NormArgs& a, int bf16, hipStream_t st);
-int32_t residual_norm_wgs(int32_t D, int64_t tokens);   // workgroups of a backward launch
+int32_t residual_norm_wgs(int32_t D, int64_t tokens);   // workgroups of a backward launch of so many rows
+int64_t residual_norm_chunk(int32_t D);                  // rows of a backward launch at most
 
 }  // namespace ttt

@@ -14,7 +14,7 @@
 // between the forward and the backward, which reads h and y again instead of saved statistics.
 //
 // Measured: 64320 rows of 768 in fp32 (two read, two written, 791 MB) 150 us, 5.3 TB/s; backward with a
-// gate of 32768 rows of 1024 in bf16 (537 MB) 117 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
+// gate of 32768 rows of 1024 in bf16 (537 MB) 116 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
 // TB/s, 5 us of each the weights' second launch; a copy of 4 GB reaches 5.0.  Without a gate bf16 rows
 // run at 6.2 to 6.7; backwards of rows past 2048 elements at 2.7 to 3.9, their barriers (one workgroup of
 // 8 or 16 waves to a row, one to a CU) no longer hidden.
@@ -25,6 +25,7 @@ namespace ttt {
 namespace {
 
 constexpr int NORM_NT = 256;
+constexpr int NORM_CHAIN = 64;   // rows of a lane in a backward launch at most, whose scales' gradients it adds up in fp32
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
@@ -238,7 +239,9 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
 }
 
 // Backward: the workgroups walk over the rows, so that the partial sums of the scales' gradients are
-// few; a second launch adds them up in order.
+// few; a second launch adds them up in order.  Rows past NORM_CHAIN to a lane go into further pairs of launches,
+// whose sums are joined in 64 bits (added up in one launch, 1024 equal rows to a lane gave sums 1.4e-5 off; a join
+// inside the loop took 10 to 20 more registers and a wave of a SIMD from every size).
 template <typename T, int W, int GATE>
 __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
   constexpr int NT = norm_threads<W>;
@@ -359,7 +362,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
 }
 
 // Columns of the partial sums added up over the workgroups: 16 columns per workgroup, 64 rows at a
-// time, in 64 bits and one order.
+// time, in 64 bits and one order, behind what earlier launches' rows gave.
 __global__ __launch_bounds__(1024) void k_norm_dw(NormArgs a) {
   __shared__ double acc[1024];
   const int which = blockIdx.y;
@@ -376,7 +379,12 @@ __global__ __launch_bounds__(1024) void k_norm_dw(NormArgs a) {
     __syncthreads();
     if ((int)threadIdx.x < half) acc[threadIdx.x] += acc[threadIdx.x + half];
   }
-  if (threadIdx.x < 16 && c < a.D) out[c] = (float)acc[threadIdx.x];
+  if (threadIdx.x < 16 && c < a.D) {
+    double* sofar = a.sofar + which * a.D + c;
+    s = acc[threadIdx.x] + (a.begun ? *sofar : 0.0);
+    if (a.more) *sofar = s;
+    else out[c] = (float)s;
+  }
 }
 
 // Waves of a row, rows of a workgroup.
@@ -390,11 +398,23 @@ int64_t norm_rows(int D) {
   return w > 4 ? 1 : NORM_NT / (w > 1 ? 64 * w : norm_lanes(D));
 }
 
+void launch_dw(const NormArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL(k_norm_dw, dim3((a.D + 15) / 16, 3), dim3(1024), 0, st, a);
+}
+
 template <typename T, bool BWD, int GATE, int W>
 hipError_t launch_w(const NormArgs& a, hipStream_t st) {
   const dim3 block(norm_threads<W>);
   if constexpr (BWD) {
-    hipLaunchKernelGGL((k_norm_bwd<T, W, GATE>), dim3(a.wgs), block, 0, st, a);
+    const int64_t most = residual_norm_chunk(a.D);
+    for (int64_t first = 0; first < a.tokens; first += most) {
+      NormArgs p = norm_part(a, first, most, sizeof(T));
+      p.wgs = residual_norm_wgs(a.D, p.tokens);
+      p.begun = first > 0;
+      p.more = first + most < a.tokens;
+      hipLaunchKernelGGL((k_norm_bwd<T, W, GATE>), dim3(p.wgs), block, 0, st, p);
+      if (a.part) launch_dw(p, st);
+    }
   } else {
     const int64_t rows = norm_rows(a.D), most = NORM_LAUNCH * rows;
     for (int64_t first = 0; first < a.tokens; first += most) {
@@ -431,16 +451,17 @@ int32_t residual_norm_wgs(int32_t D, int64_t tokens) {
   return (int32_t)(n < most ? n : most);
 }
 
+int64_t residual_norm_chunk(int32_t D) {
+  return NORM_CHAIN * norm_rows(D) * residual_norm_wgs(D, (int64_t)1 << 25);
+}
+
 hipError_t launch_residual_norm(const NormArgs& a, int bf16, hipStream_t st) {
   return bf16 ? launch_norm<u16, false>(a, st) : launch_norm<float, false>(a, st);
 }
 
 hipError_t launch_residual_norm_backward(const NormArgs& a, int bf16, hipStream_t st) {
-  if (a.tokens) {
-    const hipError_t e = bf16 ? launch_norm<u16, true>(a, st) : launch_norm<float, true>(a, st);
-    if (e != hipSuccess) return e;
-  }
-  if (a.dwy || a.drs || a.dwn) hipLaunchKernelGGL(k_norm_dw, dim3((a.D + 15) / 16, 3), dim3(1024), 0, st, a);
+  if (a.tokens) return bf16 ? launch_norm<u16, true>(a, st) : launch_norm<float, true>(a, st);
+  if (a.dwy || a.drs || a.dwn) launch_dw(a, st);   // zeros
   return hipGetLastError();
 }
 
