@@ -151,14 +151,36 @@ __device__ __forceinline__ void lin_split(float (&x)[8], bf16x8 (&p)[N]) {
 }
 
 // a^n, in 64 bits: a table made of rounded products would drift over long sequences
-__device__ __forceinline__ float lin_power(float a, int n) {
+__device__ __forceinline__ double lin_power64(float a, int n) {
   double p = 1.0, x = (double)a;
   for (; n; n >>= 1) {
     if (n & 1) p *= x;
     x *= x;
   }
-  return (float)p;
+  return p;
 }
+__device__ __forceinline__ float lin_power(float a, int n) { return (float)lin_power64(a, n); }
+
+// The state's factor for each whole chunk, a^LIN_C: of the two fp32 numbers around it, each as often as keeps
+// their product within one step of a's power.  The nearer one alone is off to the same side at every chunk (the
+// state 1.6e-5 after 131072 tokens at a decay of 1 - 2^-16, 4e-6 after 32768 at 1 - 2^-12).
+struct LinDecay {
+  uint32_t lower, share, sum;   // the number nearer to 0; the other's share of the chunks, of 2^32; and its sum so far
+  __device__ __forceinline__ void init(float a) {
+    const double p = lin_power64(a, LIN_C);
+    uint32_t u = __builtin_bit_cast(uint32_t, (float)p);
+    if (fabs((double)(float)p) > fabs(p)) --u;
+    const double x = (double)__builtin_bit_cast(float, u), step = fabs((double)__builtin_bit_cast(float, u + 1) - x);
+    lower = lin_scalar(u);
+    // the step is a power of 2, and what p is past x is less; no share where the decay is not finite
+    share = lin_scalar(step < INFINITY ? (uint32_t)__builtin_ldexp(fabs(p - x), 33 - __builtin_amdgcn_frexp_exp(step)) : 0u);
+    sum = 1u << 31;
+  }
+  __device__ __forceinline__ float next() {
+    sum += share;
+    return __builtin_bit_cast(float, lower + (sum < share));
+  }
+};
 
 // Waits until at most n of the wave's memory operations are under way (loads end in the order of
 // their issue), then for the workgroup: what the waves had loaded is there, what they had read is free.
@@ -339,6 +361,8 @@ void k_linear(LinArgs a) {
     load_v(a2, 0);
   }
   tb.init(lam, at);
+  LinDecay chunk_decay;
+  chunk_decay.init(lam);
   if (wave < 2) scores[0][wave][lane][1] = scores[3][wave][lane][1] = u32x2{0, 0};   // keys behind all of the queries
 
   const int64_t elems = (int64_t)DA * a.DB;
@@ -434,7 +458,7 @@ void k_linear(LinArgs a) {
 #pragma unroll
         for (int i = 2 * z; i < 4; ++i)
           o[i] = lin_mma(vf[z], *reinterpret_cast<const bf16x8*>(scores[i < 2 ? i : 2 * i - 2 + z][x][lane]), o[i]);
-    S.decay(tb.pw[n - 1 + e0]);
+    S.decay(n - 1 + e0 == LIN_C ? chunk_decay.next() : tb.pw[n - 1 + e0]);
     S.add(ka, ka_at, vf, tb.wt[more ? 0 : 1], g, fin != nullptr);
     // rows of 16 lanes swapped in pairs: 8 neighbouring elements of a token in a lane
 #pragma unroll
@@ -493,7 +517,10 @@ void k_linear_states(LinArgs a) {
     lv.issue(st + VO, LIN_C, LIN_C);
   };
   load(st0);
-  tb.init(a.decay[at.h], at);
+  const float lam = a.decay[at.h];
+  tb.init(lam, at);
+  LinDecay chunk_decay;
+  chunk_decay.init(lam);
   LinState<DA> S;
   S.clear();
   const int ka_at = lin_col_at<PA>(j & 3, 0), va_at = lin_col_at<PV>(2 * wave + ((j & 3) >> 1), 8 * (j & 1));
@@ -504,7 +531,7 @@ void k_linear_states(LinArgs a) {
     bf16x8 vf[2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) vf[z] = lin_col<PV>(cur + VO + 32 * z * PV, va_at);
-    S.decay(tb.pw[LIN_C]);
+    S.decay(chunk_decay.next());
     S.add(cur, ka_at, vf, tb.wt[0], g, three);
     ++c;
   };
@@ -517,7 +544,7 @@ void k_linear_states(LinArgs a) {
 }
 
 // From the segments' own sums to the states before each: a thread takes four elements of a state
-// along the segments.
+// along the segments.  The decay over a segment is two fp32 numbers, so that it does not drift over many.
 __global__ __launch_bounds__(256) void k_linear_scan(LinArgs a, int DA) {
   const int64_t elems = (int64_t)DA * a.DB;
   const int blocks = (int)(elems / 1024);
@@ -534,8 +561,10 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinArgs a, int DA) {
   f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
   if (r.init && entry >= 0)
     s = *as_global(reinterpret_cast<const f32x4*>(r.init + (entry * a.heads + h) * elems + at));
-  const float lam = a.decay[h], f = lin_power(lam, a.L);
-  float f0 = r.rev ? lin_power(lam, a.L - 1) : f;
+  const float lam = a.decay[h];
+  const double p = lin_power64(lam, a.L), p0 = r.rev ? lin_power64(lam, a.L - 1) : p;
+  const float f = (float)p, low = (float)(p - (double)f);
+  float f0 = (float)p0, low0 = (float)(p0 - (double)f0);
   for (int i = 0; i < cnt; i += 8) {
     f32x4 x[8];
 #pragma unroll
@@ -545,8 +574,9 @@ __global__ __launch_bounds__(256) void k_linear_scan(LinArgs a, int DA) {
     for (int j = 0; j < 8; ++j)
       if (i + j < cnt) {
         *as_global(reinterpret_cast<f32x4*>(w + (i + j) * elems)) = s;
-        s = s * f0 + x[j];
+        s = s * f0 + (s * low0 + x[j]);
         f0 = f;
+        low0 = low;
       }
   }
 }
