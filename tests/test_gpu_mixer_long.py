@@ -1,10 +1,11 @@
-"""Linear attention (include/ttt_mixer.h) over long memories."""
+"""Linear attention (include/ttt_mixer.h) over long memories, and over rows that the last-level cache cannot keep."""
 import numpy as np
 import pytest
 import torch
 
+import mixer_bars as bars
 import weight_sequence_layers_amd as W
-from test_gpu_mixer import BF, DEV, gen, np64, say
+from test_gpu_mixer import BF, DEV, Linear, gen, np64, say, worst
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -48,3 +49,25 @@ def test_linear_attention_of_a_long_memory(power, T, lens, K, V):
     say(f"mean error of its gradient {e:.2e}")
     assert abs(e) <= bar
     assert torch.equal(so[:B - 1], s[:B - 1])
+
+
+def test_linear_attention_past_the_last_level_cache():
+    """11100 tokens of 64 heads of 64 (273 MB of rows), two ragged sequences of many chunks: forward, and backward in
+    time, against the oracle at three of the heads."""
+    c = Linear(lens=[9001, 2099], heads=64, K=64, V=64, pad=0, decay=[0.9, 0.99, 1.0, 0.999])
+    assert 2 * c.rows * c.ld > 1 << 28
+    sin, ds = c.states(), c.states(3)
+    sout, dsin = torch.full_like(sin, 7.0), torch.full_like(ds, 7.0)
+    dout = torch.randn(c.rows, 64 * 64, generator=gen(5), device=DEV).to(BF)
+    out, grads = c.call(sin, sout), c.back(dout, sin, ds, dsin)
+    torch.cuda.synchronize()
+    assert c.kept(out, 64) and all(c.kept(g, 64) for g in grads)
+    for i in range(2):
+        for h in (0, 31, 63):
+            ops = (*c.qkv(i, h), c.lam(h), np64(sin[i, h]), c.scale)
+            (o, bar), state = bars.forward(*ops)
+            assert worst(c.part(out, i, h, 64), o, bar) <= 1 and worst(np64(sout[i, h]), *state) <= 1, (i, h)
+            ref = bars.backward(*ops, c.part(dout, i, h, 64), np64(ds[i, h]))
+            for x, (y, bar) in zip(grads, ref):
+                assert worst(c.part(x, i, h, 64), y, bar) <= 1, (i, h)
+            assert worst(np64(dsin[i, h]), *ref[3]) <= 1, (i, h)
