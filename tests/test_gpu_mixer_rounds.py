@@ -8,13 +8,14 @@ from test_gpu_mixer import BF, DEV, Norm, gen, say
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 
-# 768 workgroups of 256 / lanes rows up to rows of 2048 elements, 384 and 256 of one row beyond; the last round not
+# 768 workgroups of 256 / lanes rows up to rows of 2048 elements, 512 and 256 of one row beyond; the last round not
 # full, with 1 to 3 sums over each row
 ROUNDS = [
     dict(T=768 * 32 * 2 + 9, D=64, groups=4, kind="silu"), dict(T=768 * 4 + 1, D=512, act="f32", norm_y=False),
     dict(T=768 * 2 * 2 + 1, D=1024, kind="silu"), dict(T=768 * 2 + 1, D=1024, act="f32", groups=8, kind="sigmoid"),
     dict(T=2 * 768 + 5, D=2048, act="f32", kind="sigmoid"), dict(T=3 * 768 + 2, D=2048, n=False),
     dict(T=3 * 384 + 7, D=4096, kind="silu"), dict(T=384 + 1, D=2056, act="f32"),
+    dict(T=2 * 512 + 3, D=2056, act="f32", groups=257), dict(T=512 + 1, D=4096, kind="sigmoid"),
     dict(T=3 * 256 + 1, D=8192), dict(T=2 * 256 + 3, D=4104, act="f32", kind="silu"),
 ]
 
@@ -30,7 +31,7 @@ def integers(T, D, seed, low=-8, high=9):
 
 
 @pytest.mark.parametrize("T,D", [(768 * 256 * 3 + 77, 8), (768 * 32 * 3 + 5, 64), (768 * 2 * 5 + 1, 1024),
-                                 (768 * 3 + 2, 2048), (384 * 70 + 3, 2056), (256 * 65 + 1, 4104)])
+                                 (768 * 3 + 2, 2048), (384 * 70 + 3, 2056), (512 * 66 + 3, 2056), (256 * 65 + 1, 4104)])
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_residual_norm_backward_adds_up_every_row(T, D, act):
     """Sums of small whole numbers: exact in 32 bits in any order, so that no row may be lost or taken twice.

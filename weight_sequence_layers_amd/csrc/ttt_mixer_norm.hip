@@ -14,10 +14,11 @@
 // between the forward and the backward, which reads h and y again instead of saved statistics.
 //
 // Measured: 64320 rows of 768 in fp32 (two read, two written, 791 MB) 150 us, 5.3 TB/s; backward with a
-// gate of 32768 rows of 1024 in bf16 (537 MB) 116 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
+// gate of 32768 rows of 1024 in bf16 (537 MB) 117 us, of 24197 rows of 768 in fp32 (594 MB) 124, 4.6 and 4.8
 // TB/s, 5 us of each the weights' second launch; a copy of 4 GB reaches 5.0.  Without a gate bf16 rows
-// run at 6.2 to 6.7; backwards of rows past 2048 elements at 2.7 to 3.9, their barriers (one workgroup of
-// 8 or 16 waves to a row, one to a CU) no longer hidden.
+// run at 6.2 to 6.7; backwards of rows of 4096 and 8192 at 3.3 to 4.5 (of 2056, half of whose lanes idle, at 2.2 to
+// 3.8): one workgroup of 8 or 16 waves to a row and mostly one to a CU, whose barriers nothing hides, and with 16
+// waves and a gate 2 to 24 of a lane's registers in memory.
 #include "ttt_device.hpp"
 #include "ttt_mixer_internal.h"
 
@@ -40,6 +41,8 @@ struct Raw8<u16> {
     const uint32_t b = f2bf(x);
     w = u32x4{b, b, b, b} * 0x10001u;
   }
+  // what was computed from the elements is computed again from here on, not kept
+  __device__ __forceinline__ void again() { asm("" : "+v"(w)); }
   __device__ __forceinline__ float operator[](int i) const {
     return __builtin_bit_cast(float, i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
   }
@@ -52,6 +55,7 @@ struct Raw8<float> {
     w[1] = *as_global(reinterpret_cast<const f32x4*>(p + 4));
   }
   __device__ __forceinline__ void fill(float x) { w[0] = w[1] = f32x4{x, x, x, x}; }
+  __device__ __forceinline__ void again() { asm("" : "+v"(w[0]), "+v"(w[1])); }
   __device__ __forceinline__ float operator[](int i) const { return w[i >> 2][i & 3]; }
 };
 __device__ __forceinline__ void store8(u16* p, const float* x) {
@@ -76,7 +80,7 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
 constexpr float GATE_FAR = 110.f;
 __device__ __forceinline__ float sigmoid_tail(float g) {
   constexpr float L = -0.72134752044448170f, LL = -9.6298149556e-9f;   // -log2(e) / 2, and what its rounding leaves
-  const float a = fabsf(g) > GATE_FAR ? GATE_FAR : fabsf(g);
+  const float a = __builtin_elementwise_minimum(fabsf(g), GATE_FAR);
   const float t = a * L, low = fmaf(a, L, -t) + a * LL;
   float x = __builtin_amdgcn_exp2f(t);
   x = fmaf(x, low * 0.693147181f, x);
@@ -245,6 +249,9 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm(NormArgs a) {
 template <typename T, int W, int GATE>
 __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
   constexpr int NT = norm_threads<W>;
+  // 128 registers a lane, for which values computed again are cheaper than what would not fit (rows of 8192: bf16 silu
+  // 195 -> 162 us, fp32 171 -> 137)
+  constexpr bool FEW = W == 16;
   __shared__ float scratch[4][16];
   __shared__ __attribute__((aligned(16))) float red[W > 2 ? 1 : NT * 8];
   const int lanes = W == 1 ? norm_lanes(a.D) : 64 * W, rows = NT / lanes;
@@ -269,6 +276,11 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
   for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.tokens; t0 += (int64_t)gridDim.x * rows) {
     const int64_t t = t0 + (int)threadIdx.x / lanes;
     const bool on = has && t < a.tokens;
+    if (FEW && GATE && sizeof(T) == 2) {
+      wy.again();
+      rs.again();
+      wn.again();
+    }
     Raw8<T> y, h, g, dho, dn;
     y.fill(0.f);
     h.fill(0.f);
@@ -318,6 +330,12 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
     }
     if (a.dh && on) store8(static_cast<T*>(a.dh) + t * a.lddh + col, d);
     float dg[8], dot = 0.f;
+    if (GATE) g.again();
+    if (FEW) y.again();
+    if (FEW && GATE && sizeof(T) == 2) {
+      wy.again();
+      rs.again();
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (GATE) asm("" : "+v"(q[e]));   // the gate's values again from the tail: kept, they took 16 more registers
@@ -447,7 +465,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
 
 int32_t residual_norm_wgs(int32_t D, int64_t tokens) {
   const int64_t rows = norm_rows(D), n = (tokens + rows - 1) / rows;
-  const int w = norm_waves(D), most = w > 8 ? 256 : w > 4 ? 384 : 768;   // as many as run at once
+  // whole rounds of the CUs, which hold one workgroup of 16 waves, one or two of 8 and three or four of 4 (gated bf16
+  // rows of 4096: 180 us with 384, whose second round fills half of the CUs, 147 with 512, 143 with 256; without a
+  // gate 97, 92 and 111)
+  const int w = norm_waves(D), most = w > 8 ? 256 : w > 4 ? 512 : 768;
   return (int32_t)(n < most ? n : most);
 }
 
