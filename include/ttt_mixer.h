@@ -173,7 +173,8 @@ ttt_status ttt_residual_norm(const ttt_residual_norm_config* cfg, const void* h,
  * theirs, each NULL where not wanted, and those of the learned scales that are given (fp32 [dim],
  * overwritten, each NULL where not wanted: the sum over all rows, in an order that depends only
  * on the sizes).  A row gradient may be dh_out or dn (the same stride); other overlaps of what is
- * written (work among it) with an input or each other are TTT_E_CONFIG.
+ * written (work among it) with an input or each other are TTT_E_CONFIG.  A row whose squares pass fp32's range
+ * has a norm of zeros and no gradient through it.
  * work: workspace of the size that ttt_residual_norm_backward_work gives (needed where a scale's
  * gradient is wanted).  tokens 0 writes zero scale gradients.
  */

@@ -119,3 +119,21 @@ def test_gradients_of_rows_with_masked_gates(kind, act, monkeypatch):
     c, kw = masked(kind, act, 40)
     monkeypatch.setattr(c, "kw", lambda: kw)
     c.check_back(*c.back())
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_gradients_of_rows_whose_squares_pass_the_range(act):
+    """The norm of a row whose squares add up past fp32 is zeros, and its gradient has no part in the row's others or in
+    the sums: all as with a gradient of zeros there, bit by bit."""
+    c = Norm(T=30, D=256, act=act, groups=2, kind="silu")
+    c.h[7, :256] = 1e38
+    c.h[11, :256] = -3e37
+    c.h[19, :100] = 2e19
+    c.dn[[7, 11, 19]] *= 1000
+    got = c.back()
+    c.dn[[7, 11, 19]] = 0
+    want = c.back()
+    torch.cuda.synchronize()
+    for a, b in zip((*got[:3], *got[3]), (*want[:3], *want[3])):
+        assert bool(b.isfinite().all()) and torch.equal(a, b)
+    assert bool((c.call()[1][[7, 11, 19], :256] == 0).all())

@@ -317,7 +317,7 @@ __global__ __launch_bounds__(norm_threads<W>) void k_norm_bwd(NormArgs a) {
       }
       sum(hh, ax);
       const float p = 1.f / sqrtf(hh / (float)a.D + a.eps);
-      const float m = ax * p / (float)a.D;
+      const float m = p > 0.f ? ax * p / (float)a.D : 0.f;   // p is 0 past the squares' range, where ax may be infinite
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float x = d[e] * p;
