@@ -60,9 +60,11 @@ ttt_status check_rows(const int32_t* starts, int64_t tokens, int32_t batch, int6
 // sequence is cut only where its workgroups would leave CUs idle.
 //   - as many workgroups as run at once (`slots`): with 8 heads of 131072 tokens 64 segments take 472 us, 32
 //     take 507, 96 take 500; the three gradients of 32768 tokens take 424 us in a training step at 32
-//     segments (768 workgroups for 512 places), 437 at 21, 450 at 42;
-//   - half as many again for sequences of unequal lengths, whose segments go by the longest: 24 prompts
-//     up to 4096 tokens of 12 heads of 64 take 187 us in 2 segments, 151 in 3, 141 in 4, 150 in 6;
+//     segments (768 workgroups for 512 places), 437 at 21, 450 at 42.  The gradients take as many at other
+//     dimensions than the 128 by 128 that this was measured at;
+//   - half as many again for prompts with starts, whose segments go by the longest: 24 of up to 4096 tokens of 12
+//     heads of 64 take 187 us in 2 segments, 151 in 3, 141 in 4, 150 in 6 (the one batch measured; gradients
+//     make no difference between batches with starts and without);
 //   - down to one chunk each (3 x 777 tokens of 2 heads, a training step: 104 us whole, 58 in segments of
 //     129, 51 in segments of 65), but none for sequences of LIN_WHOLE tokens or fewer, for which the
 //     launches cost more (a prompt of 8 heads: 192 tokens 17 us whole, 21 cut; 256 21 and 21; 384 28 and 22).

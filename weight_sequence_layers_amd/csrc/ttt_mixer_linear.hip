@@ -229,8 +229,9 @@ struct LinTables {
 };
 
 // The state of a wave, 16 columns: element e of tile 2 y + t is row 32 y + 8 g + 4 t + e, column j.  fp32 in
-// accumulators over a whole segment, as an operand two bf16 parts, so that out's error stays its own
-// rounding.
+// accumulators over a whole segment.  As an operand it is two bf16 parts, 16 bits of what out, which has 8, is made
+// of: 0.3 % of out's roundings go the other way than with fp32 products (1e-4 of its norm), its error against 64 bits
+// is the same 1.66e-3.  Three parts would be half as many products again.
 template <int DA>
 struct LinState {
   static constexpr int P = DA * 2, N = DA / 16;
@@ -306,10 +307,12 @@ struct LinState {
 // leave them, decayed and split, in LDS for all: the barrier that they need is there for v.
 //
 // A wave's matrix and vector instructions do not run side by side, those of two waves do (4 products
-// and 24 multiplications: 120 ns of one wave, 70 a wave of two): many narrow waves, four to a SIMD, at
-// the price of reading q and k from LDS for each.  Columns of 32 a wave, two to a SIMD, were as fast on
-// long sequences (131072 tokens of 8 heads of 128: 403 us, 417 so) and slower on the others (24 ragged
-// prompts 198 -> 182, a training step of 3 x 777 tokens 79 -> 75).  What bounds the long ones: loads and
+// and 24 multiplications: 120 ns of one wave, 70 a wave of two): many narrow waves, at the price of
+// reading q and k from LDS for each.  A SIMD holds four of them at key dimensions of 64 and 128 with eight
+// waves to a workgroup, three at 64 x 64, two at 128 x 64 and at 256, one at 256 x 64: what LDS and
+// registers leave.  Columns of 32 a wave, half as many to a SIMD, were as fast on long sequences (131072
+// tokens of 8 heads of 128: 403 us, 417 so) and slower on the others (24 ragged prompts 198 -> 182, a training
+// step of 3 x 777 tokens 79 -> 75).  What bounds the long ones: loads and
 // stores alone take 223 us of this kernel there, its work without loads 238, both 310; the matrix cores
 // are busy 31 % of the cycles, the vector units 42, the LDS 44, at 1.6 to 1.9 GHz: four waves of a SIMD
 // that each wait for their own chain of products, and power; neither another order of the instructions

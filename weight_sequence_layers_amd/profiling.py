@@ -55,14 +55,14 @@ def source_digest(part: str = "layer") -> str:
     """Hash of the kernel sources: part "layer" covers every file under csrc/ that the TTT
     layer is built from, "block" the files of the block around it (ttt_block*), "attention"
     those of the attention calls (ttt_attention*), "mixer" those of the mixer calls
-    (ttt_mixer*)."""
+    (ttt_mixer*) and the host headers that they share with the others."""
     h = hashlib.sha256()
     csrc = os.path.join(PKG, "csrc")
     for f in sorted(os.listdir(csrc)):
         own = ("block" if f.startswith("ttt_block") else
                "attention" if f.startswith("ttt_attention") else
                "mixer" if f.startswith("ttt_mixer") else "layer")
-        if own != part:
+        if own != part and not (part == "mixer" and f in ("ttt_attention_host.h", "ttt_block_host.h")):
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
