@@ -70,8 +70,8 @@ ttt_status ttt_validate_linear_attention_config(const ttt_linear_attention_confi
  * q k, sums, states and powers are fp32 or more.  What out is made of (states, a token's weights and
  * decayed values) enters its products as two bf16 numbers each (16 significant bits), so that out is
  * rounded once; for a state that is given back the decayed values enter as three (24 bits, as
- * fp32), so that out's last bit may differ with whether one is wanted.  A state's decay over many tokens is
- * exact to a rounding of fp32, its product with the state is rounded once in 64 tokens.  Every sum has one
+ * fp32), so that out's last bit may differ with whether one is wanted.  A state's decay over many tokens stays
+ * within one step of fp32, its product with the state is rounded once in 64 tokens.  Every sum has one
  * order: the results are the same from run to run.
  * Limits: batch in [0, 65535], batch * heads at most 2^20, 0 <= seq_len <= 2^30, 0 <= tokens < 2^31, every ld at
  * least heads * dim, below 2^24 and a multiple of 8.  tokens, seq_len and batch may be 0.
