@@ -60,11 +60,13 @@ ttt_status check_rows(const int32_t* starts, int64_t tokens, int32_t batch, int6
 // sequence is cut only where its workgroups would leave CUs idle.
 //   - as many workgroups as run at once (`slots`): with 8 heads of 131072 tokens 64 segments take 472 us, 32
 //     take 507, 96 take 500; the three gradients of 32768 tokens take 424 us in a training step at 32
-//     segments (768 workgroups for 512 places), 437 at 21, 450 at 42.  The gradients take as many at other
-//     dimensions than the 128 by 128 that this was measured at;
+//     segments (768 workgroups for 512 places), 437 at 21, 450 at 42.  The gradients of 16384 tokens at half as
+//     many segments, as many and twice as many take 164, 126, 136 us (heads of 64 by 64), 148, 143, 164 (128 by
+//     128), 162, 124, 125 (128 by 64), 167, 166, 216 (256 by 128), but 125, 136, 155 (64 by 256), 157, 178, 224
+//     (128 by 256) and 248, 306, 404 (256 by 256), where fewer would do: the rule does not ask for the dimensions;
 //   - half as many again for prompts with starts, whose segments go by the longest: 24 of up to 4096 tokens of 12
-//     heads of 64 take 187 us in 2 segments, 151 in 3, 141 in 4, 150 in 6 (the one batch measured; gradients
-//     make no difference between batches with starts and without);
+//     heads of 64 take 187 us in 2 segments, 151 in 3, 141 in 4, 150 in 6.  Gradients make no difference between
+//     batches with starts and without (12 of up to 3815 tokens, 8 heads of 128: 273 us, 242 at twice the segments);
 //   - down to one chunk each (3 x 777 tokens of 2 heads, a training step: 104 us whole, 58 in segments of
 //     129, 51 in segments of 65), but none for sequences of LIN_WHOLE tokens or fewer, for which the
 //     launches cost more (a prompt of 8 heads: 192 tokens 17 us whole, 21 cut; 256 21 and 21; 384 28 and 22).
